@@ -5,24 +5,8 @@
 #include <mutex>
 #include <new>
 
-#include "internal.h"
-#include "../../include/moe_layout.h"
+#include "handle.h"
 #include "../../include/moe_bench.h"
-
-struct moe_handle_s {
-  static constexpr uint32_t kMagic = 0x4D4F454Cu;  // "MOEL"
-  uint32_t magic = kMagic;
-  bool has_layout = false;
-  int64_t T = 0;
-  int K = 0, E = 0, P = 0;
-  int pad = 1;     // expert segments padded to a multiple of this (fixed at creation)
-  int64_t R = 0;   // receive rows of the current layout: T*K + E*(pad-1)
-  char* ws = nullptr;
-  moe::WsLayout plan{};
-  moe::Tuning tune{};
-  hipEvent_t ev_start = nullptr;  // moe_time_next_kernel: for the next kernel launch only
-  hipEvent_t ev_stop = nullptr;
-};
 
 namespace moe {
 
@@ -81,7 +65,11 @@ WsLayout plan_workspace(int64_t T, int K, int E, int P, int layout_pairs, int pa
 
 namespace {
 
-bool valid_handle(const moe_handle_s* h) { return h && h->magic == moe_handle_s::kMagic; }
+using moe::aligned;
+using moe::elem_bytes;
+using moe::hip_status;
+using moe::valid_handle;
+using moe::ws_ptr;
 
 // The tuning of a kernel launch: the handle's, plus the events armed by
 // moe_time_next_kernel, which this launch takes (so no later one records them).
@@ -92,10 +80,6 @@ moe::Tuning take_tuning(moe_handle_s* h) {
   h->ev_start = h->ev_stop = nullptr;
   return t;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : dtype == MOE_BF16 ? 2 : 0; }
 
 int check_shape(int64_t T, int K, int E, int P) {
   if (T < 0) return MOE_ERR_INVALID_ARG;
@@ -133,14 +117,6 @@ int check_rows(const moe_handle_s* h, int dtype, int64_t H, int* NV) {
 // The router-weight-gradient kernels keep one float per (segment, k) in LDS.
 int check_dot(const moe_handle_s* h, int NV) {
   return moe::dot_lds_bytes(NV, h->K) <= moe::kMaxDotLds ? MOE_OK : MOE_ERR_UNSUPPORTED;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-
-template <typename T>
-T* ws_ptr(const moe_handle_s* h, size_t off) {
-  return reinterpret_cast<T*>(h->ws + off);
 }
 
 // Padded layouts: zero rows (and zero scores) in the padding of every expert
