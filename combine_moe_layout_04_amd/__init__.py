@@ -23,6 +23,8 @@ from .api import (  # noqa: F401
     moe_expand,
     moe_reduce_partitions,
     moe_combine_partitions,
+    moe_route,
+    moe_route_bwd,
 )
 from . import autograd  # noqa: F401
 

@@ -20,6 +20,11 @@ class MoeTuning(ctypes.Structure):
                 ("layout_pairs", c_int), ("gather_mode", c_int)]
 
 
+class MoeRouteOptions(ctypes.Structure):
+    _fields_ = [("score", c_int), ("renormalize", c_int), ("num_groups", c_int), ("topk_groups", c_int),
+                ("scale", ctypes.c_float)]
+
+
 # name -> (restype, argtypes); the functions declared in include/moe_layout.h and
 # include/moe_bench.h (the measurement entry points)
 SIGNATURES = {
@@ -48,6 +53,10 @@ SIGNATURES = {
                                       c_int64, c_void_p]),
     "moe_combine_partitions": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p,
                                        c_void_p]),
+    "moe_route": (c_int, [c_void_p, c_int, c_int64, c_int, c_int, ctypes.POINTER(MoeRouteOptions),
+                          c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_route_bwd": (c_int, [c_void_p, c_int, c_int64, c_int, c_int, ctypes.POINTER(MoeRouteOptions),
+                              c_void_p, c_void_p, c_void_p, c_void_p]),
     "moe_handle_field": (c_int, [c_void_p, c_int, ctypes.POINTER(c_void_p), ctypes.POINTER(c_size_t)]),
     "moe_handle_dims": (c_int, [c_void_p, ctypes.POINTER(c_int64), ctypes.POINTER(c_int),
                                 ctypes.POINTER(c_int), ctypes.POINTER(c_int)]),

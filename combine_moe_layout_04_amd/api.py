@@ -12,10 +12,11 @@ from typing import Optional
 
 import torch
 
-from ._lib import MoeTuning, lib
+from ._lib import MoeRouteOptions, MoeTuning, lib
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_I32, MOE_I64 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 STATUS_BAD_EXPERT, STATUS_BAD_POSITION = 1, 2
 
 FIELDS = {  # name -> (id, dtype, shape as a function of (T,K,E,P,R))
@@ -422,6 +423,95 @@ def moe_combine_partitions(handle: Handle, partial: torch.Tensor,
     _check(lib().moe_combine_partitions(h.ptr, _ptr(partial), _dtype_code(partial), H, partial.shape[0],
                                         _ptr(out), _stream(h.device)), "moe_combine_partitions")
     return out
+
+
+# ---- router ---------------------------------------------------------------------
+
+def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call that has no handle, taken from its first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, it is on {t.device}")
+    return t.device
+
+
+def _run(dev, where: str, *args) -> None:
+    """The library call `where` on torch's current stream of `dev`, with `dev`
+    current while it launches."""
+    f = getattr(lib(), where)
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(dev)), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(dev)), where)
+
+
+_ROUTE_OPTIONS = {}  # options -> the struct the library reads (a handful in any program)
+
+
+def _route_options(score, renormalize, num_groups, topk_groups, scale):
+    key = (score, renormalize, num_groups, topk_groups, scale)
+    o = _ROUTE_OPTIONS.get(key)
+    if o is None:
+        if score not in SCORES:
+            raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+        if len(_ROUTE_OPTIONS) >= 256:
+            _ROUTE_OPTIONS.clear()
+        o = _ROUTE_OPTIONS[key] = ctypes.byref(MoeRouteOptions(
+            SCORES[score], int(bool(renormalize)), int(num_groups), int(topk_groups), float(scale)))
+    return o
+
+
+def _logits(logits: torch.Tensor):
+    dev = _on_gpu(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    _need(logits, "logits", dev)
+    return dev, logits.shape[0], logits.shape[1], _dtype_code(logits)
+
+
+def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+              renormalize: bool = True, num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0,
+              topk_idx: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None):
+    """Chooses each token's k experts from its logits [T, E] (see moe_layout.h).
+
+    score: "softmax" or "sigmoid"; bias [E] float32 moves the choice, not the weights; with
+    topk_groups < num_groups only the best groups of neighbouring experts take part.
+    Returns (topk_idx int32 [T, k], topk_weights float32 [T, k])."""
+    dev, T, E, dt = _logits(logits)
+    if bias is not None:
+        _need(bias, "bias", dev, (E,), torch.float32)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    else:
+        _need(topk_idx, "topk_idx", dev, (T, k), torch.int32)
+    if topk_weights is None:
+        topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        _need(topk_weights, "topk_weights", dev, (T, k), torch.float32)
+    _run(dev, "moe_route", logits.data_ptr(), dt, T, E, k,
+         _route_options(score, renormalize, num_groups, topk_groups, scale), _ptr(bias),
+         topk_idx.data_ptr(), topk_weights.data_ptr())
+    return topk_idx, topk_weights
+
+
+def moe_route_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor,
+                  score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                  grad_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The logits' gradient [T, E] from the weights' [T, k], for the choice topk_idx (int32)."""
+    dev, T, E, dt = _logits(logits)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k]")
+    K = topk_idx.shape[1]
+    _need(topk_idx, "topk_idx", dev, (T, K), torch.int32)
+    _need(grad_weights, "grad_weights", dev, (T, K), torch.float32)
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _need(grad_logits, "grad_logits", dev, (T, E), logits.dtype)
+    _run(dev, "moe_route_bwd", logits.data_ptr(), dt, T, E, K,
+         _route_options(score, renormalize, 1, 1, scale), topk_idx.data_ptr(), grad_weights.data_ptr(),
+         grad_logits.data_ptr())
+    return grad_logits
 
 
 class CuBudgetStream:

@@ -80,6 +80,29 @@ class _Combine(torch.autograd.Function):
         return grad_y, grad_w, None
 
 
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, bias, score, renormalize, num_groups, topk_groups, scale):
+        idx, w = api.moe_route(logits, k, bias, score, renormalize, num_groups, topk_groups, scale)
+        ctx.save_for_backward(logits, idx)
+        ctx.options = (score, renormalize, scale)
+        ctx.mark_non_differentiable(idx)
+        return idx, w
+
+    @staticmethod
+    def backward(ctx, _grad_idx, grad_w):
+        logits, idx = ctx.saved_tensors
+        grad = api.moe_route_bwd(logits, idx, grad_w.contiguous(), *ctx.options)
+        return (grad,) + (None,) * 7
+
+
+def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+          renormalize: bool = True, num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0):
+    """Differentiable router; returns (topk_idx, topk_weights).  The choice has
+    no gradient, and the bias, which only moves the choice, none either."""
+    return _Route.apply(logits, k, bias, score, renormalize, num_groups, topk_groups, scale)
+
+
 def dispatch(x: torch.Tensor, topk_weights: Optional[torch.Tensor], handle: api.Handle,
              scale_rows: bool = False):
     """Differentiable dispatch; returns (recv, recv_scores or None)."""

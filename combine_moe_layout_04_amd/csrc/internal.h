@@ -151,6 +151,32 @@ struct StagedArgs {
   PadArgs pad;            // expand: padding rows of dst, filled by the grid's first pad.nwaves waves
 };
 
+// The router: scores, choice and weights of one token per wavefront, and the
+// gradient back to the logits.
+struct RouteArgs {
+  const void* z;          // [T, E] logits
+  const float* bias;      // [E] or null: added to the scores for the choice only
+  int* idx;               // [T, K]
+  float* w;               // [T, K]
+  int T, E, K, dtype;
+  int score;              // MOE_SCORE_*
+  bool renorm;
+  float scale;
+  int groups, topk_groups;
+  int per, L;             // experts per group, lanes per group (set by the launcher)
+};
+
+struct RouteBwdArgs {
+  const void* z;          // [T, E] logits
+  const int* idx;         // [T, K]
+  const float* grad_w;    // [T, K]
+  void* grad_z;           // [T, E]
+  int T, E, K, dtype;
+  int score;
+  bool renorm;
+  float scale;
+};
+
 struct Tuning {
   int chunks_per_lane;  // 1, 2, 4: consecutive 64-chunk segments per wave
   int nontemporal;      // 0, 1, 2
@@ -192,6 +218,8 @@ hipError_t launch_send(const StagedArgs& a, const Tuning& t, hipStream_t s);
 hipError_t launch_expand(const StagedArgs& a, const Tuning& t, hipStream_t s);
 hipError_t launch_reduce_partitions(const StagedArgs& a, const Tuning& t, hipStream_t s);
 hipError_t launch_combine_partitions(const StagedArgs& a, const Tuning& t, hipStream_t s);
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s);
 hipError_t launch_copy(void* dst, const void* src, size_t bytes, hipStream_t s);
 
 }  // namespace moe

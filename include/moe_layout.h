@@ -334,6 +334,62 @@ int moe_reduce_partitions(moe_handle_t h, const void* y, int dtype, int64_t H,
 int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64_t H,
                            int64_t send_rows, void* out, hipStream_t stream);
 
+/* ---- router ------------------------------------------------------------------
+ * From a token's expert logits to the topk_idx and topk_weights that the other
+ * calls take.  No handle: the calls stand before moe_layout.
+ *
+ *   s = softmax(z) over the token's E experts, or sigmoid(z) of each;
+ *   c = s + bias, the value experts are chosen by (without a bias and without
+ *       a group limit the choice goes by the logits themselves);
+ *   with topk_groups < num_groups: experts form num_groups groups of
+ *       E/num_groups neighbours, a group's value is the sum of its two largest
+ *       c (its one c if it has a single expert), and only the topk_groups
+ *       groups of largest value take part;
+ *   the K largest c are chosen, in descending order; equal values (experts or
+ *       groups) go to the lower index;
+ *   w[t,k] = scale * s of the chosen expert, divided by the sum of the token's
+ *       K chosen s if renormalize.
+ * Sums and comparisons that follow arithmetic (bias, groups) are made in 64
+ * bits, all others in 32.  A NaN logit counts as -inf in the choice; it makes
+ * its own sigmoid weight NaN (all of the token's if renormalised) and every
+ * softmax weight of its token, as +inf does in a softmax.  A token whose
+ * logits are all -inf (or whose chosen scores add up to zero) gets weight zero
+ * throughout and the lowest ids that may take part.                         */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+typedef struct moe_route_options {
+  int score;        /* MOE_SCORE_*                                             */
+  int renormalize;  /* 1: the K weights of a token add up to scale; 0: not     */
+  int num_groups;   /* 1..64, divides E; 1 with topk_groups 1: no group limit  */
+  int topk_groups;  /* 1..num_groups; K <= topk_groups * E/num_groups          */
+  float scale;      /* finite factor of every weight                           */
+} moe_route_options;
+
+/* logits [T,E] dtype (any E from 1 to 1024; rows need no alignment beyond the
+ * element's), bias [E] float32 or NULL; topk_idx [T,K] int32 and topk_weights
+ * [T,K] float32 are written.  MOE_ERR_INVALID_ARG for options out of range,
+ * MOE_ERR_SHAPE for K > E, groups that do not divide E or hold fewer than K
+ * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above.  T = 0 is
+ * valid.                                                                     */
+int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
+              const float* bias, int32_t* topk_idx, float* topk_weights, hipStream_t stream);
+
+/* Backward of moe_route: grad_logits[t,:] from the gradient of the weights,
+ * for the choice topk_idx (the choice itself has no gradient, and neither has
+ * the bias).  With G_k = scale * grad_weights[t,k], s the token's scores:
+ *   softmax:               dz_j = s_j (sum_k [idx_k = j] G_k - sum_k s_k G_k)
+ *   softmax, renormalised: dz at idx_k = q_k (G_k - sum_m q_m G_m), q = s / sum of the chosen s
+ *   sigmoid:               dz at idx_k = G_k s_k (1 - s_k)
+ *   sigmoid, renormalised: dz at idx_k = (G_k - sum_m q_m G_m) q_k (1 - s_k)
+ * and zero elsewhere.  float32 throughout, rounded once to dtype.  The same
+ * options as the forward call (groups are checked, and have no other part).
+ * An id that repeats within a token adds up; an id outside [0,E) has no part.
+ *   logits, grad_logits [T,E] dtype; topk_idx [T,K] int32; grad_weights [T,K]
+ *   float32.                                                                 */
+int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
+                  const int32_t* topk_idx, const float* grad_weights, void* grad_logits,
+                  hipStream_t stream);
+
 /* Device pointer and byte size of one handle field (no synchronisation). */
 int moe_handle_field(moe_handle_t h, int field, void** dev_ptr, size_t* bytes);
 
