@@ -25,6 +25,9 @@ from .api import (  # noqa: F401
     moe_combine_partitions,
     moe_route,
     moe_route_bwd,
+    moe_few,
+    moe_few_workspace_size,
+    FEW_MAX_PAIRS,
 )
 from . import autograd  # noqa: F401
 

@@ -16,6 +16,8 @@ from ._lib import MoeRouteOptions, MoeTuning, lib
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_I32, MOE_I64 = 0, 1
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+FEW_MAX_PAIRS = 512
 SCORES = {"softmax": 0, "sigmoid": 1}
 STATUS_BAD_EXPERT, STATUS_BAD_POSITION = 1, 2
 
@@ -512,6 +514,65 @@ def moe_route_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: to
          _route_options(score, renormalize, 1, 1, scale), topk_idx.data_ptr(), grad_weights.data_ptr(),
          grad_logits.data_ptr())
     return grad_logits
+
+
+# ---- expert layer for a few tokens -------------------------------------------------
+
+def moe_few_workspace_size(dtype: torch.dtype, T: int, K: int, I: int) -> int:
+    n = ctypes.c_size_t(0)
+    code = MOE_F32 if dtype == torch.float32 else MOE_BF16 if dtype == torch.bfloat16 else -1
+    _check(lib().moe_few_workspace_size(code, T, K, I, ctypes.byref(n)), "moe_few_workspace_size")
+    return n.value
+
+
+def _itype(topk_idx: torch.Tensor) -> int:
+    if topk_idx.dtype == torch.int32:
+        return MOE_I32
+    if topk_idx.dtype == torch.int64:
+        return MOE_I64
+    raise TypeError("topk_idx must be int32 or int64")
+
+
+def moe_few(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torch.Tensor],
+            w13: torch.Tensor, w2: torch.Tensor, activation: str = "silu",
+            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole expert layer for at most FEW_MAX_PAIRS (token, k) pairs (see moe_layout.h).
+
+    x [T, H]; topk_idx [T, K] (ids outside [0, E) add nothing); topk_weights [T, K] float32 or
+    None (plain sum); w13 [E, 2I, H] (gate rows, then up rows); w2 [E, H, I].  Returns out [T, H]."""
+    dev = _on_gpu(x, "x")
+    dt = _dtype_code(x)
+    if x.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x and topk_idx must have 2 dimensions, w13 and w2 three")
+    T, H = x.shape
+    K = topk_idx.shape[1]
+    E, I = w2.shape[0], w2.shape[2]
+    _need(x, "x", dev)
+    _need(topk_idx, "topk_idx", dev, (T, K))
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", dev, (T, K), torch.float32)
+    _need(w13, "w13", dev, (E, 2 * I, H), x.dtype)
+    _need(w2, "w2", dev, (E, H, I), x.dtype)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", dev, (T, H), x.dtype)
+    if workspace is None:
+        # a call that the library refuses launches nothing: its workspace need not be allocated
+        pairs = T * K if T * K <= FEW_MAX_PAIRS else 0
+        workspace = torch.empty(pairs * I, dtype=x.dtype, device=dev)
+    else:
+        _need(workspace, "workspace", dev)
+    _run(dev, "moe_few", x.data_ptr(), dt, T, H, topk_idx.data_ptr(), _itype(topk_idx), K, _ptr(topk_weights),
+         w13.data_ptr(), w2.data_ptr(), E, I, _activation(activation), out.data_ptr(), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return out
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
 
 
 class CuBudgetStream:

@@ -177,6 +177,25 @@ struct RouteBwdArgs {
   float scale;
 };
 
+// A whole expert layer for a few tokens (at most kFewMaxPairs pairs).
+constexpr int kFewMaxPairs = 512;  // MOE_FEW_MAX_PAIRS
+
+struct FewArgs {
+  const void* x;          // [T, H]
+  const void* idx;        // [T, K] int32 or int64
+  const float* w;         // [T, K] or null (plain sum)
+  const void* w13;        // [E, 2I, H]: gate rows, then up rows
+  const void* w2;         // [E, H, I]
+  void* mid;              // [T*K, I] workspace: the activations
+  void* out;              // [T, H]
+  int T, K, E, H, I;
+  int itype, dtype, act;
+  int pairs;              // T*K
+  int hch, ich;           // 16-byte chunks of a row of H, of I
+  int groups;             // experts, or pairs when those are fewer (set by the launcher)
+  int split, part_ch;     // parts of the sum over I, chunks of a part (set by the launcher)
+};
+
 struct Tuning {
   int chunks_per_lane;  // 1, 2, 4: consecutive 64-chunk segments per wave
   int nontemporal;      // 0, 1, 2
@@ -220,6 +239,7 @@ hipError_t launch_reduce_partitions(const StagedArgs& a, const Tuning& t, hipStr
 hipError_t launch_combine_partitions(const StagedArgs& a, const Tuning& t, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s);
+hipError_t launch_few(const FewArgs& a, hipStream_t s);
 hipError_t launch_copy(void* dst, const void* src, size_t bytes, hipStream_t s);
 
 }  // namespace moe

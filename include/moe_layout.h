@@ -390,6 +390,34 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
                   const int32_t* topk_idx, const float* grad_weights, void* grad_logits,
                   hipStream_t stream);
 
+/* ---- expert layer for a few tokens ---------------------------------------------
+ * The whole layer of a decode step, without a layout, a dispatch or a combine:
+ *   act[t,k] = f(Wg_e x[t]) * (Wu_e x[t]),   e = topk_idx[t,k]
+ *   out[t]   = round(sum_k w[t,k] * (W2_e act[t,k]))
+ * with Wg the first I and Wu the last I rows of w13[e], f(g) = g / (1 +
+ * exp(-g)) (MOE_ACT_SILU) or the tanh form of gelu (MOE_ACT_GELU_TANH).
+ * float32 sums; act is rounded once to dtype; the sum over k runs in k order
+ * from +0.0, products and sums rounded on their own.  Results are bitwise
+ * reproducible.  Only the chosen experts' weights are read.
+ *
+ *   x [T,H], w13 [E,2I,H], w2 [E,H,I], out [T,H] dtype, 16-byte aligned;
+ *   topk_idx [T,K] int32 or int64; topk_weights [T,K] float32, or NULL for a
+ *   plain sum; workspace 256-byte aligned, moe_few_workspace_size bytes (one
+ *   per call in flight: calls that overlap in time must not share it).
+ * An id outside [0,E) is no expert of this call and adds nothing (the ids of
+ * other ranks' experts in an expert-parallel layer); a token without an
+ * expert gets a zero row.  The same id may repeat within a token.
+ * MOE_ERR_UNSUPPORTED above MOE_FEW_MAX_PAIRS pairs (larger batches go through
+ * moe_layout, moe_dispatch and moe_combine), MOE_ERR_SHAPE for rows of H or I
+ * that are not whole 16-byte chunks.  T = 0 is valid.  K may exceed E.       */
+#define MOE_FEW_MAX_PAIRS 512
+enum moe_activation { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 };
+
+int moe_few_workspace_size(int dtype, int64_t T, int K, int64_t I, size_t* bytes);
+int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx, int itype, int K,
+            const float* topk_weights, const void* w13, const void* w2, int E, int64_t I, int activation,
+            void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Device pointer and byte size of one handle field (no synchronisation). */
 int moe_handle_field(moe_handle_t h, int field, void** dev_ptr, size_t* bytes);
 
