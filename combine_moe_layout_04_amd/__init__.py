@@ -26,6 +26,8 @@ from .api import (  # noqa: F401
     moe_route,
     moe_route_bwd,
     moe_few,
+    moe_lowrank,
+    moe_lowrank_bwd,
     moe_few_workspace_size,
     FEW_MAX_PAIRS,
 )

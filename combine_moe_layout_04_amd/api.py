@@ -575,6 +575,99 @@ def _activation(name: str) -> int:
     return ACTIVATIONS[name]
 
 
+# ---- low-rank adapters -------------------------------------------------------------
+
+def _adapters(h: Handle, x, H, a, b, dtype, topk_weights):
+    """Checks the arguments that moe_lowrank and its backward share; (A, r, N)."""
+    dev = h.device
+    if dev is None:
+        raise RuntimeError("the handle has no layout yet")
+    if a is not None and a.dim() != 3 or b is not None and b.dim() != 3:
+        raise ValueError("a must be [A, r, H] and b [A, r, N]")
+    A, r, N = b.shape
+    _need(b, "b", dev, dtype=dtype)
+    if a is not None:
+        _need(a, "a", dev, (A, r, H), dtype)
+    if x is not None:
+        _need(x, "x", dev, (h.T, H), dtype)
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", dev, (h.T, 1), torch.float32)
+    return A, r, N
+
+
+def moe_lowrank(handle: Handle, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                topk_weights: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None):
+    """out[t] = base[t] + w[t] * (x[t] a_e^T) b_e for the token's adapter e (see moe_layout.h).
+
+    The handle's layout has K = 1 and E >= A experts; ids from A up have no adapter.  a [A, r, H],
+    b [A, r, N], base [T, N] or None (0), topk_weights [T, 1] float32 or None (1); out may be base.
+    Returns (out [T, N], u float32 [R, r]); u belongs to the backward pass."""
+    h = handle
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    H = x.shape[1]
+    dt = _dtype_code(x)
+    A, r, N = _adapters(h, x, H, a, b, x.dtype, topk_weights)
+    dev = h.device
+    if base is not None:
+        _need(base, "base", dev, (h.T, N), x.dtype)
+    if out is None:
+        out = torch.empty((h.T, N), dtype=x.dtype, device=dev)
+    else:
+        _need(out, "out", dev, (h.T, N), x.dtype)
+    if u is None:
+        u = torch.empty((h.R, r), dtype=torch.float32, device=dev)
+    else:
+        _need(u, "u", dev, (h.R, r), torch.float32)
+    _run(dev, "moe_lowrank", h.ptr, x.data_ptr(), dt, H, a.data_ptr(), b.data_ptr(), A, r, N, _ptr(topk_weights),
+         _ptr(base), out.data_ptr(), u.data_ptr())
+    return out, u
+
+
+def moe_lowrank_bwd(handle: Handle, grad_out: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                    u: torch.Tensor, topk_weights: Optional[torch.Tensor] = None,
+                    grad_base: Optional[torch.Tensor] = None, grad_x=None, grad_a=None, grad_b=None, grad_w=False,
+                    workspace: Optional[torch.Tensor] = None):
+    """Gradients of moe_lowrank on the forward's layout and u (see moe_layout.h).
+
+    grad_x, grad_a, grad_b, grad_w: None or True (allocate), False (not produced) or a tensor.
+    grad_base [T, H], the gradient through the shared projection, is added to grad_x.
+    Returns (grad_x, grad_a, grad_b, grad_w), None for those not produced."""
+    h = handle
+    if x.dim() != 2 or grad_out.dim() != 2:
+        raise ValueError("x must be [T, H] and grad_out [T, N]")
+    H = x.shape[1]
+    dt = _dtype_code(grad_out)
+    A, r, N = _adapters(h, x, H, a, b, grad_out.dtype, topk_weights)
+    dev, T, dtype = h.device, h.T, grad_out.dtype
+    _need(grad_out, "grad_out", dev, (T, N))
+    _need(u, "u", dev, (h.R, r), torch.float32)
+    if grad_base is not None:
+        _need(grad_base, "grad_base", dev, (T, H), dtype)
+
+    def given(t, name, shape, dtype):
+        if t is False:
+            return None
+        if t is None or t is True:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _need(t, name, dev, shape, dtype)
+        return t
+
+    grad_x = given(grad_x, "grad_x", (T, H), dtype)
+    grad_a = given(grad_a, "grad_a", (A, r, H), dtype)
+    grad_b = given(grad_b, "grad_b", (A, r, N), dtype)
+    grad_w = given(grad_w, "grad_w", (T, 1), torch.float32)
+    if workspace is None:
+        workspace = torch.empty(h.R * r, dtype=torch.float32, device=dev)
+    else:
+        _need(workspace, "workspace", dev)
+    _run(dev, "moe_lowrank_bwd", h.ptr, grad_out.data_ptr(), dt, H, x.data_ptr(), a.data_ptr(), b.data_ptr(), A, r, N,
+         _ptr(topk_weights), u.data_ptr(), _ptr(grad_base), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b), _ptr(grad_w),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return grad_x, grad_a, grad_b, grad_w
+
+
 class CuBudgetStream:
     """A HIP stream restricted to compute units [cu_first, cu_first + cu_count)
     (moe_stream_create_cu_budget), usable as a torch stream (`.stream`)."""

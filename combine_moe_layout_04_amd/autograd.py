@@ -103,6 +103,35 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, sco
     return _Route.apply(logits, k, bias, score, renormalize, num_groups, topk_groups, scale)
 
 
+class _Lowrank(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, a, b, topk_weights, handle, base):
+        out, u = api.moe_lowrank(handle, x, a, b, topk_weights, base)
+        ctx.handle = handle
+        ctx.generation = handle.generation
+        ctx.save_for_backward(x, a, b, topk_weights, u)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        _same_layout(ctx, "lowrank")
+        x, a, b, w, u = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grad_out = grad_out.contiguous()
+        got = (None,) * 4
+        if any(need[:4]):
+            got = api.moe_lowrank_bwd(ctx.handle, grad_out, x, a, b, u, w, grad_x=need[0], grad_a=need[1],
+                                      grad_b=need[2], grad_w=need[3])
+        return got + (None, grad_out if need[5] else None)
+
+
+def lowrank(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_weights: Optional[torch.Tensor],
+            handle: api.Handle, base: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable low-rank adapters on a layout of one adapter per token,
+    beside the shared projection's output `base`."""
+    return _Lowrank.apply(x, a, b, topk_weights, handle, base)
+
+
 def dispatch(x: torch.Tensor, topk_weights: Optional[torch.Tensor], handle: api.Handle,
              scale_rows: bool = False):
     """Differentiable dispatch; returns (recv, recv_scores or None)."""

@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libmoe_layout.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["abi.hip", "layout_kernels.hip", "row_kernels.hip", "staged_kernels.hip", "copy_kernels.hip",
-           "abi_route.hip", "route_kernels.hip", "abi_few.hip", "few_kernels.hip"]
+           "abi_route.hip", "route_kernels.hip", "abi_few.hip", "few_kernels.hip",
+           "abi_lowrank.hip", "lowrank_kernels.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

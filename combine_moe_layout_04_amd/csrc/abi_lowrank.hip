@@ -1,0 +1,122 @@
+// C ABI of the low-rank adapters (moe_lowrank, moe_lowrank_bwd): host-side
+// validation and launches, under the same rules as abi.hip.
+#include "handle.h"
+
+namespace {
+
+int check_lowrank(const moe_handle_s* h, int dtype, int64_t H, int64_t N, int A, int r) {
+  if (!moe::valid_handle(h)) return MOE_ERR_INVALID_ARG;
+  if (!h->has_layout) return MOE_ERR_HANDLE;
+  const int eb = moe::elem_bytes(dtype);
+  if (eb == 0) return MOE_ERR_UNSUPPORTED;
+  if (h->K != 1 || A < 1 || A > h->E || r < 1 || H < 1 || N < 1) return MOE_ERR_SHAPE;
+  if (r > MOE_MAX_RANK || H > (int64_t(1) << 20) || N > (int64_t(1) << 20)) return MOE_ERR_UNSUPPORTED;
+  if ((H * eb) % 16 != 0 || (N * eb) % 16 != 0 || (r * eb) % 16 != 0) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+moe::LowrankArgs lowrank_args(const moe_handle_s* h, int dtype, int A, int r) {
+  moe::LowrankArgs a{};
+  a.expert_offset = moe::ws_ptr<int>(h, h->plan.expert_offset);
+  a.recv_token = moe::ws_ptr<int>(h, h->plan.recv_token);
+  a.T = (int)h->T;
+  a.E = h->E;
+  a.A = A;
+  a.R = (int)h->R;
+  a.r = r;
+  a.dtype = dtype;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
+                int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,
+                float* u, hipStream_t stream) {
+  int st = check_lowrank(h, dtype, H, N, num_adapters, rank);
+  if (st != MOE_OK) return st;
+  if (h->T == 0) return MOE_OK;  // nothing to read or write; empty arrays may be NULL
+  if (!x || !a || !b || !out || !u) return MOE_ERR_INVALID_ARG;
+  if (!moe::aligned(x, 16) || !moe::aligned(a, 16) || !moe::aligned(b, 16) || !moe::aligned(out, 16) ||
+      !moe::aligned(u, 16) || (base && !moe::aligned(base, 16)) || (topk_weights && !moe::aligned(topk_weights, 4)))
+    return MOE_ERR_ALIGNMENT;
+  const int es = moe::elem_bytes(dtype);
+  moe::LowrankArgs k = lowrank_args(h, dtype, num_adapters, rank);
+  k.rows = x;
+  k.bank = a;
+  k.u = u;
+  k.wch = (int)(H * es / 16);
+  st = moe::hip_status(moe::launch_lowrank_shrink(k, stream));
+  if (st != MOE_OK) return st;
+  k.bank = b;
+  k.w = topk_weights;
+  k.base = base;
+  k.out = out;
+  k.wch = (int)(N * es / 16);
+  return moe::hip_status(moe::launch_lowrank_expand(k, stream));
+}
+
+int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, const void* x, const void* a,
+                    const void* b, int num_adapters, int rank, int64_t N, const float* topk_weights,
+                    const float* u, const void* grad_base, void* grad_x, void* grad_a, void* grad_b,
+                    float* grad_w, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int st = check_lowrank(h, dtype, H, N, num_adapters, rank);
+  if (st != MOE_OK) return st;
+  if (!grad_x && !grad_a && !grad_b && !grad_w) return MOE_ERR_INVALID_ARG;
+  const bool through = grad_x || grad_a || grad_w;  // gradients that pass through the rank's space
+  if (h->T > 0) {
+    if (!grad_out || (through && (!b || !workspace))) return MOE_ERR_INVALID_ARG;
+    if ((grad_x && !a) || (grad_a && !x) || ((grad_b || grad_w) && !u)) return MOE_ERR_INVALID_ARG;
+  }
+  if (!moe::aligned(grad_out, 16) || !moe::aligned(x, 16) || !moe::aligned(a, 16) || !moe::aligned(b, 16) ||
+      !moe::aligned(u, 16) || !moe::aligned(grad_base, 16) || !moe::aligned(grad_x, 16) ||
+      !moe::aligned(grad_a, 16) || !moe::aligned(grad_b, 16) || !moe::aligned(topk_weights, 4) ||
+      !moe::aligned(grad_w, 4) || !moe::aligned(workspace, 16))
+    return MOE_ERR_ALIGNMENT;
+  if (through && workspace_bytes < (size_t)h->R * rank * sizeof(float)) return MOE_ERR_WORKSPACE;
+  const int es = moe::elem_bytes(dtype);
+  const int hch = (int)(H * es / 16), nch = (int)(N * es / 16);
+  moe::LowrankArgs k = lowrank_args(h, dtype, num_adapters, rank);
+  float* gu = static_cast<float*>(workspace);
+  if (through && h->T > 0) {
+    k.rows = grad_out;
+    k.bank = b;
+    k.w = topk_weights;
+    k.u = gu;
+    k.saved = u;
+    k.dot = grad_w;
+    k.wch = nch;
+    k.backward = true;
+    if ((st = moe::hip_status(moe::launch_lowrank_shrink(k, stream))) != MOE_OK) return st;
+  }
+  if (grad_x && h->T > 0) {
+    k.bank = a;
+    k.w = nullptr;  // gu holds the weight
+    k.u = gu;
+    k.base = grad_base;
+    k.out = grad_x;
+    k.wch = hch;
+    if ((st = moe::hip_status(moe::launch_lowrank_expand(k, stream))) != MOE_OK) return st;
+  }
+  if (grad_a) {  // also for an empty batch: zeros
+    k.rows = x;
+    k.w = nullptr;
+    k.u = gu;
+    k.out = grad_a;
+    k.wch = hch;
+    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(k, stream))) != MOE_OK) return st;
+  }
+  if (grad_b) {
+    k.rows = grad_out;
+    k.w = topk_weights;
+    k.u = const_cast<float*>(u);
+    k.out = grad_b;
+    k.wch = nch;
+    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(k, stream))) != MOE_OK) return st;
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -196,6 +196,25 @@ struct FewArgs {
   int split, part_ch;     // parts of the sum over I, chunks of a part (set by the launcher)
 };
 
+// Low-rank adapters on a layout of one adapter per token: the three kernels'
+// shared arguments.
+struct LowrankArgs {
+  const int* expert_offset;  // [E+1]
+  const int* recv_token;     // [R], -1 for a row without a token
+  const void* rows;          // [T, W]: shrink and wgrad read them
+  const void* bank;          // [A, r, W]
+  const float* w;            // [T] or null: shrink (backward), expand and wgrad multiply by it
+  float* u;                  // [R, r]: shrink writes it, expand and wgrad read it
+  const float* saved;        // [R, r]: the forward's u (backward shrink with dot)
+  float* dot;                // [T] or null: <raw, saved>
+  const void* base;          // [T, W] or null: added by expand
+  void* out;                 // [T, W] (expand), [A, r, W] (wgrad)
+  int T, E, A, R, r;
+  int wch;                   // 16-byte chunks of a wide row
+  int dtype;
+  bool backward;             // shrink: u = w * raw
+};
+
 struct Tuning {
   int chunks_per_lane;  // 1, 2, 4: consecutive 64-chunk segments per wave
   int nontemporal;      // 0, 1, 2
@@ -240,6 +259,9 @@ hipError_t launch_combine_partitions(const StagedArgs& a, const Tuning& t, hipSt
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s);
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
+hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s);
+hipError_t launch_lowrank_expand(const LowrankArgs& a, hipStream_t s);
+hipError_t launch_lowrank_wgrad(const LowrankArgs& a, hipStream_t s);
 hipError_t launch_copy(void* dst, const void* src, size_t bytes, hipStream_t s);
 
 }  // namespace moe

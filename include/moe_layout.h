@@ -418,6 +418,51 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
             const float* topk_weights, const void* w13, const void* w2, int E, int64_t I, int activation,
             void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- low-rank adapters -----------------------------------------------------------
+ * Adapters of many requests at once, beside a projection that they share: each
+ * token has one adapter, or none, and the layout groups the tokens by adapter
+ * (moe_layout with K = 1, the adapter's number as the expert id and E >= the
+ * number of adapters).  Tokens whose id is num_adapters or above (below E)
+ * have no adapter.  One layout serves every projection of a batch.
+ *   u[p]   = a_e x[t]                   p = recv_pos[t], e the token's adapter
+ *   out[t] = round(base[t] + w[t] * (u[p] b_e))
+ * w = topk_weights, or 1 where NULL; base, the shared projection's output, or
+ * 0 where NULL; for a token without an adapter out = base and u = 0.  Sums and
+ * u in float32 (u takes part in products as two bfloat16 halves, 16 bits of
+ * it), one rounding at the end; results are bitwise reproducible.
+ *
+ *   x [T,H], a [num_adapters,r,H], b [num_adapters,r,N], base and out [T,N]
+ *   dtype, 16-byte aligned (out may be base); topk_weights [T,1] float32; u
+ *   [R,r] float32, written, 16-byte aligned (rows in receive order; moe_lowrank_bwd takes it).
+ * MOE_ERR_SHAPE unless the layout has K = 1 and E >= num_adapters, and rows of
+ * H, N and r are whole 16-byte chunks (a smaller rank is padded with zero
+ * rows); MOE_ERR_UNSUPPORTED for r > MOE_MAX_RANK.                          */
+#define MOE_MAX_RANK 128
+int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
+                int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,
+                float* u, hipStream_t stream);
+
+/* Backward of moe_lowrank, on the forward's layout and u.  With g = grad_out,
+ * raw[p] = b_e g[t] and gu[p] = w[t] * raw[p]:
+ *   grad_x[t] = round(grad_base[t] + gu[p] a_e)     (grad_base: 0 where NULL)
+ *   grad_a[e] = round(sum_p gu[p]^T x[t]),  grad_b[e] = round(sum_p w[t] u[p]^T g[t])
+ *   grad_w[t] = <raw[p], u[p]>
+ * Any of the four outputs may be NULL, not all (grad_w needs no topk_weights:
+ * it is then the gradient at w = 1).  An adapter without tokens gets zero
+ * gradients, a token without an adapter grad_x = grad_base and grad_w = 0.
+ * grad_base, added to grad_x, is the gradient that reaches x through the
+ * shared projection; grad_x may be grad_base.  (The gradient of base is
+ * grad_out itself.)
+ *   grad_out [T,N], x [T,H], a, b as above, grad_x, grad_base [T,H], grad_a
+ *   [num_adapters,r,H], grad_b [num_adapters,r,N] dtype; u as the forward call
+ *   wrote it; grad_w [T,1] float32; workspace 16-byte aligned, R * r * 4
+ *   bytes (not needed for grad_b alone).  With T = 0 grad_a and grad_b are
+ *   set to zero.                                                             */
+int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, const void* x, const void* a,
+                    const void* b, int num_adapters, int rank, int64_t N, const float* topk_weights,
+                    const float* u, const void* grad_base, void* grad_x, void* grad_a, void* grad_b,
+                    float* grad_w, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Device pointer and byte size of one handle field (no synchronisation). */
 int moe_handle_field(moe_handle_t h, int field, void** dev_ptr, size_t* bytes);
 

@@ -1,0 +1,314 @@
+"""Low-rank adapters and their gradients against the formulas in float64.
+
+Bounds, with u = 2^-24 and n terms of a float32 sum in any order off by n u
+times the sum of magnitudes.  A rank-space value s (u, raw, gu) from rows of W
+terms: ds = W u sum|bank||row|, one more product by w.  Where it is an operand
+of a bfloat16 instruction its two halves leave (eps/2)^2 = 2^-16 of it, and
+the sum has twice the terms.  The result is rounded once: eps/2 for bfloat16,
+u for float32 (with the addition of the base).
+"""
+import math
+
+import pytest
+import torch
+
+import combine_moe_layout_04_amd as M
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+F32, BF16 = torch.float32, torch.bfloat16
+U = 2.0 ** -24
+
+
+def make(T, A, r, H, N, dtype, seed, weights=True, none=0.2, E=None):
+    g = torch.Generator().manual_seed(seed)
+    E = E or A + 1
+    ids = torch.randint(0, A, (T, 1), generator=g)
+    ids = torch.where(torch.rand(T, 1, generator=g) < none, torch.randint(A, E, (T, 1), generator=g) if E > A else ids, ids)
+    d = dict(x=torch.randn(T, H, generator=g).to(dtype), a=(torch.randn(A, r, H, generator=g) * H ** -0.5).to(dtype),
+             b=(torch.randn(A, r, N, generator=g) * r ** -0.5).to(dtype), base=torch.randn(T, N, generator=g).to(dtype),
+             g=torch.randn(T, N, generator=g).to(dtype), gbase=torch.randn(T, H, generator=g).to(dtype),
+             w=torch.randn(T, 1, generator=g) if weights else None)
+    d = {k: None if v is None else v.to(DEV) for k, v in d.items()}
+    return ids.to(torch.int32).to(DEV), E, d
+
+
+def reference(ids, d, with_base=True, with_gbase=True):
+    """{name: (value, bound)} in float64 on the CPU."""
+    dtype = d["x"].dtype
+    half = torch.finfo(dtype).eps / 2
+    split = 2.0 ** -16 if dtype == BF16 else 0.0
+    c = {k: None if v is None else v.cpu().double() for k, v in d.items()}
+    T, H = c["x"].shape
+    A, r, N = c["b"].shape
+    w = c["w"] if c["w"] is not None else torch.ones(T, 1, dtype=torch.float64)
+    ids = ids.cpu().view(-1)
+    z = lambda *s: torch.zeros(*s, dtype=torch.float64)  # noqa: E731
+    out = c["base"].clone() if with_base else z(T, N)
+    gx = c["gbase"].clone() if with_gbase else z(T, H)
+    ga, gb, gw = z(A, r, H), z(A, r, N), z(T, 1)
+    to, tx, ta, tb, tw = z(T, N), z(T, H), z(A, r, H), z(A, r, N), z(T, 1)
+    for e in range(A):
+        t = torch.nonzero(ids == e).view(-1)
+        n = len(t)
+        if not n:
+            continue
+        a, b, x, g, wt = c["a"][e], c["b"][e], c["x"][t], c["g"][t], w[t]
+        u, du = x @ a.t(), H * U * (x.abs() @ a.abs().t())
+        raw, draw = g @ b.t(), N * U * (g.abs() @ b.abs().t())
+        wu, gu = wt * u, wt * raw
+        dwu = wt.abs() * du + 2 * U * wu.abs() + split * wu.abs()
+        dgu = wt.abs() * draw + 2 * U * gu.abs() + split * gu.abs()
+        out[t] += wu @ b
+        to[t] = dwu @ b.abs() + (2 * r + 2) * U * (wu.abs() @ b.abs())
+        gx[t] += gu @ a
+        tx[t] = dgu @ a.abs() + (2 * r + 2) * U * (gu.abs() @ a.abs())
+        ga[e] = gu.t() @ x
+        ta[e] = dgu.t() @ x.abs() + (2 * n + 8) * U * (gu.abs().t() @ x.abs())
+        gb[e] = wu.t() @ g
+        tb[e] = dwu.t() @ g.abs() + (2 * n + 8) * U * (wu.abs().t() @ g.abs())
+        gw[t] = (raw * u).sum(1, keepdim=True)
+        tw[t] = ((draw * (u.abs() + du) + raw.abs() * du) + (r + 4) * U * (raw * u).abs()).sum(1, keepdim=True)
+    done = lambda v, tol: (v, tol + half * (v.abs() + tol) + U * v.abs() + 1e-37)  # noqa: E731
+    return dict(out=done(out, to), grad_x=done(gx, tx), grad_a=done(ga, ta), grad_b=done(gb, tb), grad_w=(gw, tw + 1e-37))
+
+
+def near(got, ref, what):
+    v, tol = ref
+    err = (got.cpu().double() - v).abs()
+    assert got.shape == v.shape and bool((err <= tol).all()), (what, float((err - tol).max()))
+
+
+def check(ids, E, d, pad=1):
+    h = M.moe_layout(ids, E, 1, handle=M.Handle(pad_multiple=pad))
+    ref = reference(ids, d)
+    u0 = torch.full((h.R, d["a"].shape[1]), math.nan, device=DEV)
+    out, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"], u=u0)
+    near(out, ref["out"], "out")
+    assert not torch.isnan(u[:int(h.field("expert_offset")[-1])]).any()  # every row is written
+    got = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_base=d["gbase"], grad_w=True)
+    for n, t in zip(("grad_x", "grad_a", "grad_b", "grad_w"), got):
+        near(t, ref[n], n)
+    assert h.check() == 0
+    return h, u, out, got
+
+
+SHAPES = [(1, 1, 8, 64, 64), (1, 40, 16, 2048, 96), (3, 2, 8, 8, 8), (17, 3, 24, 136, 264), (64, 32, 16, 256, 512),
+          (100, 7, 40, 1000, 72), (333, 5, 64, 520, 1032), (1000, 1, 128, 128, 192), (257, 200, 8, 64, 40),
+          (2000, 11, 32, 264, 136), (50, 1000, 16, 32, 24), (130, 4, 72, 96, 4096), (77, 6, 96, 168, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,A,r,H,N", SHAPES)
+def test_every_output_against_the_formulas(dtype, T, A, r, H, N):
+    ids, E, d = make(T, A, r, H, N, dtype, T + A + r)
+    check(ids, E, d)
+
+
+@pytest.mark.parametrize("T,A,r,H,N", [(19, 3, 4, 12, 20), (65, 2, 12, 612, 36), (40, 5, 20, 4, 4), (9, 4, 124, 44, 1028)])
+def test_float32_chunks_of_four(T, A, r, H, N):
+    ids, E, d = make(T, A, r, H, N, F32, T)
+    check(ids, E, d)
+
+
+@pytest.mark.parametrize("pad", [2, 16, 100])
+def test_padded_layouts(pad):
+    ids, E, d = make(150, 6, 16, 72, 136, BF16, pad, E=9)
+    check(ids, E, d, pad)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_all_none_one_adapter_and_sorted(dtype):
+    ids, E, d = make(90, 4, 16, 64, 80, dtype, 1)
+    for fill in (4, 2):
+        ids[:] = fill
+        _, _, out, (gx, ga, gb, gw) = check(ids, E, d)
+        if fill == 4:  # nobody has an adapter
+            assert torch.equal(out, d["base"]) and torch.equal(gx, d["gbase"])
+            assert (ga == 0).all() and (gb == 0).all() and (gw == 0).all()
+    ids[:] = torch.arange(90, device=DEV).view(-1, 1) // 23
+    check(ids, E, d)
+
+
+def test_without_weights_and_base_and_in_place():
+    ids, E, d = make(70, 5, 16, 136, 72, BF16, 2, weights=False)
+    h = M.moe_layout(ids, E, 1)
+    ref = reference(ids, d, with_base=False, with_gbase=False)
+    out, u = M.moe_lowrank(h, d["x"], d["a"], d["b"])
+    near(out, ref["out"], "out")
+    gx, ga, gb, gw = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u)
+    near(gx, ref["grad_x"], "grad_x")
+    assert gw is None
+    only = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, grad_x=False, grad_a=False, grad_w=True)
+    assert only[0] is None and only[1] is None and torch.equal(only[2], gb)
+    near(only[3], ref["grad_w"], "grad_w")
+    # in place: out on base, grad_x on grad_base
+    base, gbase = d["base"].clone(), d["gbase"].clone()
+    full, u2 = M.moe_lowrank(h, d["x"], d["a"], d["b"], base=d["base"])
+    M.moe_lowrank(h, d["x"], d["a"], d["b"], base=base, out=base)
+    assert torch.equal(base, full) and torch.equal(u2, u)
+    want = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, grad_base=d["gbase"])[0]
+    M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, grad_base=gbase, grad_x=gbase)
+    assert torch.equal(gbase, want)
+
+
+def test_nothing_leaks_between_tokens_and_adapters():
+    ids, E, d = make(100, 8, 16, 64, 72, BF16, 4, none=0.0)
+    ids[ids == 3] = 2        # adapter 3 has no token
+    ids[40] = 8              # token 40 has no adapter
+    h = M.moe_layout(ids, E, 1)
+    ref, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+    rgx, rga, rgb, _ = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"])
+    d["a"][3], d["b"][3] = math.nan, math.inf
+    d["x"][40] = math.nan
+    d["x"][41] = math.inf
+    d["g"][40], d["g"][41] = math.nan, math.nan
+    got, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+    gx, ga, gb, _ = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"])
+    keep = [t for t in range(100) if t != 41]
+    assert torch.equal(got[keep], ref[keep]) and torch.equal(gx[keep], rgx[keep])
+    other = [e for e in range(8) if e != int(ids[41])]
+    assert torch.equal(ga[other], rga[other]) and torch.equal(gb[other], rgb[other])
+
+
+def test_gradients_against_differences():
+    """Central differences of the float64 formula along random directions.  It is
+    linear in each argument, so a difference is exact but for float64 rounding
+    (1e-12 of its terms here); the kernel's side is bound as in the module text."""
+    ids, E, d = make(30, 3, 8, 32, 40, F32, 6)
+    h, u, out, got = check(ids, E, d)
+    g = torch.Generator().manual_seed(0)
+    c = {k: v.cpu().double() for k, v in d.items()}
+    flat = ids.cpu().view(-1).long()
+
+    def value(c):
+        y = torch.zeros(30, 40, dtype=torch.float64)
+        for t in range(30):
+            if flat[t] < 3:
+                y[t] = c["w"][t] * ((c["a"][flat[t]] @ c["x"][t]) @ c["b"][flat[t]])
+        return (y * c["g"]).sum()
+
+    ref = reference(ids, d, with_gbase=False)
+    plain = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_w=True)
+    for name, n, t in (("x", "grad_x", plain[0]), ("a", "grad_a", plain[1]), ("b", "grad_b", plain[2]), ("w", "grad_w", plain[3])):
+        v = torch.randn(c[name].shape, generator=g, dtype=torch.float64)
+        up, down = dict(c), dict(c)
+        up[name], down[name] = c[name] + v, c[name] - v
+        slope = (value(up) - value(down)) / 2
+        mine = (t.cpu().double() * v).sum()
+        assert abs(float(slope - mine)) <= float((ref[n][1] * v.abs()).sum()) + 1e-9, name
+
+
+def test_autograd_matches_the_calls_and_refuses_a_stale_layout():
+    ids, E, d = make(60, 4, 16, 64, 72, BF16, 8)
+    h = M.moe_layout(ids, E, 1)
+    leaves = {k: d[k].clone().requires_grad_() for k in ("x", "a", "b", "w", "base")}
+    out = M.autograd.lowrank(leaves["x"], leaves["a"], leaves["b"], leaves["w"], h, leaves["base"])
+    out.backward(d["g"])
+    ref, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+    assert torch.equal(out, ref)
+    got = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_w=True)
+    for k, t in zip(("x", "a", "b", "w"), got):
+        assert torch.equal(leaves[k].grad, t), k
+    assert torch.equal(leaves["base"].grad, d["g"])
+    # only the adapters learn
+    a2 = d["a"].clone().requires_grad_()
+    M.autograd.lowrank(d["x"], a2, d["b"], None, h, d["base"]).sum().backward()
+    assert a2.grad is not None
+    out = M.autograd.lowrank(leaves["x"], leaves["a"], leaves["b"], None, h)
+    M.moe_layout(ids, E, 1, handle=h)
+    with pytest.raises(M.autograd.StaleLayoutError):
+        out.sum().backward()
+
+
+def test_empty_batch():
+    ids, E, d = make(5, 3, 8, 16, 24, BF16, 1)
+    h = M.moe_layout(ids[:0], E, 1)
+    out, u = M.moe_lowrank(h, d["x"][:0], d["a"], d["b"], base=d["base"][:0])
+    assert out.shape == (0, 24) and u.shape == (0, 8)
+    ga = torch.full_like(d["a"], 5)
+    gx, ga, gb, _ = M.moe_lowrank_bwd(h, d["g"][:0], d["x"][:0], d["a"], d["b"], u, grad_a=ga)
+    assert gx.shape == (0, 16) and (ga == 0).all() and (gb == 0).all()
+
+
+def test_results_repeat_and_neighbours_stay():
+    ids, E, d = make(700, 6, 32, 264, 520, BF16, 3)
+    h, u, out, got = check(ids, E, d)
+    buf = torch.full((704, 520), 3.0, dtype=BF16, device=DEV)
+    for _ in range(4):
+        M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"], out=buf[2:702])
+        assert torch.equal(buf[2:702], out) and (buf[:2] == 3).all() and (buf[702:] == 3).all()
+        again = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_base=d["gbase"], grad_w=True)
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+def test_graph_replays_with_new_ids():
+    ids, E, d = make(48, 8, 16, 256, 264, BF16, 5)
+    h = M.Handle()
+    ws = torch.empty(M.moe_workspace_size(48, 1, E, 1), dtype=torch.uint8, device=DEV)
+    out, u = torch.empty_like(d["base"]), torch.empty((48, 16), device=DEV)
+    gx, ga, gb = torch.empty_like(d["x"]), torch.empty_like(d["a"]), torch.empty_like(d["b"])
+    gu = torch.empty((48, 16), device=DEV)
+
+    def step():
+        M.moe_layout(ids, E, 1, handle=h, workspace=ws)
+        M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"], out=out, u=u)
+        M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_x=gx, grad_a=ga, grad_b=gb, workspace=gu)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(4):
+        ids2, _, d2 = make(48, 8, 16, 256, 264, BF16, 60 + seed)
+        ids.copy_(ids2)
+        for k in ("x", "g", "base", "w"):
+            d[k].copy_(d2[k])
+        h2 = M.moe_layout(ids, E, 1)
+        ro, ru = M.moe_lowrank(h2, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+        rg = M.moe_lowrank_bwd(h2, d["g"], d["x"], d["a"], d["b"], ru, d["w"])
+        torch.cuda.synchronize()
+        for t in (out, u, gx, ga, gb, gu):
+            t.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ro) and torch.equal(gx, rg[0]) and torch.equal(ga, rg[1]) and torch.equal(gb, rg[2])
+
+
+def test_refusals():
+    ids, E, d = make(10, 3, 8, 16, 24, F32, 1)
+    x, a, b = d["x"], d["a"], d["b"]
+    h = M.moe_layout(ids, E, 1)
+    with pytest.raises(M.MoeError) as e:  # two adapters a token
+        M.moe_lowrank(M.moe_layout(ids.view(5, 2).contiguous(), E, 1), x[:5], a, b)
+    assert e.value.code == -2
+    with pytest.raises(M.MoeError) as e:  # more adapters than the layout has ids
+        M.moe_lowrank(M.moe_layout(ids.clamp(max=1), 2, 1), x, a, b)
+    assert e.value.code == -2
+    wide = torch.zeros(3, 132, 16, device=DEV)
+    with pytest.raises(M.MoeError) as e:
+        M.moe_lowrank(h, x, wide, torch.zeros(3, 132, 24, device=DEV))
+    assert e.value.code == -3
+    with pytest.raises(M.MoeError) as e:
+        M.moe_lowrank(h, x, torch.zeros(3, 6, 16, device=DEV), torch.zeros(3, 6, 24, device=DEV))
+    assert e.value.code == -2
+    with pytest.raises(RuntimeError, match="no layout"):
+        M.moe_lowrank(M.Handle(), x, a, b)
+    for bad in (lambda: M.moe_lowrank(h, x[:9], a, b), lambda: M.moe_lowrank(h, x, a[:2], b),
+                lambda: M.moe_lowrank(h, x, a.to(BF16), b), lambda: M.moe_lowrank(h, x, a, b, torch.ones(10, device=DEV)),
+                lambda: M.moe_lowrank(h, x, a, b, base=d["base"].t().contiguous().t()),
+                lambda: M.moe_lowrank_bwd(h, d["g"], x, a, b, torch.zeros(9, 8, device=DEV))):
+        with pytest.raises(ValueError):
+            bad()
+    _, u = M.moe_lowrank(h, x, a, b)
+    with pytest.raises(M.MoeError) as e:
+        M.moe_lowrank_bwd(h, d["g"], x, a, b, u, workspace=torch.empty(8, device=DEV))
+    assert e.value.code == -5
+    with pytest.raises(M.MoeError) as e:
+        M.moe_lowrank_bwd(h, d["g"], x, a, b, u, grad_x=False, grad_a=False, grad_b=False)
+    assert e.value.code == -1
