@@ -11,7 +11,7 @@ int check_few(int dtype, int64_t T, int K, int E, int64_t H, int64_t I) {
   if (eb == 0) return MOE_ERR_UNSUPPORTED;
   if (K > MOE_MAX_K || E > MOE_MAX_E) return MOE_ERR_UNSUPPORTED;
   if (T > MOE_FEW_MAX_PAIRS || T * K > MOE_FEW_MAX_PAIRS) return MOE_ERR_UNSUPPORTED;
-  if (H > (int64_t(1) << 20) || I > (int64_t(1) << 20)) return MOE_ERR_UNSUPPORTED;
+  if (H > (int64_t(1) << 18) || I > (int64_t(1) << 18)) return MOE_ERR_UNSUPPORTED;
   if ((H * eb) % 16 != 0 || (I * eb) % 16 != 0) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

@@ -31,4 +31,23 @@ __device__ __forceinline__ f32x4 mma_chunk(const u32x4 a, const u32x4 b, f32x4 a
   }
 }
 
+// Rows in memory as a buffer of `bytes` from p (uniform over the wave): a load
+// whose offset is past the end gives zeros and touches no memory, so the ends
+// of rows and tiles need no branches.  Offsets are 32 bits; kOutside lies past
+// every buffer made here (each below 2 GiB).
+constexpr uint32_t kOutside = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rows(const void* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
+}
+
+// The chunk at byte `lane_off` (per lane) + `off` (uniform).
+__device__ __forceinline__ u32x4 load_rows(__amdgpu_buffer_rsrc_t rows, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)lane_off, (int)off, 0));
+}
+
+// Keeps loads and products in the order they are written in: left alone, the
+// compiler gathers the loads of a software pipeline and waits for all of them.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 }  // namespace moe
