@@ -5,14 +5,14 @@
 //
 // A decode batch reads far more weight bytes than it computes on: the chosen
 // experts' weights, 3 H I elements each, are the floor, and each is read once
-// per call.  The matrix cores take 16 weight rows against up to 16 of the
-// expert's tokens a tile; one step of 1 KiB of weights costs 16 cycles of
-// matrix core for bfloat16, about a twenty-fifth of what the bytes cost.
+// per call.  The matrix cores take 8 weight rows against up to 8 of the
+// expert's tokens a tile; 1 KiB of weights costs 16 cycles of one matrix core
+// for bfloat16, about a twenty-fifth of what the bytes cost.
 //
 // No layout runs before: a call has at most 512 pairs, every wave holds their
 // ids in registers, and ballots give an expert's pairs.  A workgroup of the
-// first kernel owns (expert, 16 columns of act); its four waves split the sum
-// over H.  A workgroup of the second owns 8 columns of out for all pairs: its
+// first kernel owns (expert, columns of act); its four waves split the sum over H.
+//  A workgroup of the second owns 8 columns of out for all pairs: its
 // waves share out the experts, leave each pair's 8 values in LDS, and the
 // top-k sum is formed there in k order, so that no second pass over pairs, no
 // atomics and no order left to chance remain.  An id outside [0, E) belongs to
@@ -80,19 +80,40 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return 0.5f * g * (1.f + tanhf(y)) * u;
 }
 
-constexpr int kUpWaves = 4;
-constexpr int kUpDepth = 4;  // units of two steps in flight
+// A weight tile is 8 rows by one 128-byte line of each, one load instruction
+// of whole lines.  As an operand its 16 rows are the 8 rows twice, with the
+// first and the second half of the line; the 16 columns of the other operand
+// are 8 tokens twice likewise.  Two diagonal quarters of the result are the
+// halves' sums over the line, the other two are not used: the matrix cores
+// have far more to spare than the memory has.  (Streaming 0.8 GB of rows of 4
+// KiB on MI355X: 16 rows by 64 bytes an instruction 6.2 TB/s, whole lines
+// non-temporal 6.9 TB/s.)
+struct Lane {
+  int row, half, q;  // row (or token) of the tile, half of its line, chunk of the half
+  __device__ __forceinline__ Lane() : row(lane_id() & 7), half((lane_id() >> 3) & 1), q(lane_id() >> 4) {}
+  __device__ __forceinline__ int chunk() const { return half * 4 + q; }
+};
 
-// act for 16 columns of one expert.  A unit is 128 bytes of each row (two
-// steps), so that a wave reads whole cache lines; units go to the waves in
-// turn, and each wave keeps kUpDepth of them in flight.
-template <int DT, int NR, int NT>
+// Rows 4q..4q+3 (q < 2) of column `row` in the lanes of the first half: the
+// second half's quarter (rows 8.., columns 8..) joins the first's.
+__device__ __forceinline__ f32x4 join_halves(f32x4 acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += __shfl(acc[i], lane_id() + 40, kWave);
+  return acc;
+}
+
+constexpr int kUpWaves = 4;
+
+// act for 8 RT columns of one expert, NT tiles of 8 of its pairs at a time.
+// The lines of a row go to the waves in turn; a wave keeps `kDepth` lines of
+// every row of its tiles in flight.
+template <int DT, int NR, int RT, int NT>
 __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
-  constexpr int kDepth = NT == 1 ? kUpDepth : 2;
+  constexpr int kDepth = NT == 1 ? 4 : 2;
   __shared__ uint16_t list[kFewMaxPairs];
-  __shared__ f32x4 part[kUpWaves][NT][2][kWave];
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-  const int col = lane & 15, q = lane >> 4;
+  __shared__ f32x4 part[kUpWaves][NT][RT][2][kWave / 4];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+  const Lane at;
 
   int id[NR];
   load_ids(a, id);
@@ -110,82 +131,88 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 
   const int nch = a.hch;  // chunks of an x or w13 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
-  const int i0 = blockIdx.x * 16;
+  const int i0 = blockIdx.x * 8 * RT;
   const char* w13 = static_cast<const char*>(a.w13) + ((size_t)e * 2 * a.I + i0) * row_bytes;
   // rows past the last one are outside the buffer and read as zeros
-  const size_t tile_bytes = (size_t)min(16, a.I - i0) * row_bytes;
+  const size_t tile_bytes = (size_t)min(8 * RT, a.I - i0) * row_bytes;
   const auto gate = make_rows(w13, tile_bytes);
   const auto up = make_rows(w13 + (size_t)a.I * row_bytes, tile_bytes);
   const auto xs = make_rows(a.x, (size_t)a.T * row_bytes);
-  const uint32_t w_off = (uint32_t)col * row_bytes + q * 16;
-  const int units = (nch + 7) / 8;
+  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
+  const int lines = (nch + 7) / 8;
 
-  for (int first = 0; first < n; first += 16 * NT) {
+  for (int first = 0; first < n; first += 8 * NT) {
     uint32_t x_off[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {  // columns past the last pair repeat it and are not stored
-      const int p = list[min(first + c * 16 + col, n - 1)];
-      x_off[c] = (uint32_t)(p / a.K) * row_bytes + q * 16;
+      const int p = list[min(first + c * 8 + at.row, n - 1)];
+      x_off[c] = (uint32_t)(p / a.K) * row_bytes + at.chunk() * 16;
     }
-    f32x4 g[NT], u[NT];
+    f32x4 g[NT][RT], u[NT][RT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) g[c] = u[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 wg[kDepth][2], wu[kDepth][2], b[kDepth][2][NT];
-    auto fetch = [&](int d, int unit) {
-      const int ch = unit * 8;
-      const bool in0 = ch + q < nch, in1 = ch + 4 + q < nch;
-      const uint32_t off = (uint32_t)ch * 16;
-      wg[d][0] = load_rows(gate, in0 ? w_off : kOutside, off);
-      wg[d][1] = load_rows(gate, in1 ? w_off + 64 : kOutside, off);
-      wu[d][0] = load_rows(up, in0 ? w_off : kOutside, off);
-      wu[d][1] = load_rows(up, in1 ? w_off + 64 : kOutside, off);
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        b[d][0][c] = load_rows(xs, in0 ? x_off[c] : kOutside, off);
-        b[d][1][c] = load_rows(xs, in1 ? x_off[c] + 64 : kOutside, off);
+      for (int r = 0; r < RT; ++r) g[c][r] = u[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 wg[kDepth][RT], wu[kDepth][RT], b[kDepth][NT];
+    auto fetch = [&](int d, int line) {
+      const bool in = line * 8 + at.chunk() < nch;
+      const uint32_t off = (uint32_t)line * 128;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        wg[d][r] = load_rows<true>(gate, in ? w_off + r * 8 * row_bytes : kOutside, off);
+        wu[d][r] = load_rows<true>(up, in ? w_off + r * 8 * row_bytes : kOutside, off);
       }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) b[d][c] = load_rows(xs, in ? x_off[c] : kOutside, off);
     };
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       fetch(d, wave + d * kUpWaves);
       in_order();
     }
-    for (int unit = wave; unit < units; unit += kDepth * kUpWaves) {
+    for (int line = wave; line < lines; line += kDepth * kUpWaves) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int c = 0; c < NT; ++c)
 #pragma unroll
-          for (int c = 0; c < NT; ++c) {
-            g[c] = mma_chunk<DT>(wg[d][s], b[d][s][c], g[c]);
-            u[c] = mma_chunk<DT>(wu[d][s], b[d][s][c], u[c]);
+          for (int r = 0; r < RT; ++r) {
+            g[c][r] = mma_chunk<DT>(wg[d][r], b[d][c], g[c][r]);
+            u[c][r] = mma_chunk<DT>(wu[d][r], b[d][c], u[c][r]);
           }
         in_order();
-        fetch(d, unit + (d + kDepth) * kUpWaves);  // past the end: zeros
+        fetch(d, line + (d + kDepth) * kUpWaves);  // past the end: zeros
         in_order();
       }
     }
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      part[wave][c][0][lane] = g[c];
-      part[wave][c][1][lane] = u[c];
-    }
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const f32x4 sg = join_halves(g[c][r]), su = join_halves(u[c][r]);
+        if (at.half == 0 && at.q < 2) {
+          part[wave][c][r][0][at.q * 8 + at.row] = sg;
+          part[wave][c][r][1][at.q * 8 + at.row] = su;
+        }
+      }
     __syncthreads();
-    for (int c = wave; c < NT; c += kUpWaves) {
-      f32x4 sg = part[0][c][0][lane], su = part[0][c][1][lane];
+    // 16 lanes per tile: quad and pair
+    for (int i = threadIdx.x; i < NT * RT * 16; i += kUpWaves * kWave) {
+      const int slot = i & 15, r = (i >> 4) % RT, c = (i >> 4) / RT;
+      f32x4 sg = part[0][c][r][0][slot], su = part[0][c][r][1][slot];
 #pragma unroll
       for (int v = 1; v < kUpWaves; ++v) {
-        sg += part[v][c][0][lane];
-        su += part[v][c][1][lane];
+        sg += part[v][c][r][0][slot];
+        su += part[v][c][r][1][slot];
       }
-      const int at = first + c * 16 + col;
-      if (at < n) {
-        const size_t row = (size_t)list[at] * a.I;
+      const int pos = first + c * 8 + (slot & 7);
+      if (pos < n) {
+        const size_t row = (size_t)list[pos] * a.I;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int ii = i0 + q * 4 + r;
+        for (int k = 0; k < 4; ++k) {
+          const int ii = i0 + r * 8 + (slot >> 3) * 4 + k;
           if (ii < a.I) {
-            const float v = gated(sg[r], su[r], a.act);
+            const float v = gated(sg[k], su[k], a.act);
             // act is rounded to the element type: the second product's
             // operand, as between two separate products
             if constexpr (DT == kF32) static_cast<float*>(a.mid)[row + ii] = v;
@@ -199,22 +226,17 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 }
 
 // 8 columns of out, for every pair.  A wave's item is (group, part of the sum
-// over I).  The 16 rows of a matrix-core tile are 8 rows of W2 twice, once for
-// each half of the item's part, its 16 columns 8 pairs twice likewise; the two
-// diagonal quarters of the result are the halves' sums, the others are not
-// used.  So a workgroup needs 8 columns of out only, and there are enough
-// workgroups for the chip at the usual widths.  Each item leaves its pairs' 8
-// values in y[part][pair].
+// over I); it leaves its pairs' 8 values in y[part][pair].
 constexpr int kDownWaves = 16;
 
 template <int DT, int NR>
 __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
-  constexpr int kDepth = 6;  // steps in flight
+  constexpr int kDepth = 6;  // lines in flight
   extern __shared__ f32x4 lds[];
   f32x4* y = lds;  // [split][pairs][2]: 8 columns as two quads
   uint16_t* lists = reinterpret_cast<uint16_t*>(lds + (size_t)a.split * a.pairs * 2);  // [kDownWaves][pairs]
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-  const int col = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+  const Lane at;
   uint16_t* list = lists + (size_t)wave * a.pairs;
 
   int id[NR];
@@ -224,6 +246,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   const int h0 = blockIdx.x * 8;
   const size_t tile_bytes = (size_t)min(8, a.H - h0) * row_bytes;
   const auto mid = make_rows(a.mid, (size_t)a.pairs * row_bytes);
+  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
+  const int lines = (nch + 7) / 8;
   const int items = a.groups * a.split;
   for (int it = wave; it < items; it += kDownWaves) {
     const int grp = it / a.split, part = it - grp * a.split;
@@ -231,40 +255,33 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     if (e < 0) continue;
     const int n = list_pairs(id, e, list);
     const auto w2 = make_rows(static_cast<const char*>(a.w2) + ((size_t)e * a.H + h0) * row_bytes, tile_bytes);
-    // chunks [lo, hi) of this half of the part
-    const int lo = part * a.part_ch + half * (a.part_ch / 2);
-    const int hi = min(lo + a.part_ch / 2, nch);
-    const int steps = a.part_ch / 8;
-    const uint32_t w_off = (uint32_t)col * row_bytes + (lo + q) * 16;
+    const int lo = part * a.part_lines, hi = min(lo + a.part_lines, lines);
     for (int first = 0; first < n; first += 8) {
-      const int p = list[min(first + col, n - 1)];
-      const uint32_t m_off = (uint32_t)p * row_bytes + (lo + q) * 16;
+      const int p = list[min(first + at.row, n - 1)];
+      const uint32_t m_off = (uint32_t)p * row_bytes + at.chunk() * 16;
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
       u32x4 w[kDepth], b[kDepth];
-      auto fetch = [&](int d, int step) {
-        const bool in = lo + step * 4 + q < hi;
-        w[d] = load_rows(w2, in ? w_off : kOutside, (uint32_t)step * 64);
-        b[d] = load_rows(mid, in ? m_off : kOutside, (uint32_t)step * 64);
+      auto fetch = [&](int d, int line) {
+        const bool in = line < hi && line * 8 + at.chunk() < nch;
+        w[d] = load_rows<true>(w2, in ? w_off : kOutside, (uint32_t)line * 128);
+        b[d] = load_rows(mid, in ? m_off : kOutside, (uint32_t)line * 128);
       };
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        fetch(d, d);
+        fetch(d, lo + d);
         in_order();
       }
-      for (int step = 0; step < steps; step += kDepth) {
+      for (int line = lo; line < hi; line += kDepth) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
           acc = mma_chunk<DT>(w[d], b[d], acc);
           in_order();
-          fetch(d, step + kDepth + d);  // past the end: zeros
+          fetch(d, line + kDepth + d);  // past the end: zeros
           in_order();
         }
       }
-      // result rows 4q..4q+3 of column lane % 16: the second half's diagonal
-      // quarter (q >= 2, columns 8..15) joins the first's
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += __shfl(acc[i], lane + 40, kWave);
-      if (q < 2 && half == 0 && first + col < n) y[((size_t)part * a.pairs + p) * 2 + q] = acc;
+      acc = join_halves(acc);
+      if (at.half == 0 && at.q < 2 && first + at.row < n) y[((size_t)part * a.pairs + p) * 2 + at.q] = acc;
     }
   }
   __syncthreads();
@@ -283,19 +300,20 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
       for (int s = 1; s < a.split; ++s) v += yf[((size_t)s * a.pairs + p) * 8 + c];
       sum = __fadd_rn(sum, a.w ? __fmul_rn(a.w[p], v) : v);
     }
-    const size_t at = (size_t)t * a.H + h0 + c;
-    if constexpr (DT == kF32) static_cast<float*>(a.out)[at] = sum;
-    else static_cast<uint16_t*>(a.out)[at] = (uint16_t)f32_to_bf16(sum);
+    const size_t pos = (size_t)t * a.H + h0 + c;
+    if constexpr (DT == kF32) static_cast<float*>(a.out)[pos] = sum;
+    else static_cast<uint16_t*>(a.out)[pos] = (uint16_t)f32_to_bf16(sum);
   }
 }
 
 template <int DT, int NR>
 hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
-  const dim3 up((a.I + 15) / 16, a.groups);
+  constexpr int RT = 2;
+  const dim3 up((a.I + 8 * RT - 1) / (8 * RT), a.groups);
   if (a.pairs <= 8 * a.E)
-    hipLaunchKernelGGL((few_up_kernel<DT, NR, 1>), up, dim3(kUpWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL((few_up_kernel<DT, NR, RT, 1>), up, dim3(kUpWaves * kWave), 0, s, a);
   else
-    hipLaunchKernelGGL((few_up_kernel<DT, NR, 4>), up, dim3(kUpWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL((few_up_kernel<DT, NR, RT, 4>), up, dim3(kUpWaves * kWave), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t lds = (size_t)a.split * a.pairs * 32 + (size_t)kDownWaves * a.pairs * 2;
@@ -310,7 +328,7 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s) {
   a.groups = a.pairs > a.E ? a.E : a.pairs;
   a.split = 1;
   while (a.groups * a.split < kDownWaves && 2 * a.split * a.pairs <= kFewMaxPairs) a.split *= 2;
-  a.part_ch = ((a.ich + a.split - 1) / a.split + 15) / 16 * 16;  // two halves of whole cache lines
+  a.part_lines = ((a.ich + 7) / 8 + a.split - 1) / a.split;
   if (a.pairs <= kWave)
     return a.dtype == MOE_F32 ? launch_few_typed<kF32, 1>(a, s) : launch_few_typed<kBF16, 1>(a, s);
   return a.dtype == MOE_F32 ? launch_few_typed<kF32, 8>(a, s) : launch_few_typed<kBF16, 8>(a, s);

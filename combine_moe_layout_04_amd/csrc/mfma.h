@@ -41,9 +41,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rows(const void* p, size_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
 }
 
-// The chunk at byte `lane_off` (per lane) + `off` (uniform).
+// The chunk at byte `lane_off` (per lane) + `off` (uniform).  ONCE: read by
+// nobody else, so marked non-temporal; that pays only where one instruction
+// takes whole 128-byte lines.
+template <bool ONCE = false>
 __device__ __forceinline__ u32x4 load_rows(__amdgpu_buffer_rsrc_t rows, uint32_t lane_off, uint32_t off) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)lane_off, (int)off, 0));
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)lane_off, (int)off, ONCE ? 2 : 0));
 }
 
 // Keeps loads and products in the order they are written in: left alone, the
