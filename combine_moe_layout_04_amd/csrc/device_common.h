@@ -87,6 +87,24 @@ __device__ __forceinline__ float read_lane_f(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
+// Data-parallel move of a lane's value (DPP control CTRL, rows of 16 lanes in
+// the mask ROWS); lanes without a source get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += dpp0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8: rows of 16 lanes
+  v += dpp0<0x112, 0xF>(v);
+  v += dpp0<0x114, 0xF>(v);
+  v += dpp0<0x118, 0xF>(v);
+  v += dpp0<0x142, 0xA>(v);  // last lane of a row to the next row
+  v += dpp0<0x143, 0xC>(v);  // lane 31 to the upper half
+  return v;
+}
+
 // Fold the 64 lane partials: for s = 32, 16, ..., 1 every lane adds the
 // partial of lane (l xor s).  float32 addition is commutative, so every lane
 // ends with the same value, the one partial 0 holds.

@@ -9,14 +9,16 @@
 // expert's tokens a tile; 1 KiB of weights costs 16 cycles of one matrix core
 // for bfloat16, about a twenty-fifth of what the bytes cost.
 //
-// No layout runs before: a call has at most 512 pairs, every wave holds their
-// ids in registers, and ballots give an expert's pairs.  A workgroup of the
-// first kernel owns (expert, columns of act); its four waves split the sum over H.
-//  A workgroup of the second owns 8 columns of out for all pairs: its
-// waves share out the experts, leave each pair's 8 values in LDS, and the
-// top-k sum is formed there in k order, so that no second pass over pairs, no
-// atomics and no order left to chance remain.  An id outside [0, E) belongs to
-// no expert here and adds nothing.
+// No layout runs before: a call has at most 512 pairs, and every workgroup
+// groups them by expert in its LDS as it starts.  A workgroup of the first
+// kernel takes (expert, 8 columns of act) after another; its waves split the
+// sum over H.  A workgroup of the second owns 8 columns of out for all pairs:
+// its waves share out the experts, leave each pair's 8 values in LDS, and the
+// top-k sum is formed there in k order, so that no second pass over pairs and
+// no order left to chance remain.  An id outside [0, E) belongs to no expert
+// here and adds nothing.
+#include <algorithm>
+
 #include "device_common.h"
 #include "internal.h"
 #include "mfma.h"
@@ -25,52 +27,60 @@
 namespace moe {
 namespace {
 
-// The ids of all pairs, pair 64 r + lane in register r; -1 where there is no
-// pair or no expert.
-template <int NR>
-__device__ __forceinline__ void load_ids(const FewArgs& a, int (&id)[NR]) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int p = r * kWave + lane;
-    id[r] = -1;
-    if (p < a.pairs) {
-      const int64_t e = a.itype == MOE_I32 ? (int64_t)static_cast<const int*>(a.idx)[p]
-                                           : static_cast<const int64_t*>(a.idx)[p];
-      if (e >= 0 && e < a.E) id[r] = (int)e;
-    }
-  }
+__device__ __forceinline__ int pair_expert(const FewArgs& a, int p) {  // -1: none of this call's experts
+  const int64_t e = a.itype == MOE_I32 ? (int64_t)static_cast<const int*>(a.idx)[p]
+                                       : static_cast<const int64_t*>(a.idx)[p];
+  return e >= 0 && e < a.E ? (int)e : -1;
 }
 
-// Group g of the call: with fewer pairs than experts the expert of pair g,
-// unless an earlier pair has the same one (-1 then); else expert g.
-template <int NR>
-__device__ __forceinline__ int group_expert(const FewArgs& a, const int (&id)[NR], int g) {
-  if (a.pairs > a.E) return g;
-  int e = -1;
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-    if (g / kWave == r) e = read_lane_i(id[r], g % kWave);
-  if (e < 0) return -1;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const uint64_t same = __ballot(id[r] == e);
-    if (same) return r * kWave + __builtin_ctzll(same) == g ? e : -1;
-  }
-  return -1;
-}
+// The pairs of a call grouped by expert, in a workgroup's LDS.
+struct Groups {
+  int count[MOE_MAX_E];
+  uint32_t used[kFewMaxPairs];   // experts with pairs, ascending: expert << 20 | first place << 10 | pairs
+  uint16_t pairs[kFewMaxPairs];  // grouped by expert
+};
 
-// The pairs of expert e in ascending order, written to `list`; their number.
-template <int NR>
-__device__ __forceinline__ int list_pairs(const int (&id)[NR], int e, uint16_t* list) {
+// Fills g for the whole workgroup (at least kFewMaxPairs / PER threads, each
+// with PER pairs); the number of experts with pairs.  The order of an
+// expert's pairs is left to the LDS atomics: it only says which column of a
+// tile a pair takes, and a column's value does not depend on its place.
+template <int PER>
+__device__ __forceinline__ int group_pairs(const FewArgs& a, Groups& g) {
+  int e[PER], place[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int p = threadIdx.x + i * blockDim.x;
+    e[i] = p < a.pairs ? pair_expert(a, p) : -1;
+  }
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) g.count[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i) place[i] = e[i] >= 0 ? atomicAdd(&g.count[e[i]], 1) : 0;
+  __syncthreads();
+  // every wave counts the experts, the first one notes them and turns the
+  // counts into first places
   const int lane = lane_id();
   int n = 0;
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const uint64_t mine = __ballot(id[r] == e);
-    if (id[r] == e) list[n + __popcll(mine & lanes_below(lane))] = (uint16_t)(r * kWave + lane);
-    n += __popcll(mine);
+  uint32_t first = 0;
+  for (int i = 0; i < a.E; i += kWave) {
+    const uint32_t c = i + lane < a.E ? (uint32_t)g.count[i + lane] : 0u;
+    const uint64_t mask = __ballot(c != 0);
+    if (threadIdx.x < kWave) {
+      const uint32_t end = wave_scan(c);
+      if (c) g.used[n + __popcll(mask & lanes_below(lane))] = (uint32_t)(i + lane) << 20 | (first + end - c) << 10 | c;
+      first += (uint32_t)read_lane_i((int)end, 63);
+    }
+    n += __popcll(mask);
   }
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    for (int j = lane; j < n; j += kWave) g.count[g.used[j] >> 20] = (int)(g.used[j] >> 10 & 1023);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (e[i] >= 0) g.pairs[g.count[e[i]] + place[i]] = (uint16_t)(threadIdx.x + i * blockDim.x);
+  __syncthreads();
   return n;
 }
 
@@ -102,187 +112,249 @@ __device__ __forceinline__ f32x4 join_halves(f32x4 acc) {
   return acc;
 }
 
-constexpr int kUpWaves = 4;
-
-// act for 8 RT columns of one expert, NT tiles of 8 of its pairs at a time.
-// The lines of a row go to the waves in turn; a wave keeps `kDepth` lines of
-// every row of its tiles in flight.
-template <int DT, int NR, int RT, int NT>
-__global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
-  constexpr int kDepth = NT == 1 ? 4 : 2;
-  __shared__ uint16_t list[kFewMaxPairs];
-  __shared__ f32x4 part[kUpWaves][NT][RT][2][kWave / 4];
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-  const Lane at;
-
-  int id[NR];
-  load_ids(a, id);
-  const int e = group_expert(a, id, blockIdx.y);
-  if (e < 0) return;  // the whole workgroup: every wave holds the same ids
-  int n = 0;
-  if (wave == 0) {
-    n = list_pairs(id, e, list);
-  } else {
+template <int DT>
+__device__ __forceinline__ void store_act(const FewArgs& a, int pair, int i0, f32x4 g, f32x4 u) {
+  const size_t row = (size_t)pair * a.I;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) n += __popcll(__ballot(id[r] == e));
-  }
-  if (n == 0) return;
-  __syncthreads();
-
-  const int nch = a.hch;  // chunks of an x or w13 row
-  const uint32_t row_bytes = (uint32_t)nch * 16;
-  const int i0 = blockIdx.x * 8 * RT;
-  const char* w13 = static_cast<const char*>(a.w13) + ((size_t)e * 2 * a.I + i0) * row_bytes;
-  // rows past the last one are outside the buffer and read as zeros
-  const size_t tile_bytes = (size_t)min(8 * RT, a.I - i0) * row_bytes;
-  const auto gate = make_rows(w13, tile_bytes);
-  const auto up = make_rows(w13 + (size_t)a.I * row_bytes, tile_bytes);
-  const auto xs = make_rows(a.x, (size_t)a.T * row_bytes);
-  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
-  const int lines = (nch + 7) / 8;
-
-  for (int first = 0; first < n; first += 8 * NT) {
-    uint32_t x_off[NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {  // columns past the last pair repeat it and are not stored
-      const int p = list[min(first + c * 8 + at.row, n - 1)];
-      x_off[c] = (uint32_t)(p / a.K) * row_bytes + at.chunk() * 16;
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + k;
+    if (i < a.I) {
+      const float v = gated(g[k], u[k], a.act);
+      // act is rounded to the element type: the second product's operand, as
+      // between two separate products
+      if constexpr (DT == kF32) static_cast<float*>(a.mid)[row + i] = v;
+      else static_cast<uint16_t*>(a.mid)[row + i] = (uint16_t)f32_to_bf16(v);
     }
-    f32x4 g[NT][RT], u[NT][RT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) g[c][r] = u[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 wg[kDepth][RT], wu[kDepth][RT], b[kDepth][NT];
-    auto fetch = [&](int d, int line) {
-      const bool in = line * 8 + at.chunk() < nch;
-      const uint32_t off = (uint32_t)line * 128;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        wg[d][r] = load_rows<true>(gate, in ? w_off + r * 8 * row_bytes : kOutside, off);
-        wu[d][r] = load_rows<true>(up, in ? w_off + r * 8 * row_bytes : kOutside, off);
-      }
-#pragma unroll
-      for (int c = 0; c < NT; ++c) b[d][c] = load_rows(xs, in ? x_off[c] : kOutside, off);
-    };
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      fetch(d, wave + d * kUpWaves);
-      in_order();
-    }
-    for (int line = wave; line < lines; line += kDepth * kUpWaves) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            g[c][r] = mma_chunk<DT>(wg[d][r], b[d][c], g[c][r]);
-            u[c][r] = mma_chunk<DT>(wu[d][r], b[d][c], u[c][r]);
-          }
-        in_order();
-        fetch(d, line + (d + kDepth) * kUpWaves);  // past the end: zeros
-        in_order();
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const f32x4 sg = join_halves(g[c][r]), su = join_halves(u[c][r]);
-        if (at.half == 0 && at.q < 2) {
-          part[wave][c][r][0][at.q * 8 + at.row] = sg;
-          part[wave][c][r][1][at.q * 8 + at.row] = su;
-        }
-      }
-    __syncthreads();
-    // 16 lanes per tile: quad and pair
-    for (int i = threadIdx.x; i < NT * RT * 16; i += kUpWaves * kWave) {
-      const int slot = i & 15, r = (i >> 4) % RT, c = (i >> 4) / RT;
-      f32x4 sg = part[0][c][r][0][slot], su = part[0][c][r][1][slot];
-#pragma unroll
-      for (int v = 1; v < kUpWaves; ++v) {
-        sg += part[v][c][r][0][slot];
-        su += part[v][c][r][1][slot];
-      }
-      const int pos = first + c * 8 + (slot & 7);
-      if (pos < n) {
-        const size_t row = (size_t)list[pos] * a.I;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int ii = i0 + r * 8 + (slot >> 3) * 4 + k;
-          if (ii < a.I) {
-            const float v = gated(sg[k], su[k], a.act);
-            // act is rounded to the element type: the second product's
-            // operand, as between two separate products
-            if constexpr (DT == kF32) static_cast<float*>(a.mid)[row + ii] = v;
-            else static_cast<uint16_t*>(a.mid)[row + ii] = (uint16_t)f32_to_bf16(v);
-          }
-        }
-      }
-    }
-    __syncthreads();
   }
 }
 
-// 8 columns of out, for every pair.  A wave's item is (group, part of the sum
-// over I); it leaves its pairs' 8 values in y[part][pair].
-constexpr int kDownWaves = 16;
+// act, in items of (expert, 8 columns).  A workgroup's waves take the lines of
+// the item's rows in turn and meet in LDS; they work in rounds of kDepth lines
+// each and ask for the next round's while they multiply this one's, from item
+// to item too.  NT tiles of 8 of the expert's pairs at a time.
+//
+// Two things decide how near to the memory's rate this comes (64 tokens, 126
+// experts of 768 columns and rows of 4 KiB, 0.79 GB):
+//   - workgroup b takes items b, b + grid, ..., so that all of them together
+//     move through a narrow window of the weights: 164 us with even runs of
+//     neighbouring items, 140 us in steps;
+//   - each workgroup starts at another line of its rows (and goes round): rows
+//     4 KiB apart read at the same place at the same time meet in a few memory
+//     channels.  140 -> 134 us.  The sum's order depends on the item alone
+//     through its workgroup, so it is the same in every run.
+// More lines in flight (8 a wave), fewer, and other numbers of workgroups and
+// waves were all within 132 to 156 us.
+constexpr int kUpWaves = 4;
+constexpr int kUpGroups = 1024;  // workgroups at most: four a CU
 
-template <int DT, int NR>
-__global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
-  constexpr int kDepth = 6;  // lines in flight
-  extern __shared__ f32x4 lds[];
-  f32x4* y = lds;  // [split][pairs][2]: 8 columns as two quads
-  uint16_t* lists = reinterpret_cast<uint16_t*>(lds + (size_t)a.split * a.pairs * 2);  // [kDownWaves][pairs]
+template <int DT, int NT>
+__global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
+  constexpr int kDepth = NT == 1 ? 4 : 2;
+  __shared__ Groups groups;
+  __shared__ f32x4 part[kUpWaves][NT][2][kWave / 4];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
-  uint16_t* list = lists + (size_t)wave * a.pairs;
 
-  int id[NR];
-  load_ids(a, id);
+  const int slabs = (a.I + 7) / 8;
+  const int items = group_pairs<kFewMaxPairs / (kUpWaves * kWave)>(a, groups) * slabs;
+  int item = blockIdx.x;
+  if (item >= items) return;  // the whole workgroup
+
+  const int nch = a.hch;  // chunks of an x or w13 row
+  const uint32_t row_bytes = (uint32_t)nch * 16;
+  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
+  const int lines = (nch + 7) / 8;
+  const int rounds = (lines + kUpWaves * kDepth - 1) / (kUpWaves * kDepth);
+  const int start = blockIdx.x * 4 % lines;
+  const auto xs = make_rows(a.x, (size_t)a.T * row_bytes);
+
+  u32x4 wg[kDepth], wu[kDepth], b[kDepth][NT];
+  uint32_t x_off[NT];
+  auto gate = make_rows(a.w13, 0), up = gate;
+  int slab = 0, n = 0;  // of the item being fetched
+  const uint16_t* list = groups.pairs;
+  auto fetch_item = [&]() {
+    slab = item % slabs;
+    const uint32_t group = (uint32_t)__builtin_amdgcn_readfirstlane((int)groups.used[item / slabs]);
+    const int e = (int)(group >> 20);
+    list = groups.pairs + (group >> 10 & 1023);
+    n = (int)(group & 1023);
+    // rows past the last one are outside the buffer and read as zeros
+    const size_t first = (size_t)e * 2 * a.I + slab * 8;
+    const size_t bytes = (size_t)min(8, a.I - slab * 8) * row_bytes;
+    gate = make_rows(static_cast<const char*>(a.w13) + first * row_bytes, bytes);
+    up = make_rows(static_cast<const char*>(a.w13) + (first + a.I) * row_bytes, bytes);
+  };
+  auto tokens = [&](int first) {  // columns past the last pair repeat it and are not stored
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+      x_off[c] = (uint32_t)(list[min(first + c * 8 + at.row, n - 1)] / a.K) * row_bytes + at.chunk() * 16;
+  };
+  auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
+    const int line = i + start < lines ? i + start : i + start - lines;
+    const bool in = i < lines && line * 8 + at.chunk() < nch;
+    const uint32_t off = in ? w_off : kOutside;
+    wg[d] = load_rows<true>(gate, off, (uint32_t)line * 128);
+    wu[d] = load_rows<true>(up, off, (uint32_t)line * 128);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) b[d][c] = load_rows(xs, in ? x_off[c] : kOutside, (uint32_t)line * 128);
+  };
+
+  fetch_item();
+  tokens(0);
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) {
+    fetch(d, wave + d * kUpWaves);
+    in_order();
+  }
+  f32x4 g[NT], u[NT];
+#pragma unroll
+  for (int c = 0; c < NT; ++c) g[c] = u[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int first = 0, round = 0; item < items;) {
+    const int this_i = slab * 8, this_n = n, this_first = first;
+    const uint16_t* this_list = list;
+    int next = wave + (round + 1) * kDepth * kUpWaves;
+    if (++round == rounds) {
+      round = 0;
+      next = wave;
+      first += 8 * NT;
+      if (first >= n) {
+        first = 0;
+        item += gridDim.x;
+        if (item < items) fetch_item();
+        else next = lines;  // nothing more to fetch
+      }
+      tokens(first);
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        g[c] = mma_chunk<DT>(wg[d], b[d][c], g[c]);
+        u[c] = mma_chunk<DT>(wu[d], b[d][c], u[c]);
+      }
+      in_order();
+      fetch(d, next + d * kUpWaves);
+      in_order();
+    }
+    if (round == 0) {
+      __syncthreads();  // the last results have been read
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const f32x4 sg = join_halves(g[c]), su = join_halves(u[c]);
+        g[c] = u[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (at.half == 0 && at.q < 2) {
+          part[wave][c][0][at.q * 8 + at.row] = sg;
+          part[wave][c][1][at.q * 8 + at.row] = su;
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < NT * 16) {  // 16 lanes per tile: quad and pair
+        const int slot = threadIdx.x & 15, c = threadIdx.x >> 4;
+        f32x4 sg = part[0][c][0][slot], su = part[0][c][1][slot];
+#pragma unroll
+        for (int v = 1; v < kUpWaves; ++v) {
+          sg += part[v][c][0][slot];
+          su += part[v][c][1][slot];
+        }
+        const int pos = this_first + c * 8 + (slot & 7);
+        if (pos < this_n) store_act<DT>(a, this_list[pos], this_i + (slot >> 3) * 4, sg, su);
+      }
+    }
+  }
+}
+
+// 8 columns of out, for every pair.  A wave's item is (expert, part of the sum
+// over I); it leaves its pairs' 8 values in y[part][pair].  The waves stream
+// their items' weights in rounds of kDepth lines, the next round's (of the same
+// item or the next) under way during this one.
+constexpr int kDownWaves = 16;
+
+template <int DT>
+__global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
+  constexpr int kDepth = 3;
+  __shared__ Groups groups;
+  __shared__ float weight[kFewMaxPairs];
+  __shared__ uint8_t here[kFewMaxPairs];
+  extern __shared__ f32x4 y[];  // [split][pairs][2]: 8 columns as two quads
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+  const Lane at;
+
+  if (threadIdx.x < a.pairs) {
+    weight[threadIdx.x] = a.w ? a.w[threadIdx.x] : 1.f;
+    here[threadIdx.x] = pair_expert(a, threadIdx.x) >= 0;
+  }
+  const int items = group_pairs<1>(a, groups) * a.split;
+  // the split divides the number of waves: a wave has one part of all its experts
+  const int part = wave % a.split;
+
   const int nch = a.ich;  // chunks of an act or w2 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
   const int h0 = blockIdx.x * 8;
   const size_t tile_bytes = (size_t)min(8, a.H - h0) * row_bytes;
   const auto mid = make_rows(a.mid, (size_t)a.pairs * row_bytes);
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
-  const int lines = (nch + 7) / 8;
-  const int items = a.groups * a.split;
-  for (int it = wave; it < items; it += kDownWaves) {
-    const int grp = it / a.split, part = it - grp * a.split;
-    const int e = group_expert(a, id, grp);
-    if (e < 0) continue;
-    const int n = list_pairs(id, e, list);
-    const auto w2 = make_rows(static_cast<const char*>(a.w2) + ((size_t)e * a.H + h0) * row_bytes, tile_bytes);
-    const int lo = part * a.part_lines, hi = min(lo + a.part_lines, lines);
-    for (int first = 0; first < n; first += 8) {
-      const int p = list[min(first + at.row, n - 1)];
-      const uint32_t m_off = (uint32_t)p * row_bytes + at.chunk() * 16;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      u32x4 w[kDepth], b[kDepth];
-      auto fetch = [&](int d, int line) {
-        const bool in = line < hi && line * 8 + at.chunk() < nch;
-        w[d] = load_rows<true>(w2, in ? w_off : kOutside, (uint32_t)line * 128);
-        b[d] = load_rows(mid, in ? m_off : kOutside, (uint32_t)line * 128);
-      };
+  const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 7) / 8);
+  const int rounds = (a.part_lines + kDepth - 1) / kDepth;
+
+  u32x4 w[kDepth], b[kDepth];
+  auto w2 = make_rows(a.w2, 0);
+  uint32_t m_off = 0;
+  int n = 0;  // pairs of the fetched item
+  const uint16_t* list = groups.pairs;
+  auto item = [&](int j) {
+    const uint32_t group = (uint32_t)__builtin_amdgcn_readfirstlane((int)groups.used[j / a.split]);
+    list = groups.pairs + (group >> 10 & 1023);
+    n = (int)(group & 1023);
+    w2 = make_rows(static_cast<const char*>(a.w2) + ((size_t)(group >> 20) * a.H + h0) * row_bytes, tile_bytes);
+  };
+  auto pairs_of = [&](int first) {  // columns past the last pair repeat it and are not stored
+    m_off = (uint32_t)list[min(first + at.row, n - 1)] * row_bytes + at.chunk() * 16;
+  };
+  auto fetch = [&](int d, int line) {
+    const bool in = line < hi && line * 8 + at.chunk() < nch;
+    w[d] = load_rows<true>(w2, in ? w_off : kOutside, (uint32_t)line * 128);
+    b[d] = load_rows(mid, in ? m_off : kOutside, (uint32_t)line * 128);
+  };
+  if (wave < items) {
+    item(wave);
+    pairs_of(0);
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        fetch(d, lo + d);
-        in_order();
-      }
-      for (int line = lo; line < hi; line += kDepth) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          acc = mma_chunk<DT>(w[d], b[d], acc);
-          in_order();
-          fetch(d, line + kDepth + d);  // past the end: zeros
-          in_order();
-        }
-      }
-      acc = join_halves(acc);
-      if (at.half == 0 && at.q < 2 && first + at.row < n) y[((size_t)part * a.pairs + p) * 2 + at.q] = acc;
+    for (int d = 0; d < kDepth; ++d) {
+      fetch(d, lo + d);
+      in_order();
     }
+  }
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int j = wave, first = 0, round = 0; j < items;) {
+    const int p = (int)list[min(first + at.row, n - 1)], left = n - first;
+    int next_j = j, next_first = first, next_round = round + 1;
+    if (next_round == rounds) {
+      next_round = 0;
+      next_first += 8;
+      if (next_first >= n) {
+        next_first = 0;
+        next_j += kDownWaves;
+        if (next_j < items) item(next_j);
+      }
+      if (next_j < items) pairs_of(next_first);
+    }
+    const int next_line = next_j < items ? lo + next_round * kDepth : hi;
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      acc = mma_chunk<DT>(w[d], b[d], acc);
+      in_order();
+      fetch(d, next_line + d);  // past the end: zeros
+      in_order();
+    }
+    if (next_round == 0) {
+      acc = join_halves(acc);
+      if (at.half == 0 && at.q < 2 && at.row < left) y[((size_t)part * a.pairs + p) * 2 + at.q] = acc;
+      acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    j = next_j;
+    first = next_first;
+    round = next_round;
   }
   __syncthreads();
 
@@ -293,12 +365,10 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k) {
       const int p = t * a.K + k;
-      const int64_t e = a.itype == MOE_I32 ? (int64_t)static_cast<const int*>(a.idx)[p]
-                                           : static_cast<const int64_t*>(a.idx)[p];
-      if (e < 0 || e >= a.E) continue;
+      if (!here[p]) continue;
       float v = yf[(size_t)p * 8 + c];
-      for (int s = 1; s < a.split; ++s) v += yf[((size_t)s * a.pairs + p) * 8 + c];
-      sum = __fadd_rn(sum, a.w ? __fmul_rn(a.w[p], v) : v);
+      for (int i = 1; i < a.split; ++i) v += yf[((size_t)i * a.pairs + p) * 8 + c];
+      sum = __fadd_rn(sum, __fmul_rn(weight[p], v));
     }
     const size_t pos = (size_t)t * a.H + h0 + c;
     if constexpr (DT == kF32) static_cast<float*>(a.out)[pos] = sum;
@@ -306,18 +376,17 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   }
 }
 
-template <int DT, int NR>
+template <int DT>
 hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
-  constexpr int RT = 2;
-  const dim3 up((a.I + 8 * RT - 1) / (8 * RT), a.groups);
-  if (a.pairs <= 8 * a.E)
-    hipLaunchKernelGGL((few_up_kernel<DT, NR, RT, 1>), up, dim3(kUpWaves * kWave), 0, s, a);
+  const int up = (int)std::min<int64_t>(kUpGroups, (int64_t)a.groups * ((a.I + 7) / 8));
+  if (a.pairs <= 4 * a.E)
+    hipLaunchKernelGGL((few_up_kernel<DT, 1>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
   else
-    hipLaunchKernelGGL((few_up_kernel<DT, NR, RT, 4>), up, dim3(kUpWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL((few_up_kernel<DT, 4>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = (size_t)a.split * a.pairs * 32 + (size_t)kDownWaves * a.pairs * 2;
-  hipLaunchKernelGGL((few_down_kernel<DT, NR>), dim3((a.H + 7) / 8), dim3(kDownWaves * kWave), lds, s, a);
+  hipLaunchKernelGGL((few_down_kernel<DT>), dim3((a.H + 7) / 8), dim3(kDownWaves * kWave),
+                     (size_t)a.split * a.pairs * 32, s, a);
   return hipGetLastError();
 }
 
@@ -325,13 +394,11 @@ hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
 
 hipError_t launch_few(const FewArgs& args, hipStream_t s) {
   FewArgs a = args;
-  a.groups = a.pairs > a.E ? a.E : a.pairs;
-  a.split = 1;
+  a.groups = std::min(a.pairs, a.E);
+  a.split = 1;  // parts for every wave of a workgroup of the second product, when experts are few
   while (a.groups * a.split < kDownWaves && 2 * a.split * a.pairs <= kFewMaxPairs) a.split *= 2;
   a.part_lines = ((a.ich + 7) / 8 + a.split - 1) / a.split;
-  if (a.pairs <= kWave)
-    return a.dtype == MOE_F32 ? launch_few_typed<kF32, 1>(a, s) : launch_few_typed<kBF16, 1>(a, s);
-  return a.dtype == MOE_F32 ? launch_few_typed<kF32, 8>(a, s) : launch_few_typed<kBF16, 8>(a, s);
+  return a.dtype == MOE_F32 ? launch_few_typed<kF32>(a, s) : launch_few_typed<kBF16>(a, s);
 }
 
 }  // namespace moe

@@ -192,7 +192,7 @@ struct FewArgs {
   int itype, dtype, act;
   int pairs;              // T*K
   int hch, ich;           // 16-byte chunks of a row of H, of I
-  int groups;             // experts, or pairs when those are fewer (set by the launcher)
+  int groups;             // distinct experts a call can have at most (set by the launcher)
   int split, part_lines;  // parts of the sum over I, 128-byte lines of a part (set by the launcher)
 };
 

@@ -29,11 +29,6 @@ namespace {
 
 // ---- wave-wide reductions (DPP; the total arrives in lane 63) -----------------
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp0(uint32_t v) {  // lanes without a source get 0
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = max(v, dpp0<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8: rows of 16 lanes
   v = max(v, dpp0<0x112, 0xF>(v));
@@ -47,17 +42,17 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 __device__ __forceinline__ uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
 
 template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp0(float v) {
+__device__ __forceinline__ float dpp_float(float v) {
   return __uint_as_float(dpp0<CTRL, ROWS>(__float_as_uint(v)));
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
-  v += dpp0<0x111, 0xF>(v);
-  v += dpp0<0x112, 0xF>(v);
-  v += dpp0<0x114, 0xF>(v);
-  v += dpp0<0x118, 0xF>(v);
-  v += dpp0<0x142, 0xA>(v);
-  v += dpp0<0x143, 0xC>(v);
+  v += dpp_float<0x111, 0xF>(v);
+  v += dpp_float<0x112, 0xF>(v);
+  v += dpp_float<0x114, 0xF>(v);
+  v += dpp_float<0x118, 0xF>(v);
+  v += dpp_float<0x142, 0xA>(v);
+  v += dpp_float<0x143, 0xC>(v);
   return read_lane_f(v, 63);
 }
 
