@@ -212,6 +212,7 @@ struct LowrankArgs {
   int T, E, A, R, r;
   int wch;                   // 16-byte chunks of a wide row
   int dtype;
+  int tiles;                 // expand: tiles of rows a wave takes (set by the launcher)
   bool backward;             // shrink: u = w * raw
 };
 

@@ -78,148 +78,218 @@ __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
 
 // ---- shrink ---------------------------------------------------------------------
 //
-// One workgroup per (tile, slot).  Its waves split the sum over the row in
-// pairs of 64-byte steps and meet in LDS; the first wave adds the parts and
-// writes 16 rows of r float32.
+// One workgroup per (RT tiles of 16 rows, slot).  Its waves split the sum over
+// the row, a 128-byte line of every row each in turn, kDepth lines in flight,
+// and meet in LDS; wave rt adds the parts of tile rt and writes its 16 rows of
+// r float32.  Workgroups start at different lines (and go round): rows a power
+// of two apart, read at the same place at once, meet in a few memory channels.
 constexpr int kShrinkWaves = 8;
 
-template <int DT, int JT>
+template <int DT, int JT, int RT>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs a) {
-  constexpr int kSteps = JT <= 2 ? 4 : 2;  // steps in flight
+  constexpr int kDepth = JT <= 2 ? 2 : 1;
+  constexpr int kMeet = JT * RT <= 4 ? JT : 4 / RT;  // tiles of the rank that meet in LDS together
   __shared__ int off[kMaxOff];
-  constexpr int kMeet = JT < 4 ? JT : 4;  // tiles of the rank that meet in LDS together
-  __shared__ f32x4 part[kShrinkWaves][kMeet][kWave];
-  const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
+  __shared__ f32x4 part[kShrinkWaves][RT][kMeet][kWave];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const int col = lane & 15, q = lane >> 4;
   load_offsets(off, a);
-  const int r0 = blockIdx.x * kTile, r1 = min(r0 + kTile, a.R);
+  const int nch = a.wch, lines = (nch + 7) / 8;
+  const int start = (blockIdx.x + blockIdx.y) * 5 % lines;
+  const uint32_t row_bytes = (uint32_t)nch * 16;
+  const int r0 = blockIdx.x * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
-    const int p = r0 + col;
-    const bool mine = p >= lo && p < hi;
-    const int t = mine ? row_token(a, p) : -1;
+    int t[RT];
+    bool mine[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int p = r0 + rt * kTile + col;
+      mine[rt] = p >= lo && p < hi;
+      t[rt] = row_token(a, mine[rt] ? p : lo);
+    }
     if (e >= a.A) {  // no adapter: u = 0, and no gradient
-      if (wave == 0 && mine) {
-        for (int j = q * 4; j < a.r; j += 16) *reinterpret_cast<f32x4*>(a.u + (size_t)p * a.r + j) = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (a.dot && q == 0 && t >= 0) a.dot[t] = 0.f;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (wave != rt || !mine[rt]) continue;
+        const size_t p = r0 + rt * kTile + col;
+        for (int j = q * 4; j < a.r; j += 16) *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (a.dot && q == 0 && t[rt] >= 0) a.dot[t[rt]] = 0.f;
       }
       return;
     }
-    // columns of other adapters read a row of this one; their results are dropped
-    const int tt = max(row_token(a, mine ? p : lo), 0);
-    const int nch = a.wch;
-    const u32x4* x = static_cast<const u32x4*>(a.rows) + (size_t)tt * nch;
-    const u32x4* bank = static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch;
-    const u32x4* br[JT];
+    // columns of other adapters (and padding) read a row; their results are dropped
+    const u32x4* x[RT];
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) br[jt] = bank + (size_t)min(jt * 16 + col, a.r - 1) * nch;
-    f32x4 acc[JT];
+    for (int rt = 0; rt < RT; ++rt) x[rt] = static_cast<const u32x4*>(a.rows) + (size_t)max(t[rt], 0) * nch;
+    const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
+    const uint32_t b_off = (uint32_t)col * row_bytes + q * 16;
+    u32x4 xv[kDepth][2][RT], bv[kDepth][2][JT];
+    auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
+      const int line = i + start < lines ? i + start : i + start - lines;
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int c0 = wave * 4 * kSteps + q; c0 - q < nch; c0 += kShrinkWaves * 4 * kSteps) {
-      u32x4 xv[kSteps], bv[kSteps][JT];
+      for (int s = 0; s < 2; ++s) {
+        const int c = line * 8 + s * 4 + q;
+        const bool in = i < lines && c < nch;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int c = c0 + 4 * s;
-        xv[s] = u32x4{0u, 0u, 0u, 0u};
-        if (c < nch) xv[s] = x[c];
-#pragma unroll
-        for (int jt = 0; jt < JT; ++jt) {
-          bv[s][jt] = u32x4{0u, 0u, 0u, 0u};
-          if (c < nch) bv[s][jt] = br[jt][c];
+        for (int rt = 0; rt < RT; ++rt) {
+          xv[d][s][rt] = x[rt][in ? c : 0];
+          // the bank's zeros alone would leave NaN where a row holds one
+          if (!in) xv[d][s][rt] = u32x4{0u, 0u, 0u, 0u};
         }
+#pragma unroll
+        for (int jt = 0; jt < JT; ++jt)
+          bv[d][s][jt] = load_rows(bank, in ? b_off + (uint32_t)jt * 16 * row_bytes : kOutside, (uint32_t)(line * 128 + s * 64));
       }
+    };
+    f32x4 acc[RT][JT];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int jt = 0; jt < JT; ++jt) acc[jt] = mma_chunk<DT>(bv[s][jt], xv[s], acc[jt]);
+      for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      fetch(d, wave + d * kShrinkWaves);
+      in_order();
     }
-    const float w = wave == 0 && a.w && t >= 0 ? a.w[t] : 1.f;
-    float dot = 0.f;
+    for (int i = wave; i < lines; i += kShrinkWaves * kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = mma_chunk<DT>(bv[d][s][jt], xv[d][s][rt], acc[rt][jt]);
+        in_order();
+        fetch(d, i + (d + kDepth) * kShrinkWaves);
+        in_order();
+      }
+    }
+    float w = 1.f, dot = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+      if (wave == rt && a.w && t[rt] >= 0) w = a.w[t[rt]];
 #pragma unroll
     for (int first = 0; first < JT; first += kMeet) {
 #pragma unroll
-      for (int m = 0; m < kMeet; ++m) part[wave][m][lane] = acc[first + m];
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int m = 0; m < kMeet; ++m) part[wave][rt][m][lane] = acc[rt][first + m];
       __syncthreads();
-      if (wave == 0) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (wave != rt) continue;
+        const size_t p = r0 + rt * kTile + col;
 #pragma unroll
         for (int m = 0; m < kMeet; ++m) {
-          f32x4 v = part[0][m][lane];
+          f32x4 v = part[0][rt][m][lane];
 #pragma unroll
-          for (int k = 1; k < kShrinkWaves; ++k) v += part[k][m][lane];
+          for (int k = 1; k < kShrinkWaves; ++k) v += part[k][rt][m][lane];
           const int j = (first + m) * 16 + q * 4;
-          if (mine && j < a.r) {
-            if (t < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
-            const size_t at = (size_t)p * a.r + j;
+          if (mine[rt] && j < a.r) {
+            if (t[rt] < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
             if (a.backward) {
               if (a.dot) {
-                const f32x4 u = *reinterpret_cast<const f32x4*>(a.saved + at);
+                const f32x4 u = *reinterpret_cast<const f32x4*>(a.saved + p * a.r + j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dot += v[i] * u[i];
               }
               v *= w;
             }
-            *reinterpret_cast<f32x4*>(a.u + at) = v;
+            *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = v;
           }
         }
       }
       __syncthreads();
     }
-    if (wave == 0 && a.dot) {
+    if (a.dot) {
       dot += __shfl_xor(dot, 16, kWave);
       dot += __shfl_xor(dot, 32, kWave);
-      if (q == 0 && t >= 0) a.dot[t] = dot;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = dot;
     }
   });
 }
 
-// ---- expand ---------------------------------------------------------------------
+// ---- products over the rank or over rows --------------------------------------------
+//
+// Here the summed index is the row index of the wide operand (the bank's rows,
+// or tokens): a lane loads the same chunk of V neighbouring rows, and element i
+// of all of them is its operand for the i-th of V result tiles.  The tile's 16
+// columns are then V columns apart, and a lane ends with V neighbouring
+// elements of four chunks.
 
 // Splits 8 floats into two bfloat16 parts, hi + lo.
 __device__ __forceinline__ void split_bf16(const float (&f)[8], u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    const uint32_t a = f32_to_bf16(f[2 * d]), b = f32_to_bf16(f[2 * d + 1]);
-    hi[d] = a | (b << 16);
-    const float x = f[2 * d] - __uint_as_float(a << 16), y = f[2 * d + 1] - __uint_as_float(b << 16);
+    hi[d] = round_bf16x2(f[2 * d], f[2 * d + 1]);
+    const float x = f[2 * d] - bf16_lo(hi[d]), y = f[2 * d + 1] - bf16_hi(hi[d]);
     // beyond the finite numbers the difference is not a number: no second part
-    lo[d] = f32_to_bf16(x - x == 0.f ? x : 0.f) | (f32_to_bf16(y - y == 0.f ? y : 0.f) << 16);
+    lo[d] = round_bf16x2(x - x == 0.f ? x : 0.f, y - y == 0.f ? y : 0.f);
   }
 }
 
-// Element i of eight rows' chunks, as one operand chunk along the rows.
-__device__ __forceinline__ u32x4 across_rows(const u32x4 (&w)[8], int i) {
-  u32x4 o;
-#pragma unroll
-  for (int d = 0; d < 4; ++d)
-    o[d] = __builtin_amdgcn_perm(w[2 * d + 1][i / 2], w[2 * d][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-  return o;
-}
-
-// acc[i] += (element i of the rows w) . f over a block of the summed index.
+// The operands of V result tiles from the chunks of V rows: for bfloat16
+// element i across the rows, for float32 the rows as they are.
 template <int DT, int V>
-__device__ __forceinline__ void mma_across(const u32x4 (&w)[V], const float (&f)[V], f32x4 (&acc)[V]) {
+__device__ __forceinline__ void across(const u32x4 (&w)[V], u32x4 (&o)[V]) {
   if constexpr (DT == kBF16) {
-    u32x4 hi, lo;
-    split_bf16(f, hi, lo);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const u32x4 a = across_rows(w, i);
-      acc[i] = mma_chunk<kBF16>(a, hi, acc[i]);
-      acc[i] = mma_chunk<kBF16>(a, lo, acc[i]);
-    }
-  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[j][i]), f[j], acc[i], 0, 0, 0);
+      for (int d = 0; d < 4; ++d)
+        o[i][d] = __builtin_amdgcn_perm(w[2 * d + 1][i / 2], w[2 * d][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = w[i];
   }
 }
 
-// One wave per (tile, COLS columns, slot): out of 16 receive rows.
+// The other operand: V floats along the summed index.
+template <int DT>
+struct Factor;
+template <>
+struct Factor<kBF16> {
+  u32x4 hi, lo;
+  __device__ __forceinline__ explicit Factor(const float (&f)[8]) { split_bf16(f, hi, lo); }
+};
+template <>
+struct Factor<kF32> {
+  float f[4];
+  __device__ __forceinline__ explicit Factor(const float (&g)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = g[i];
+  }
+};
+
+// acc[i] += operand i . factor over a block of the summed index.
+template <int DT, int V>
+__device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const Factor<DT>& f, f32x4 (&acc)[V]) {
+  if constexpr (DT == kBF16) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      acc[i] = mma_chunk<kBF16>(o[i], f.hi, acc[i]);
+      acc[i] = mma_chunk<kBF16>(o[i], f.lo, acc[i]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(o[j][i]), f.f[j], acc[i], 0, 0, 0);
+  }
+}
+
+// ---- expand ---------------------------------------------------------------------
+//
+// One wave per (a.tiles tiles of 16 receive rows, COLS columns, slot); it keeps
+// its columns of an adapter's bank in registers from tile to tile.  BLOCKS
+// blocks of KB ranks.
 constexpr int kExpandWaves = 4;
 
-template <int DT>
+template <int DT, int BLOCKS>
 __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(LowrankArgs a) {
   using S = Shape<DT>;
   constexpr int V = S::V;
@@ -230,51 +300,79 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
   const int nch = a.wch;
   const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
   if (c0 >= nch) return;
-  const int r0 = blockIdx.x * kTile, r1 = min(r0 + kTile, a.R);
-  each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
-    const int p = r0 + col;
-    const bool mine = p >= lo && p < hi;
-    const int t = mine ? row_token(a, p) : -1;
-    f32x4 acc[V];
+  const uint32_t row_bytes = (uint32_t)nch * 16;
+  // ranks and columns past the end are outside the bank and read as zeros
+  const int mine_c = c0 + slot_chunk(col);
+  const uint32_t b_off = mine_c < nch ? (uint32_t)mine_c * 16 : kOutside;
+  u32x4 bank[BLOCKS][V];
+  int held = -1;  // the adapter whose bank is held
+  for (int tile = 0; tile < a.tiles; ++tile) {
+    const int r0 = (blockIdx.x * a.tiles + tile) * kTile, r1 = min(r0 + kTile, a.R);
+    if (r0 >= a.R) break;
+    each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
+      const int p = r0 + col;
+      const bool mine = p >= lo && p < hi;
+      const int t = mine ? row_token(a, p) : -1;
+      float f[BLOCKS][V];
+      if (e < a.A) {
+        const float* u = a.u + (size_t)(mine ? p : lo) * a.r;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (e < a.A) {
-      const float w = a.w && t >= 0 ? a.w[t] : 1.f;
-      const int c = c0 + slot_chunk(col);
-      const u32x4* bank = static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch + c;
-      const float* u = a.u + (size_t)(mine ? p : lo) * a.r;
-      for (int j0 = q * V; j0 - q * V < a.r; j0 += S::KB) {
-        u32x4 b[V];
-        float f[V];
+        for (int k = 0; k < BLOCKS; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          b[j] = u32x4{0u, 0u, 0u, 0u};
-          if (j0 < a.r && c < nch) b[j] = bank[(size_t)(j0 + j) * nch];
+          for (int j = 0; j < V; j += 4) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (k * S::KB + q * V < a.r) v = *reinterpret_cast<const f32x4*>(u + k * S::KB + q * V + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[k][j + i] = v[i];
+          }
+        if (e != held) {
+          held = e;
+          const auto rows = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
+#pragma unroll
+          for (int k = 0; k < BLOCKS; ++k) {
+            u32x4 b[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const int jj = k * S::KB + q * V + j;
+              b[j] = load_rows(rows, jj < a.r ? b_off + (uint32_t)jj * row_bytes : kOutside, 0);
+            }
+            across<DT, V>(b, bank[k]);
+          }
         }
+      }
+      u32x4 base[4];
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
-          if (j0 < a.r) v = *reinterpret_cast<const f32x4*>(u + j0 + j);
+      for (int s = 0; s < 4; ++s) {
+        base[s] = u32x4{0u, 0u, 0u, 0u};
+        const int c = c0 + s * 4 + q;
+        if (a.base && t >= 0 && c < nch) base[s] = static_cast<const u32x4*>(a.base)[(size_t)t * nch + c];
+      }
+      f32x4 acc[V];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[j + i] = v[i] * w;
+      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (e < a.A) {
+        const float w = a.w && t >= 0 ? a.w[t] : 1.f;
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[k][j] *= w;
+          mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
         }
-        mma_across<DT, V>(b, f, acc);
       }
-    }
-    if (t < 0) return;
+      if (t < 0) return;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int c = c0 + s * 4 + q;
-      if (c < nch) {
-        const size_t at = (size_t)t * nch + c;
-        float o[V];
-        if (a.base) unpack<DT>(static_cast<const u32x4*>(a.base)[at], o);
+      for (int s = 0; s < 4; ++s) {
+        const int c = c0 + s * 4 + q;
+        if (c < nch) {
+          float o[V];
+          unpack<DT>(base[s], o);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = a.base ? o[i] + acc[i][s] : acc[i][s];
-        static_cast<u32x4*>(a.out)[at] = pack<DT>(o);
+          for (int i = 0; i < V; ++i) o[i] = a.base ? o[i] + acc[i][s] : acc[i][s];
+          static_cast<u32x4*>(a.out)[(size_t)t * nch + c] = pack<DT>(o);
+        }
       }
-    }
-  });
+    });
+  }
 }
 
 // ---- gradients of the adapters ---------------------------------------------------
@@ -282,8 +380,9 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
 // grad[e][j][c] = sum over the adapter's rows p of coef[p][j] rows[t_p][c],
 // coef = u (times w for grad_B).  One workgroup per (COLS columns, adapter, 16
 // JT of the rank): its waves take the adapter's rows in turn, each a block of
-// KB rows at a time, and meet in LDS.  An adapter without rows gets zeros.
-constexpr int kWgradWaves = 4;
+// KB rows at a time with the next block's rows on their way, and meet in LDS.
+// An adapter without rows gets zeros.
+constexpr int kWgradWaves = 8;
 
 template <int DT, int JT>
 __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a) {
@@ -294,35 +393,63 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   const int col = lane & 15, q = lane >> 4;
   const int e = blockIdx.y;
   const int nch = a.wch;
-  const int c0 = blockIdx.x * 16;
-  const int c = c0 + slot_chunk(col);
-  const int j0 = blockIdx.z * JT * 16;
+  const int parts = (a.r + 16 * JT - 1) / (16 * JT);
+  const int c0 = blockIdx.x / parts * 16;
+  const int j0 = blockIdx.x % parts * JT * 16;
+  const int c = min(c0 + slot_chunk(col), nch - 1);  // chunks past the end repeat the last and are not stored
   const int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
   f32x4 acc[JT][V];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[jt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int p0 = lo + wave * S::KB; p0 < hi; p0 += kWgradWaves * S::KB) {
-    u32x4 x[V];
-    float w[V];
-    int pp[V];
+  u32x4 x[V];
+  int t[V], next_t[V];
+  auto tokens = [&](int p0, int (&to)[V]) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int p = p0 + q * V + k;
-      const int t = p < hi ? row_token(a, p) : -1;
-      pp[k] = t >= 0 ? p : -1;
-      x[k] = u32x4{0u, 0u, 0u, 0u};
-      if (t >= 0 && c < nch) x[k] = static_cast<const u32x4*>(a.rows)[(size_t)t * nch + c];
-      w[k] = a.w && t >= 0 ? a.w[t] : 1.f;
+      const int v = a.recv_token[min(p, a.R - 1)];
+      to[k] = p < hi && (unsigned)v < (unsigned)a.T ? v : -1;
     }
+  };
+  constexpr int kStep = kWgradWaves * S::KB;
+  int p0 = lo + wave * S::KB;
+  if (p0 < hi) {
+    tokens(p0, t);
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(t[k], 0) * nch + c];
+    tokens(p0 + kStep, next_t);
+  }
+  for (; p0 < hi; p0 += kStep) {
+    float f[JT][V], w[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float* u = a.u + (size_t)min(p0 + q * V + k, hi - 1) * a.r;
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) f[jt][k] = u[min(j0 + jt * 16 + col, a.r - 1)];
+      w[k] = a.w ? a.w[max(t[k], 0)] : 1.f;
+    }
+    u32x4 o[V];
+    {
+      u32x4 z[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) z[k] = t[k] >= 0 ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
+      across<DT, V>(z, o);
+    }
+    bool there[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      there[k] = t[k] >= 0;
+      t[k] = next_t[k];
+      x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(t[k], 0) * nch + c];
+    }
+    tokens(p0 + 2 * kStep, next_t);
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
-      const int j = j0 + jt * 16 + col;
-      float f[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = pp[k] >= 0 && j < a.r ? a.u[(size_t)pp[k] * a.r + j] * w[k] : 0.f;
-      mma_across<DT, V>(x, f, acc[jt]);
+      for (int k = 0; k < V; ++k) f[jt][k] = there[k] ? f[jt][k] * w[k] : 0.f;
+      mma_across<DT, V>(o, Factor<DT>(f[jt]), acc[jt]);
     }
   }
 #pragma unroll
@@ -332,17 +459,16 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
     for (int i = 0; i < V; ++i) part[wave][i][lane] = acc[jt][i];
     __syncthreads();
     const int j = j0 + jt * 16 + col;
-    // wave s stores the chunks of quad s
-    for (int s = wave; s < 4; s += kWgradWaves) {
+    if (wave < 4) {  // wave s stores the chunks of quad s
       float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float* f = reinterpret_cast<const float*>(&part[0][i][lane]) + s;
+        const float* f = reinterpret_cast<const float*>(&part[0][i][lane]) + wave;
         o[i] = f[0];
 #pragma unroll
         for (int k = 1; k < kWgradWaves; ++k) o[i] += f[(size_t)k * V * kWave * 4];
       }
-      const int cc = c0 + s * 4 + q;
+      const int cc = c0 + wave * 4 + q;
       if (j < a.r && cc < nch) static_cast<u32x4*>(a.out)[((size_t)e * a.r + j) * nch + cc] = pack<DT>(o);
     }
   }
@@ -363,28 +489,49 @@ int slots_for(int64_t workgroups, int E) {  // adapters of a tile side by side w
 }  // namespace
 
 hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
-  const int tiles = (a.R + kTile - 1) / kTile;
+  // two tiles a workgroup, which halves what is read of the banks, when that
+  // still leaves a workgroup for every CU
+  const int rt = a.r <= 64 && a.R >= 2 * kTile * 256 ? 2 : 1;
+  const int tiles = (a.R + kTile * rt - 1) / (kTile * rt);
   const dim3 grid(tiles, slots_for(tiles, a.E)), block(kShrinkWaves * kWave);
-#define MOE_SHRINK(J)                                                                                  \
+#define MOE_SHRINK(J, T)                                                                               \
   return launched([&] {                                                                                \
-    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J>), grid, block, 0, s, a);        \
-    else hipLaunchKernelGGL((shrink_kernel<kBF16, J>), grid, block, 0, s, a);                          \
+    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T>), grid, block, 0, s, a);     \
+    else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T>), grid, block, 0, s, a);                       \
   })
-  if (a.r <= 16) MOE_SHRINK(1);
-  if (a.r <= 32) MOE_SHRINK(2);
-  if (a.r <= 64) MOE_SHRINK(4);
-  MOE_SHRINK(8);
+  if (rt == 2) {
+    if (a.r <= 16) MOE_SHRINK(1, 2);
+    if (a.r <= 32) MOE_SHRINK(2, 2);
+    MOE_SHRINK(4, 2);
+  }
+  if (a.r <= 16) MOE_SHRINK(1, 1);
+  if (a.r <= 32) MOE_SHRINK(2, 1);
+  if (a.r <= 64) MOE_SHRINK(4, 1);
+  MOE_SHRINK(8, 1);
 #undef MOE_SHRINK
 }
 
-hipError_t launch_lowrank_expand(const LowrankArgs& a, hipStream_t s) {
+hipError_t launch_lowrank_expand(const LowrankArgs& args, hipStream_t s) {
+  LowrankArgs a = args;
   const int tiles = (a.R + kTile - 1) / kTile;
   const int cols = (a.wch + 16 * kExpandWaves - 1) / (16 * kExpandWaves);
-  const dim3 grid(tiles, cols, slots_for((int64_t)tiles * cols, a.E)), block(kExpandWaves * kWave);
-  return launched([&] {
-    if (a.dtype == MOE_F32) hipLaunchKernelGGL((expand_lowrank_kernel<kF32>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((expand_lowrank_kernel<kBF16>), grid, block, 0, s, a);
-  });
+  // up to 4 tiles a wave while there are four workgroups a CU
+  a.tiles = 1;
+  while (a.tiles < 4 && (int64_t)tiles * cols >= 2 * a.tiles * 1024) a.tiles *= 2;
+  const int blocks = (tiles + a.tiles - 1) / a.tiles;
+  const dim3 grid(blocks, cols, a.tiles > 1 ? 1 : slots_for((int64_t)tiles * cols, a.E)), block(kExpandWaves * kWave);
+#define MOE_EXPAND(D, B) \
+  return launched([&] { hipLaunchKernelGGL((expand_lowrank_kernel<D, B>), grid, block, 0, s, a); })
+  if (a.dtype == MOE_F32) {
+    if (a.r <= 16) MOE_EXPAND(kF32, 1);
+    if (a.r <= 32) MOE_EXPAND(kF32, 2);
+    if (a.r <= 64) MOE_EXPAND(kF32, 4);
+    MOE_EXPAND(kF32, 8);
+  }
+  if (a.r <= 32) MOE_EXPAND(kBF16, 1);
+  if (a.r <= 64) MOE_EXPAND(kBF16, 2);
+  MOE_EXPAND(kBF16, 4);
+#undef MOE_EXPAND
 }
 
 hipError_t launch_lowrank_wgrad(const LowrankArgs& a, hipStream_t s) {
@@ -392,13 +539,12 @@ hipError_t launch_lowrank_wgrad(const LowrankArgs& a, hipStream_t s) {
   const int cols = (a.wch + 15) / 16;
 #define MOE_WGRAD(J)                                                                                   \
   return launched([&] {                                                                                \
-    const dim3 grid(cols, a.A, (a.r + 16 * J - 1) / (16 * J));                                         \
+    const dim3 grid(cols * ((a.r + 16 * J - 1) / (16 * J)), a.A);                                      \
     if (a.dtype == MOE_F32) hipLaunchKernelGGL((wgrad_kernel<kF32, J>), grid, block, 0, s, a);         \
     else hipLaunchKernelGGL((wgrad_kernel<kBF16, J>), grid, block, 0, s, a);                           \
   })
   if (a.r <= 16) MOE_WGRAD(1);
-  if (a.r <= 32) MOE_WGRAD(2);
-  MOE_WGRAD(4);
+  MOE_WGRAD(2);
 #undef MOE_WGRAD
 }
 

@@ -31,6 +31,14 @@ __device__ __forceinline__ f32x4 mma_chunk(const u32x4 a, const u32x4 b, f32x4 a
   }
 }
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two floats as bfloat16, nearest even (one instruction).
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // Rows in memory as a buffer of `bytes` from p (uniform over the wave): a load
 // whose offset is past the end gives zeros and touches no memory, so the ends
 // of rows and tiles need no branches.  Offsets are 32 bits; kOutside lies past

@@ -111,6 +111,14 @@ def test_float32_chunks_of_four(T, A, r, H, N):
     check(ids, E, d)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,A,r,H,N", [(8200, 5, 16, 40, 4104), (8209, 700, 40, 264, 72), (9000, 3, 24, 1032, 2056)])
+def test_large_batches(dtype, T, A, r, H, N):
+    """Several tiles a workgroup or wave: tiles that adapters share among them."""
+    ids, E, d = make(T, A, r, H, N, dtype, T)
+    check(ids, E, d)
+
+
 @pytest.mark.parametrize("pad", [2, 16, 100])
 def test_padded_layouts(pad):
     ids, E, d = make(150, 6, 16, 72, 136, BF16, pad, E=9)
