@@ -83,29 +83,33 @@ __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
 // and meet in LDS; wave rt adds the parts of tile rt and writes its 16 rows of
 // r float32.  Workgroups start at different lines (and go round): rows a power
 // of two apart, read at the same place at once, meet in a few memory channels.
+// FAR: the wide rows reach past what a buffer's 32-bit offsets do (2 GiB).
 constexpr int kShrinkWaves = 8;
 
-template <int DT, int JT, int RT>
+template <int DT, int JT, int RT, bool FAR>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs a) {
-  constexpr int kDepth = JT <= 2 ? 2 : 1;
+  // lines in flight: about 128 registers of them; a call has one or two
+  // workgroups a CU, so each has to keep the memory busy by itself
+  constexpr int kDepth = JT + RT <= 4 ? 4 : JT + RT <= 6 ? 3 : 2;
   constexpr int kMeet = JT * RT <= 4 ? JT : 4 / RT;  // tiles of the rank that meet in LDS together
   __shared__ int off[kMaxOff];
   __shared__ f32x4 part[kShrinkWaves][RT][kMeet][kWave];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const int col = lane & 15, q = lane >> 4;
-  load_offsets(off, a);
   const int nch = a.wch, lines = (nch + 7) / 8;
   const int start = (blockIdx.x + blockIdx.y) * 5 % lines;
   const uint32_t row_bytes = (uint32_t)nch * 16;
   const int r0 = blockIdx.x * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
+  int t[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + col);
+  load_offsets(off, a);
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
-    int t[RT];
     bool mine[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int p = r0 + rt * kTile + col;
       mine[rt] = p >= lo && p < hi;
-      t[rt] = row_token(a, mine[rt] ? p : lo);
     }
     if (e >= a.A) {  // no adapter: u = 0, and no gradient
 #pragma unroll
@@ -117,10 +121,16 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
       }
       return;
     }
-    // columns of other adapters (and padding) read a row; their results are dropped
+    // columns of other adapters read their rows (padding the first one); the
+    // results are dropped
     const u32x4* x[RT];
+    uint32_t x_off[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) x[rt] = static_cast<const u32x4*>(a.rows) + (size_t)max(t[rt], 0) * nch;
+    for (int rt = 0; rt < RT; ++rt) {
+      x[rt] = static_cast<const u32x4*>(a.rows) + (size_t)max(t[rt], 0) * nch;
+      x_off[rt] = (uint32_t)max(t[rt], 0) * row_bytes + q * 16;
+    }
+    const auto wide = make_rows(a.rows, FAR ? 0 : (size_t)a.T * row_bytes);
     const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
     const uint32_t b_off = (uint32_t)col * row_bytes + q * 16;
     u32x4 xv[kDepth][2][RT], bv[kDepth][2][JT];
@@ -130,15 +140,20 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
       for (int s = 0; s < 2; ++s) {
         const int c = line * 8 + s * 4 + q;
         const bool in = i < lines && c < nch;
+        const uint32_t at = (uint32_t)(line * 128 + s * 64);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          xv[d][s][rt] = x[rt][in ? c : 0];
-          // the bank's zeros alone would leave NaN where a row holds one
-          if (!in) xv[d][s][rt] = u32x4{0u, 0u, 0u, 0u};
+          if constexpr (FAR) {
+            xv[d][s][rt] = x[rt][in ? c : 0];
+            // the bank's zeros alone would leave NaN where a row holds one
+            if (!in) xv[d][s][rt] = u32x4{0u, 0u, 0u, 0u};
+          } else {
+            xv[d][s][rt] = load_rows(wide, in ? x_off[rt] : kOutside, at);
+          }
         }
 #pragma unroll
         for (int jt = 0; jt < JT; ++jt)
-          bv[d][s][jt] = load_rows(bank, in ? b_off + (uint32_t)jt * 16 * row_bytes : kOutside, (uint32_t)(line * 128 + s * 64));
+          bv[d][s][jt] = load_rows(bank, in ? b_off + (uint32_t)jt * 16 * row_bytes : kOutside, at);
       }
     };
     f32x4 acc[RT][JT];
@@ -210,6 +225,15 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
         if (wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = dot;
     }
   });
+}
+
+// A chunk of V floats rounded to the element type.
+template <int DT, int V>
+__device__ __forceinline__ u32x4 pack_rows(const float (&f)[V]) {
+  u32x4 c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = DT == kF32 ? __float_as_uint(f[i]) : round_bf16x2(f[2 * i % V], f[(2 * i + 1) % V]);
+  return c;
 }
 
 // ---- products over the rank or over rows --------------------------------------------
@@ -285,8 +309,8 @@ __device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const Factor<DT>
 // ---- expand ---------------------------------------------------------------------
 //
 // One wave per (a.tiles tiles of 16 receive rows, COLS columns, slot); it keeps
-// its columns of an adapter's bank in registers from tile to tile.  BLOCKS
-// blocks of KB ranks.
+// its columns of an adapter's bank in registers from tile to tile, and has the
+// next tile's rows of base on their way.  BLOCKS blocks of KB ranks.
 constexpr int kExpandWaves = 4;
 
 template <int DT, int BLOCKS>
@@ -296,35 +320,59 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
   __shared__ int off[kMaxOff];
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
   const int col = lane & 15, q = lane >> 4;
-  load_offsets(off, a);
   const int nch = a.wch;
   const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
-  if (c0 >= nch) return;
   const uint32_t row_bytes = (uint32_t)nch * 16;
   // ranks and columns past the end are outside the bank and read as zeros
   const int mine_c = c0 + slot_chunk(col);
   const uint32_t b_off = mine_c < nch ? (uint32_t)mine_c * 16 : kOutside;
+
+  // a tile's rows: token, weight and the chunks of base
+  struct Rows {
+    int t;
+    float w;
+    u32x4 base[4];
+  } now, next;
+  auto fetch = [&](Rows& r, int t) {
+    r.t = t;
+    r.w = a.w ? a.w[max(t, 0)] : 1.f;
+    if (a.base) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        r.base[s] = static_cast<const u32x4*>(a.base)[(size_t)max(t, 0) * nch + min(c0 + s * 4 + q, nch - 1)];
+    }
+  };
+  int tile = blockIdx.x * a.tiles;
+  const int tile_end = min(tile + a.tiles, (a.R + kTile - 1) / kTile);
+  int next_t = row_token(a, tile * kTile + col);
+  load_offsets(off, a);
+  if (c0 >= nch) return;
+  fetch(next, next_t);
+  next_t = row_token(a, (tile + 1) * kTile + col);
+
   u32x4 bank[BLOCKS][V];
   int held = -1;  // the adapter whose bank is held
-  for (int tile = 0; tile < a.tiles; ++tile) {
-    const int r0 = (blockIdx.x * a.tiles + tile) * kTile, r1 = min(r0 + kTile, a.R);
-    if (r0 >= a.R) break;
+  for (; tile < tile_end; ++tile) {
+    now = next;
+    const int r0 = tile * kTile, r1 = min(r0 + kTile, a.R);
+    float f[BLOCKS][V];
+    const float* u = a.u + (size_t)min(r0 + col, a.R - 1) * a.r;
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const int jj = k * S::KB + q * V + j;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(u + (jj < a.r ? jj : 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[k][j + i] = jj < a.r ? v[i] * now.w : 0.f;
+      }
+    if (tile + 1 < tile_end) fetch(next, next_t);
+    next_t = row_token(a, (tile + 2) * kTile + col);
     each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
-      const int p = r0 + col;
-      const bool mine = p >= lo && p < hi;
-      const int t = mine ? row_token(a, p) : -1;
-      float f[BLOCKS][V];
+      f32x4 acc[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (e < a.A) {
-        const float* u = a.u + (size_t)(mine ? p : lo) * a.r;
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k)
-#pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (k * S::KB + q * V < a.r) v = *reinterpret_cast<const f32x4*>(u + k * S::KB + q * V + j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[k][j + i] = v[i];
-          }
         if (e != held) {
           held = e;
           const auto rows = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
@@ -339,36 +387,21 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
             across<DT, V>(b, bank[k]);
           }
         }
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
       }
-      u32x4 base[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        base[s] = u32x4{0u, 0u, 0u, 0u};
-        const int c = c0 + s * 4 + q;
-        if (a.base && t >= 0 && c < nch) base[s] = static_cast<const u32x4*>(a.base)[(size_t)t * nch + c];
-      }
-      f32x4 acc[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (e < a.A) {
-        const float w = a.w && t >= 0 ? a.w[t] : 1.f;
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[k][j] *= w;
-          mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
-        }
-      }
-      if (t < 0) return;
+      // the columns of other adapters' rows are dropped
+      const int p = r0 + col;
+      if (now.t < 0 || p < lo || p >= hi) return;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int c = c0 + s * 4 + q;
         if (c < nch) {
           float o[V];
-          unpack<DT>(base[s], o);
+          if (a.base) unpack<DT>(now.base[s], o);
 #pragma unroll
           for (int i = 0; i < V; ++i) o[i] = a.base ? o[i] + acc[i][s] : acc[i][s];
-          static_cast<u32x4*>(a.out)[(size_t)t * nch + c] = pack<DT>(o);
+          static_cast<u32x4*>(a.out)[(size_t)now.t * nch + c] = pack_rows<DT>(o);
         }
       }
     });
@@ -469,7 +502,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
         for (int k = 1; k < kWgradWaves; ++k) o[i] += f[(size_t)k * V * kWave * 4];
       }
       const int cc = c0 + wave * 4 + q;
-      if (j < a.r && cc < nch) static_cast<u32x4*>(a.out)[((size_t)e * a.r + j) * nch + cc] = pack<DT>(o);
+      if (j < a.r && cc < nch) static_cast<u32x4*>(a.out)[((size_t)e * a.r + j) * nch + cc] = pack_rows<DT>(o);
     }
   }
 }
@@ -491,23 +524,28 @@ int slots_for(int64_t workgroups, int E) {  // adapters of a tile side by side w
 hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
   // two tiles a workgroup, which halves what is read of the banks, when that
   // still leaves a workgroup for every CU
-  const int rt = a.r <= 64 && a.R >= 2 * kTile * 256 ? 2 : 1;
+  const bool far = (int64_t)a.T * a.wch * 16 >= (int64_t(1) << 31);
+  const int rt = !far && a.r <= 64 && a.R >= 2 * kTile * 256 ? 2 : 1;
   const int tiles = (a.R + kTile * rt - 1) / (kTile * rt);
   const dim3 grid(tiles, slots_for(tiles, a.E)), block(kShrinkWaves * kWave);
-#define MOE_SHRINK(J, T)                                                                               \
+#define MOE_SHRINK(J, T, F)                                                                            \
   return launched([&] {                                                                                \
-    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T>), grid, block, 0, s, a);     \
-    else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T>), grid, block, 0, s, a);                       \
+    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T, F>), grid, block, 0, s, a);  \
+    else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T, F>), grid, block, 0, s, a);                    \
   })
-  if (rt == 2) {
-    if (a.r <= 16) MOE_SHRINK(1, 2);
-    if (a.r <= 32) MOE_SHRINK(2, 2);
-    MOE_SHRINK(4, 2);
+  if (far) {
+    if (a.r <= 32) MOE_SHRINK(2, 1, true);
+    MOE_SHRINK(8, 1, true);
   }
-  if (a.r <= 16) MOE_SHRINK(1, 1);
-  if (a.r <= 32) MOE_SHRINK(2, 1);
-  if (a.r <= 64) MOE_SHRINK(4, 1);
-  MOE_SHRINK(8, 1);
+  if (rt == 2) {
+    if (a.r <= 16) MOE_SHRINK(1, 2, false);
+    if (a.r <= 32) MOE_SHRINK(2, 2, false);
+    MOE_SHRINK(4, 2, false);
+  }
+  if (a.r <= 16) MOE_SHRINK(1, 1, false);
+  if (a.r <= 32) MOE_SHRINK(2, 1, false);
+  if (a.r <= 64) MOE_SHRINK(4, 1, false);
+  MOE_SHRINK(8, 1, false);
 #undef MOE_SHRINK
 }
 
