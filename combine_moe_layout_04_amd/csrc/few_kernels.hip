@@ -5,9 +5,9 @@
 //
 // A decode batch reads far more weight bytes than it computes on: the chosen
 // experts' weights, 3 H I elements each, are the floor, and each is read once
-// per call.  The matrix cores take 8 weight rows against up to 8 of the
-// expert's tokens a tile; 1 KiB of weights costs 16 cycles of one matrix core
-// for bfloat16, about a twenty-fifth of what the bytes cost.
+// per call.  The matrix cores take 4 weight rows against 4 of the expert's
+// tokens a tile; 1 KiB of weights costs 16 cycles of one matrix core for
+// bfloat16, about a twenty-fifth of what the bytes cost.
 //
 // No layout runs before: a call has at most 512 pairs, and every workgroup
 // groups them by expert in its LDS as it starts.  A workgroup of the first
@@ -90,68 +90,29 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return 0.5f * g * (1.f + tanhf(y)) * u;
 }
 
-// A weight tile is 8 rows by one 128-byte line of each, one load instruction
-// of whole lines.  As an operand its 16 rows are the 8 rows twice, with the
-// first and the second half of the line; the 16 columns of the other operand
-// are 8 tokens twice likewise.  Two diagonal quarters of the result are the
-// halves' sums over the line, the other two are not used: the matrix cores
-// have far more to spare than the memory has.  (Streaming 0.8 GB of rows of 4
-// KiB on MI355X: 16 rows by 64 bytes an instruction 6.2 TB/s, whole lines
-// non-temporal 6.9 TB/s.)
-struct Lane {
-  int row, half, q;  // row (or token) of the tile, half of its line, chunk of the half
-  __device__ __forceinline__ Lane() : row(lane_id() & 7), half((lane_id() >> 3) & 1), q(lane_id() >> 4) {}
-  __device__ __forceinline__ int chunk() const { return half * 4 + q; }
-};
-
-// Rows 4q..4q+3 (q < 2) of column `row` in the lanes of the first half: the
-// second half's quarter (rows 8.., columns 8..) joins the first's.
-__device__ __forceinline__ f32x4 join_halves(f32x4 acc) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] += __shfl(acc[i], lane_id() + 40, kWave);
-  return acc;
-}
-
-template <int DT>
-__device__ __forceinline__ void store_act(const FewArgs& a, int pair, int i0, f32x4 g, f32x4 u) {
-  const size_t row = (size_t)pair * a.I;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = i0 + k;
-    if (i < a.I) {
-      const float v = gated(g[k], u[k], a.act);
-      // act is rounded to the element type: the second product's operand, as
-      // between two separate products
-      if constexpr (DT == kF32) static_cast<float*>(a.mid)[row + i] = v;
-      else static_cast<uint16_t*>(a.mid)[row + i] = (uint16_t)f32_to_bf16(v);
-    }
-  }
-}
-
-// act, in items of (expert, 8 columns).  A workgroup's waves take the lines of
-// the item's rows in turn and meet in LDS; they work in rounds of kDepth lines
-// each and ask for the next round's while they multiply this one's, from item
-// to item too.  NT tiles of 8 of the expert's pairs at a time.
+// act, in items of (expert, 8 columns).  A workgroup's waves take the 256-byte
+// lines of the item's rows in turn and meet in LDS; they work in rounds of
+// kDepth lines each and ask for the next round's while they multiply this
+// one's, from item to item too.  NT tiles of 4 of the expert's pairs at a time.
 //
-// Two things decide how near to the memory's rate this comes (64 tokens, 126
-// experts of 768 columns and rows of 4 KiB, 0.79 GB):
+// What decides how near to the memory's rate this comes (64 tokens, 126 experts
+// of 768 columns and rows of 4 KiB, 0.79 GB):
+//   - the order of lanes in a load (mfma.h): BEFORE -> AFTER us;
 //   - workgroup b takes items b, b + grid, ..., so that all of them together
 //     move through a narrow window of the weights: 164 us with even runs of
 //     neighbouring items, 140 us in steps;
 //   - each workgroup starts at another line of its rows (and goes round): rows
 //     4 KiB apart read at the same place at the same time meet in a few memory
-//     channels.  140 -> 134 us.  The sum's order depends on the item alone
-//     through its workgroup, so it is the same in every run.
-// More lines in flight (8 a wave), fewer, and other numbers of workgroups and
-// waves were all within 132 to 156 us.
+//     channels.  140 -> 134 us.  The order of the sum depends on the item
+//     through its workgroup alone, so it is the same in every run.
 constexpr int kUpWaves = 4;
 constexpr int kUpGroups = 1024;  // workgroups at most: four a CU
 
 template <int DT, int NT>
 __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
-  constexpr int kDepth = NT == 1 ? 4 : 2;
+  constexpr int kDepth = NT <= 2 ? 3 : 1;
   __shared__ Groups groups;
-  __shared__ f32x4 part[kUpWaves][NT][2][kWave / 4];
+  __shared__ float part[kUpWaves][NT][2][2][16];  // wave, tile of pairs, tile of rows, gate or up, row * 4 + pair
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
@@ -162,13 +123,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 
   const int nch = a.hch;  // chunks of an x or w13 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
-  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
-  const int lines = (nch + 7) / 8;
+  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
+  const int lines = (nch + 15) / 16;
   const int rounds = (lines + kUpWaves * kDepth - 1) / (kUpWaves * kDepth);
-  const int start = blockIdx.x * 4 % lines;
+  const int start = blockIdx.x * 2 % lines;
   const auto xs = make_rows(a.x, (size_t)a.T * row_bytes);
 
-  u32x4 wg[kDepth], wu[kDepth], b[kDepth][NT];
+  u32x4 wg[kDepth][2], wu[kDepth][2], b[kDepth][NT];
   uint32_t x_off[NT];
   auto gate = make_rows(a.w13, 0), up = gate;
   int slab = 0, n = 0;  // of the item being fetched
@@ -188,16 +149,19 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
   auto tokens = [&](int first) {  // columns past the last pair repeat it and are not stored
 #pragma unroll
     for (int c = 0; c < NT; ++c)
-      x_off[c] = (uint32_t)(list[min(first + c * 8 + at.row, n - 1)] / a.K) * row_bytes + at.chunk() * 16;
+      x_off[c] = (uint32_t)(list[min(first + c * 4 + at.row, n - 1)] / a.K) * row_bytes + at.chunk * 16;
   };
   auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
     const int line = i + start < lines ? i + start : i + start - lines;
-    const bool in = i < lines && line * 8 + at.chunk() < nch;
-    const uint32_t off = in ? w_off : kOutside;
-    wg[d] = load_rows<true>(gate, off, (uint32_t)line * 128);
-    wu[d] = load_rows<true>(up, off, (uint32_t)line * 128);
+    const bool in = i < lines && line * 16 + at.chunk < nch;
 #pragma unroll
-    for (int c = 0; c < NT; ++c) b[d][c] = load_rows(xs, in ? x_off[c] : kOutside, (uint32_t)line * 128);
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t off = in ? w_off + r * 4 * row_bytes : kOutside;
+      wg[d][r] = load_rows<true>(gate, off, (uint32_t)line * 256);
+      wu[d][r] = load_rows<true>(up, off, (uint32_t)line * 256);
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c) b[d][c] = load_rows(xs, in ? x_off[c] : kOutside, (uint32_t)line * 256);
   };
 
   fetch_item();
@@ -207,9 +171,11 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
     fetch(d, wave + d * kUpWaves);
     in_order();
   }
-  f32x4 g[NT], u[NT];
+  f32x4 g[NT][2], u[NT][2];
 #pragma unroll
-  for (int c = 0; c < NT; ++c) g[c] = u[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) g[c][r] = u[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int first = 0, round = 0; item < items;) {
     const int this_i = slab * 8, this_n = n, this_first = first;
     const uint16_t* this_list = list;
@@ -217,7 +183,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
     if (++round == rounds) {
       round = 0;
       next = wave;
-      first += 8 * NT;
+      first += 4 * NT;
       if (first >= n) {
         first = 0;
         item += gridDim.x;
@@ -229,10 +195,12 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        g[c] = mma_chunk<DT>(wg[d], b[d][c], g[c]);
-        u[c] = mma_chunk<DT>(wu[d], b[d][c], u[c]);
-      }
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          g[c][r] = mma_chunk<DT>(wg[d][r], b[d][c], g[c][r]);
+          u[c][r] = mma_chunk<DT>(wu[d][r], b[d][c], u[c][r]);
+        }
       in_order();
       fetch(d, next + d * kUpWaves);
       in_order();
@@ -240,25 +208,36 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
     if (round == 0) {
       __syncthreads();  // the last results have been read
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        const f32x4 sg = join_halves(g[c]), su = join_halves(u[c]);
-        g[c] = u[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (at.half == 0 && at.q < 2) {
-          part[wave][c][0][at.q * 8 + at.row] = sg;
-          part[wave][c][1][at.q * 8 + at.row] = su;
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float sg = join_parts(g[c][r]), su = join_parts(u[c][r]);
+          g[c][r] = u[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if ((lane_id() & 3) == 0) {
+            part[wave][c][r][0][at.first() * 4 + at.second()] = sg;
+            part[wave][c][r][1][at.first() * 4 + at.second()] = su;
+          }
         }
-      }
       __syncthreads();
-      if (threadIdx.x < NT * 16) {  // 16 lanes per tile: quad and pair
-        const int slot = threadIdx.x & 15, c = threadIdx.x >> 4;
-        f32x4 sg = part[0][c][0][slot], su = part[0][c][1][slot];
+      for (int i = threadIdx.x; i < NT * 32; i += kUpWaves * kWave) {
+        // neighbouring threads: neighbouring columns of one pair
+        const int column = i & 7, t = (i >> 3) & 3, c = i >> 5;
+        const int slot = (column & 3) * 4 + t;
+        float sg = part[0][c][column >> 2][0][slot], su = part[0][c][column >> 2][1][slot];
 #pragma unroll
         for (int v = 1; v < kUpWaves; ++v) {
-          sg += part[v][c][0][slot];
-          su += part[v][c][1][slot];
+          sg += part[v][c][column >> 2][0][slot];
+          su += part[v][c][column >> 2][1][slot];
         }
-        const int pos = this_first + c * 8 + (slot & 7);
-        if (pos < this_n) store_act<DT>(a, this_list[pos], this_i + (slot >> 3) * 4, sg, su);
+        const int pos = this_first + c * 4 + t;
+        if (pos < this_n && this_i + column < a.I) {
+          const float v = gated(sg, su, a.act);
+          const size_t to = (size_t)this_list[pos] * a.I + this_i + column;
+          // act is rounded to the element type: the second product's operand,
+          // as between two separate products
+          if constexpr (DT == kF32) static_cast<float*>(a.mid)[to] = v;
+          else static_cast<uint16_t*>(a.mid)[to] = (uint16_t)f32_to_bf16(v);
+        }
       }
     }
   }
@@ -270,13 +249,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 // item or the next) under way during this one.
 constexpr int kDownWaves = 16;
 
-template <int DT>
+template <int DT, int NT>
 __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
-  constexpr int kDepth = 3;
+  constexpr int kDepth = NT <= 2 ? 3 : 1;
   __shared__ Groups groups;
   __shared__ float weight[kFewMaxPairs];
   __shared__ uint8_t here[kFewMaxPairs];
-  extern __shared__ f32x4 y[];  // [split][pairs][2]: 8 columns as two quads
+  extern __shared__ float y[];  // [split][pairs][8]
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
@@ -293,13 +272,13 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   const int h0 = blockIdx.x * 8;
   const size_t tile_bytes = (size_t)min(8, a.H - h0) * row_bytes;
   const auto mid = make_rows(a.mid, (size_t)a.pairs * row_bytes);
-  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk() * 16;
-  const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 7) / 8);
+  const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
+  const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 15) / 16);
   const int rounds = (a.part_lines + kDepth - 1) / kDepth;
 
-  u32x4 w[kDepth], b[kDepth];
+  u32x4 w[kDepth][2], b[kDepth][NT];
   auto w2 = make_rows(a.w2, 0);
-  uint32_t m_off = 0;
+  uint32_t m_off[NT];
   int n = 0;  // pairs of the fetched item
   const uint16_t* list = groups.pairs;
   auto item = [&](int j) {
@@ -309,12 +288,17 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     w2 = make_rows(static_cast<const char*>(a.w2) + ((size_t)(group >> 20) * a.H + h0) * row_bytes, tile_bytes);
   };
   auto pairs_of = [&](int first) {  // columns past the last pair repeat it and are not stored
-    m_off = (uint32_t)list[min(first + at.row, n - 1)] * row_bytes + at.chunk() * 16;
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+      m_off[c] = (uint32_t)list[min(first + c * 4 + at.row, n - 1)] * row_bytes + at.chunk * 16;
   };
   auto fetch = [&](int d, int line) {
-    const bool in = line < hi && line * 8 + at.chunk() < nch;
-    w[d] = load_rows<true>(w2, in ? w_off : kOutside, (uint32_t)line * 128);
-    b[d] = load_rows(mid, in ? m_off : kOutside, (uint32_t)line * 128);
+    const bool in = line < hi && line * 16 + at.chunk < nch;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      w[d][r] = load_rows<true>(w2, in ? w_off + r * 4 * row_bytes : kOutside, (uint32_t)line * 256);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) b[d][c] = load_rows(mid, in ? m_off[c] : kOutside, (uint32_t)line * 256);
   };
   if (wave < items) {
     item(wave);
@@ -325,13 +309,18 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
       in_order();
     }
   }
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[NT][2];
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int j = wave, first = 0, round = 0; j < items;) {
-    const int p = (int)list[min(first + at.row, n - 1)], left = n - first;
+    const uint16_t* this_list = list;
+    const int this_n = n;
     int next_j = j, next_first = first, next_round = round + 1;
     if (next_round == rounds) {
       next_round = 0;
-      next_first += 8;
+      next_first += 4 * NT;
       if (next_first >= n) {
         next_first = 0;
         next_j += kDownWaves;
@@ -342,15 +331,26 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     const int next_line = next_j < items ? lo + next_round * kDepth : hi;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      acc = mma_chunk<DT>(w[d], b[d], acc);
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c], acc[c][r]);
       in_order();
       fetch(d, next_line + d);  // past the end: zeros
       in_order();
     }
     if (next_round == 0) {
-      acc = join_halves(acc);
-      if (at.half == 0 && at.q < 2 && at.row < left) y[((size_t)part * a.pairs + p) * 2 + at.q] = acc;
-      acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const int pos = first + c * 4 + at.second();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float v = join_parts(acc[c][r]);
+          acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if ((lane_id() & 3) == 0 && pos < this_n)
+            y[((size_t)part * a.pairs + this_list[pos]) * 8 + r * 4 + at.first()] = v;
+        }
+      }
     }
     j = next_j;
     first = next_first;
@@ -358,7 +358,6 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   }
   __syncthreads();
 
-  const float* yf = reinterpret_cast<const float*>(y);
   for (int o = threadIdx.x; o < a.T * 8; o += kDownWaves * kWave) {
     const int t = o >> 3, c = o & 7;
     if (h0 + c >= a.H) continue;
@@ -366,8 +365,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     for (int k = 0; k < a.K; ++k) {
       const int p = t * a.K + k;
       if (!here[p]) continue;
-      float v = yf[(size_t)p * 8 + c];
-      for (int i = 1; i < a.split; ++i) v += yf[((size_t)i * a.pairs + p) * 8 + c];
+      float v = y[(size_t)p * 8 + c];
+      for (int i = 1; i < a.split; ++i) v += y[((size_t)i * a.pairs + p) * 8 + c];
       sum = __fadd_rn(sum, __fmul_rn(weight[p], v));
     }
     const size_t pos = (size_t)t * a.H + h0 + c;
@@ -376,18 +375,23 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   }
 }
 
-template <int DT>
+template <int DT, int NT>
 hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
   const int up = (int)std::min<int64_t>(kUpGroups, (int64_t)a.groups * ((a.I + 7) / 8));
-  if (a.pairs <= 4 * a.E)
-    hipLaunchKernelGGL((few_up_kernel<DT, 1>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
-  else
-    hipLaunchKernelGGL((few_up_kernel<DT, 4>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
+  hipLaunchKernelGGL((few_up_kernel<DT, NT>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((few_down_kernel<DT>), dim3((a.H + 7) / 8), dim3(kDownWaves * kWave),
+  hipLaunchKernelGGL((few_down_kernel<DT, NT>), dim3((a.H + 7) / 8), dim3(kDownWaves * kWave),
                      (size_t)a.split * a.pairs * 32, s, a);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
+  // pairs a chosen expert has on average, if the choice is even
+  if (a.pairs <= a.E) return launch_few_typed<DT, 1>(a, s);
+  if (a.pairs <= 5 * a.E) return launch_few_typed<DT, 2>(a, s);
+  return launch_few_typed<DT, 8>(a, s);
 }
 
 }  // namespace
@@ -397,8 +401,8 @@ hipError_t launch_few(const FewArgs& args, hipStream_t s) {
   a.groups = std::min(a.pairs, a.E);
   a.split = 1;  // parts for every wave of a workgroup of the second product, when experts are few
   while (a.groups * a.split < kDownWaves && 2 * a.split * a.pairs <= kFewMaxPairs) a.split *= 2;
-  a.part_lines = ((a.ich + 7) / 8 + a.split - 1) / a.split;
-  return a.dtype == MOE_F32 ? launch_few_typed<kF32>(a, s) : launch_few_typed<kBF16>(a, s);
+  a.part_lines = ((a.ich + 15) / 16 + a.split - 1) / a.split;
+  return a.dtype == MOE_F32 ? launch_few_tiles<kF32>(a, s) : launch_few_tiles<kBF16>(a, s);
 }
 
 }  // namespace moe

@@ -193,7 +193,7 @@ struct FewArgs {
   int pairs;              // T*K
   int hch, ich;           // 16-byte chunks of a row of H, of I
   int groups;             // distinct experts a call can have at most (set by the launcher)
-  int split, part_lines;  // parts of the sum over I, 128-byte lines of a part (set by the launcher)
+  int split, part_lines;  // parts of the sum over I, 256-byte lines of a part (set by the launcher)
 };
 
 // Low-rank adapters on a layout of one adapter per token: the three kernels'

@@ -57,6 +57,38 @@ __device__ __forceinline__ u32x4 load_rows(__amdgpu_buffer_rsrc_t rows, uint32_t
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)lane_off, (int)off, ONCE ? 2 : 0));
 }
 
+// Tiles of 4 rows by 256 bytes of each, one load instruction in which every
+// quad of lanes takes 64 contiguous bytes.  That order is what the address unit
+// wants: 1 KiB loads from L2 run at 25.6 TB/s so, and at 9.2 TB/s where each
+// lane of a quad is on another row (MI355X), as the operand layout above would
+// have it.  As an operand the tile's 16 rows are the 4 rows with 4 chunks each
+// (every fourth lane quarter's); the other operand's 16 columns are 4 rows
+// likewise.  The result's elements that meet in the same chunk are one of the
+// four in each lane; a quad of lanes holds the four parts of one sum.  Three
+// quarters of the products are not used: where memory is the limit the matrix
+// cores have far more to spare.
+struct Lane {
+  int row, chunk;  // of the 4 rows, of the 16 chunks of its 256 bytes
+  __device__ __forceinline__ Lane() : row((lane_id() >> 2) & 3), chunk((lane_id() >> 4) * 4 + (lane_id() & 3)) {}
+  // the joined result in this lane: first operand's row, second operand's row
+  __device__ __forceinline__ int first() const { return lane_id() >> 4; }
+  __device__ __forceinline__ int second() const { return row; }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float quad_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+// The sum of the parts, in every lane of the quad.
+__device__ __forceinline__ float join_parts(f32x4 acc) {
+  const int k = lane_id() & 3;
+  float v = k == 0 ? acc[0] : k == 1 ? acc[1] : k == 2 ? acc[2] : acc[3];
+  v += quad_move<0xB1>(v);  // lanes 1 0 3 2
+  v += quad_move<0x4E>(v);  // lanes 2 3 0 1
+  return v;
+}
+
 // Keeps loads and products in the order they are written in: left alone, the
 // compiler gathers the loads of a software pipeline and waits for all of them.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
