@@ -105,12 +105,12 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
 //     4 KiB apart read at the same place at the same time meet in a few memory
 //     channels.  140 -> 134 us.  The order of the sum depends on the item
 //     through its workgroup alone, so it is the same in every run.
-constexpr int kUpWaves = 4;
-constexpr int kUpGroups = 1024;  // workgroups at most: four a CU
+constexpr int kUpWaves = 8;
+constexpr int kUpGroups = 512;  // workgroups at most: two a CU
 
 template <int DT, int NT>
 __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
-  constexpr int kDepth = NT <= 2 ? 3 : 1;
+  constexpr int kDepth = 1;  // the other waves' lines are in flight meanwhile
   __shared__ Groups groups;
   __shared__ float part[kUpWaves][NT][2][2][16];  // wave, tile of pairs, tile of rows, gate or up, row * 4 + pair
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
@@ -389,7 +389,7 @@ hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
 template <int DT>
 hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
   // pairs a chosen expert has on average, if the choice is even
-  if (a.pairs <= a.E) return launch_few_typed<DT, 1>(a, s);
+  if (a.pairs <= 2 * a.E) return launch_few_typed<DT, 1>(a, s);
   if (a.pairs <= 5 * a.E) return launch_few_typed<DT, 2>(a, s);
   return launch_few_typed<DT, 8>(a, s);
 }
