@@ -33,10 +33,6 @@ namespace {
 constexpr int kTile = 16;        // receive rows of a tile
 constexpr int kMaxOff = 1024 + 1;
 
-// Chunk of 16 that slot m of an operand takes, chosen so that the four lanes
-// of one result column store four neighbouring chunks.
-__device__ __forceinline__ int slot_chunk(int m) { return (m & 3) * 4 + (m >> 2); }
-
 template <int DT>
 struct Shape {
   static constexpr int V = DT == kBF16 ? 8 : 4;   // elements of a chunk
@@ -81,26 +77,44 @@ __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
 // One workgroup per (RT tiles of 16 rows, slot).  Its waves split the sum over
 // the row, a 128-byte line of every row each in turn, kDepth lines in flight,
 // and meet in LDS; wave rt adds the parts of tile rt and writes its 16 rows of
-// r float32.  Workgroups start at different lines (and go round): rows a power
-// of two apart, read at the same place at once, meet in a few memory channels.
-// FAR: the wide rows reach past what a buffer's 32-bit offsets do (2 GiB).
-constexpr int kShrinkWaves = 8;
+// r float32.
+//
+// A wave loads whole lines, eight lanes to a line: the bank is read again for
+// every tile, from L2, and L2 gives 25.6 TB/s in that order but 9.2 TB/s in the
+// operands' (each lane of a quad on another row).  The lines pass through the
+// wave's own piece of LDS, chunks rotated by row so that neither side meets a
+// bank twice.  Workgroups start at different lines (and go round): rows a
+// power of two apart, read at the same place at once, meet in a few memory
+// channels.  FAR: the wide rows reach past what a buffer's 32-bit offsets do (2
+// GiB).
+template <int JT, int RT>
+struct Shrink {
+  static constexpr int kMeet = JT * RT <= 4 ? JT : 4 / RT;     // tiles of the rank that meet in LDS together
+  static constexpr int kStaged = JT < 4 ? JT : 4;              // tiles of the rank in LDS at a time
+  static constexpr int kRows = 16 * (RT + kStaged);            // rows of a stage: the tokens', then the bank's
+  static constexpr int kWaves = JT + RT <= 3 ? 8 : 4;
+  static constexpr size_t kLds = (size_t)kWaves * kRows * 128;  // at most 48 KiB
+};
 
 template <int DT, int JT, int RT, bool FAR>
-__global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs a) {
-  // lines in flight: about 128 registers of them; a call has one or two
-  // workgroups a CU, so each has to keep the memory busy by itself
-  constexpr int kDepth = JT + RT <= 4 ? 4 : JT + RT <= 6 ? 3 : 2;
-  constexpr int kMeet = JT * RT <= 4 ? JT : 4 / RT;  // tiles of the rank that meet in LDS together
+__global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kernel(LowrankArgs a) {
+  constexpr int kShrinkWaves = Shrink<JT, RT>::kWaves, kMeet = Shrink<JT, RT>::kMeet;
+  constexpr int kStaged = Shrink<JT, RT>::kStaged, kRows = Shrink<JT, RT>::kRows;
+  constexpr int kDepth = JT + RT <= 2 ? 3 : JT + RT <= 4 ? 2 : 1;
   __shared__ int off[kMaxOff];
-  __shared__ f32x4 part[kShrinkWaves][RT][kMeet][kWave];
+  extern __shared__ u32x4 lds[];  // [waves][kRows][8 chunks]; then [waves][RT][kMeet][64] to meet in
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-  const int col = lane & 15, q = lane >> 4;
+  const int col = lane & 15, q = lane >> 4;  // of an operand
+  const int row8 = lane >> 3, chunk = lane & 7;  // of a load: 8 rows by one line
+  u32x4* stage = lds + (size_t)wave * kRows * 8;
+  f32x4* part = reinterpret_cast<f32x4*>(lds);
   const int nch = a.wch, lines = (nch + 7) / 8;
   const int start = (blockIdx.x + blockIdx.y) * 5 % lines;
   const uint32_t row_bytes = (uint32_t)nch * 16;
   const int r0 = blockIdx.x * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
-  int t[RT];
+  int t[RT], load_t[2 * RT];
+#pragma unroll
+  for (int i = 0; i < 2 * RT; ++i) load_t[i] = max(row_token(a, r0 + i * 8 + row8), 0);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + col);
   load_offsets(off, a);
@@ -112,49 +126,35 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
       mine[rt] = p >= lo && p < hi;
     }
     if (e >= a.A) {  // no adapter: u = 0, and no gradient
+      for (int i = threadIdx.x; i < (hi - lo) * a.r; i += kShrinkWaves * kWave) a.u[(size_t)lo * a.r + i] = 0.f;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (wave != rt || !mine[rt]) continue;
-        const size_t p = r0 + rt * kTile + col;
-        for (int j = q * 4; j < a.r; j += 16) *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (a.dot && q == 0 && t[rt] >= 0) a.dot[t[rt]] = 0.f;
-      }
+      for (int rt = 0; rt < RT; ++rt)
+        if (a.dot && wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = 0.f;
       return;
     }
-    // columns of other adapters read their rows (padding the first one); the
+    // columns of other adapters take their rows (padding the first one); the
     // results are dropped
-    const u32x4* x[RT];
-    uint32_t x_off[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      x[rt] = static_cast<const u32x4*>(a.rows) + (size_t)max(t[rt], 0) * nch;
-      x_off[rt] = (uint32_t)max(t[rt], 0) * row_bytes + q * 16;
-    }
     const auto wide = make_rows(a.rows, FAR ? 0 : (size_t)a.T * row_bytes);
     const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
-    const uint32_t b_off = (uint32_t)col * row_bytes + q * 16;
-    u32x4 xv[kDepth][2][RT], bv[kDepth][2][JT];
+    const uint32_t b_off = (uint32_t)row8 * row_bytes + chunk * 16;
+    u32x4 in[kDepth][2 * (RT + JT)];
     auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
       const int line = i + start < lines ? i + start : i + start - lines;
+      const int c = line * 8 + chunk;
+      const bool ok = i < lines && c < nch;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int c = line * 8 + s * 4 + q;
-        const bool in = i < lines && c < nch;
-        const uint32_t at = (uint32_t)(line * 128 + s * 64);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          if constexpr (FAR) {
-            xv[d][s][rt] = x[rt][in ? c : 0];
-            // the bank's zeros alone would leave NaN where a row holds one
-            if (!in) xv[d][s][rt] = u32x4{0u, 0u, 0u, 0u};
-          } else {
-            xv[d][s][rt] = load_rows(wide, in ? x_off[rt] : kOutside, at);
-          }
+      for (int k = 0; k < 2 * RT; ++k) {
+        if constexpr (FAR) {
+          in[d][k] = static_cast<const u32x4*>(a.rows)[(size_t)load_t[k] * nch + (ok ? c : 0)];
+          // the bank's zeros alone would leave NaN where a row holds one
+          if (!ok) in[d][k] = u32x4{0u, 0u, 0u, 0u};
+        } else {
+          in[d][k] = load_rows(wide, ok ? (uint32_t)load_t[k] * row_bytes + chunk * 16 : kOutside, (uint32_t)line * 128);
         }
-#pragma unroll
-        for (int jt = 0; jt < JT; ++jt)
-          bv[d][s][jt] = load_rows(bank, in ? b_off + (uint32_t)jt * 16 * row_bytes : kOutside, at);
       }
+#pragma unroll
+      for (int k = 0; k < 2 * JT; ++k)
+        in[d][2 * RT + k] = load_rows(bank, ok ? b_off + (uint32_t)k * 8 * row_bytes : kOutside, (uint32_t)line * 128);
     };
     f32x4 acc[RT][JT];
 #pragma unroll
@@ -169,14 +169,33 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
     for (int i = wave; i < lines; i += kShrinkWaves * kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
+        // row r's chunk c stands at place c ^ (r / 2 % 8)
+        auto put = [&](int r, const u32x4 v) { stage[r * 8 + (chunk ^ (r >> 1 & 7))] = v; };
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int k = 0; k < 2 * RT; ++k) put(k * 8 + row8, in[d][k]);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+        for (int j0 = 0; j0 < JT; j0 += kStaged) {
 #pragma unroll
-            for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = mma_chunk<DT>(bv[d][s][jt], xv[d][s][rt], acc[rt][jt]);
-        in_order();
-        fetch(d, i + (d + kDepth) * kShrinkWaves);
+          for (int k = 0; k < 2 * kStaged; ++k) put((2 * RT + k) * 8 + row8, in[d][2 * RT + 2 * j0 + k]);
+          if (j0 + kStaged == JT) {
+            in_order();
+            fetch(d, i + (d + kDepth) * kShrinkWaves);
+            in_order();
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int place = (s * 4 + q) ^ (col >> 1);
+            u32x4 xv[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) xv[rt] = stage[(rt * 16 + col) * 8 + place];
+#pragma unroll
+            for (int m = 0; m < kStaged; ++m) {
+              const u32x4 bv = stage[((RT + m) * 16 + col) * 8 + place];
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) acc[rt][j0 + m] = mma_chunk<DT>(bv, xv[rt], acc[rt][j0 + m]);
+            }
+          }
+        }
         in_order();
       }
     }
@@ -186,10 +205,11 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
       if (wave == rt && a.w && t[rt] >= 0) w = a.w[t[rt]];
 #pragma unroll
     for (int first = 0; first < JT; first += kMeet) {
+      __syncthreads();  // every wave is done with its stage, or with the parts before
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int m = 0; m < kMeet; ++m) part[wave][rt][m][lane] = acc[rt][first + m];
+        for (int m = 0; m < kMeet; ++m) part[((wave * RT + rt) * kMeet + m) * kWave + lane] = acc[rt][first + m];
       __syncthreads();
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -197,9 +217,9 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
         const size_t p = r0 + rt * kTile + col;
 #pragma unroll
         for (int m = 0; m < kMeet; ++m) {
-          f32x4 v = part[0][rt][m][lane];
+          f32x4 v = part[(rt * kMeet + m) * kWave + lane];
 #pragma unroll
-          for (int k = 1; k < kShrinkWaves; ++k) v += part[k][rt][m][lane];
+          for (int k = 1; k < kShrinkWaves; ++k) v += part[((k * RT + rt) * kMeet + m) * kWave + lane];
           const int j = (first + m) * 16 + q * 4;
           if (mine[rt] && j < a.r) {
             if (t[rt] < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
@@ -215,7 +235,6 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
           }
         }
       }
-      __syncthreads();
     }
     if (a.dot) {
       dot += __shfl_xor(dot, 16, kWave);
@@ -224,6 +243,7 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void shrink_kernel(LowrankArgs
       for (int rt = 0; rt < RT; ++rt)
         if (wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = dot;
     }
+    __syncthreads();  // the parts have been read
   });
 }
 
@@ -241,8 +261,8 @@ __device__ __forceinline__ u32x4 pack_rows(const float (&f)[V]) {
 // Here the summed index is the row index of the wide operand (the bank's rows,
 // or tokens): a lane loads the same chunk of V neighbouring rows, and element i
 // of all of them is its operand for the i-th of V result tiles.  The tile's 16
-// columns are then V columns apart, and a lane ends with V neighbouring
-// elements of four chunks.
+// columns are then V columns apart, and a lane ends with all V elements of
+// chunks 4q .. 4q+3.
 
 // Splits 8 floats into two bfloat16 parts, hi + lo.
 __device__ __forceinline__ void split_bf16(const float (&f)[8], u32x4& hi, u32x4& lo) {
@@ -310,36 +330,43 @@ __device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const Factor<DT>
 //
 // One wave per (a.tiles tiles of 16 receive rows, COLS columns, slot); it keeps
 // its columns of an adapter's bank in registers from tile to tile, and has the
-// next tile's rows of base on their way.  BLOCKS blocks of KB ranks.
+// next tile's rows of base on their way.  BLOCKS blocks of KB ranks.  The
+// products pass through LDS, so that base is read and out is written with 16
+// lanes to a row.
 constexpr int kExpandWaves = 4;
 
 template <int DT, int BLOCKS>
 __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(LowrankArgs a) {
   using S = Shape<DT>;
   constexpr int V = S::V;
+  constexpr int kStride = 16 * V + 4;  // floats of a row in LDS: rows shifted by four banks
   __shared__ int off[kMaxOff];
+  __shared__ __align__(16) float products[kExpandWaves][kTile * kStride];
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
   const int col = lane & 15, q = lane >> 4;
+  float* prod = products[wave];
   const int nch = a.wch;
   const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
   const uint32_t row_bytes = (uint32_t)nch * 16;
+  const int my_c = c0 + col;
+  const bool in = my_c < nch;
   // ranks and columns past the end are outside the bank and read as zeros
-  const int mine_c = c0 + slot_chunk(col);
-  const uint32_t b_off = mine_c < nch ? (uint32_t)mine_c * 16 : kOutside;
+  const uint32_t b_off = in ? (uint32_t)my_c * 16 : kOutside;
 
-  // a tile's rows: token, weight and the chunks of base
+  // a tile's rows: the token of row `col`, and base where this lane adds it
+  // (rows q, 4 + q, ..., chunk `col`)
   struct Rows {
     int t;
-    float w;
     u32x4 base[4];
   } now, next;
   auto fetch = [&](Rows& r, int t) {
     r.t = t;
-    r.w = a.w ? a.w[max(t, 0)] : 1.f;
     if (a.base) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        r.base[s] = static_cast<const u32x4*>(a.base)[(size_t)max(t, 0) * nch + min(c0 + s * 4 + q, nch - 1)];
+      for (int s = 0; s < 4; ++s) {
+        const int tt = max(__shfl(t, s * 4 + q, kWave), 0);
+        r.base[s] = static_cast<const u32x4*>(a.base)[(size_t)tt * nch + min(my_c, nch - 1)];
+      }
     }
   };
   int tile = blockIdx.x * a.tiles;
@@ -355,6 +382,7 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
   for (; tile < tile_end; ++tile) {
     now = next;
     const int r0 = tile * kTile, r1 = min(r0 + kTile, a.R);
+    const float w = a.w ? a.w[max(now.t, 0)] : 1.f;
     float f[BLOCKS][V];
     const float* u = a.u + (size_t)min(r0 + col, a.R - 1) * a.r;
 #pragma unroll
@@ -364,14 +392,11 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
         const int jj = k * S::KB + q * V + j;
         const f32x4 v = *reinterpret_cast<const f32x4*>(u + (jj < a.r ? jj : 0));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[k][j + i] = jj < a.r ? v[i] * now.w : 0.f;
+        for (int i = 0; i < 4; ++i) f[k][j + i] = jj < a.r ? v[i] * w : 0.f;
       }
     if (tile + 1 < tile_end) fetch(next, next_t);
     next_t = row_token(a, (tile + 2) * kTile + col);
     each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
-      f32x4 acc[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (e < a.A) {
         if (e != held) {
           held = e;
@@ -387,22 +412,38 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
             across<DT, V>(b, bank[k]);
           }
         }
+        f32x4 acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < BLOCKS; ++k) mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
+        // row `col`, chunks 4q .. 4q+3
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<f32x4*>(prod + col * kStride + (q * 4 + s) * V + i) =
+                f32x4{acc[i][s], acc[i + 1][s], acc[i + 2][s], acc[i + 3][s]};
       }
-      // the columns of other adapters' rows are dropped
-      const int p = r0 + col;
-      if (now.t < 0 || p < lo || p >= hi) return;
+      // the rows of other adapters are dropped
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const int c = c0 + s * 4 + q;
-        if (c < nch) {
-          float o[V];
-          if (a.base) unpack<DT>(now.base[s], o);
+        const int row = s * 4 + q, t = __shfl(now.t, row, kWave);
+        float o[V];
+        if (a.base) unpack<DT>(now.base[s], o);
+        if (e < a.A) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = a.base ? o[i] + acc[i][s] : acc[i][s];
-          static_cast<u32x4*>(a.out)[(size_t)now.t * nch + c] = pack_rows<DT>(o);
+          for (int i = 0; i < V; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(prod + row * kStride + col * V + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i + k] = a.base ? o[i + k] + v[k] : v[k];
+          }
+        } else if (!a.base) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = 0.f;
         }
+        if (t >= 0 && r0 + row >= lo && r0 + row < hi && in)
+          static_cast<u32x4*>(a.out)[(size_t)t * nch + my_c] = pack_rows<DT>(o);
       }
     });
   }
@@ -429,7 +470,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   const int parts = (a.r + 16 * JT - 1) / (16 * JT);
   const int c0 = blockIdx.x / parts * 16;
   const int j0 = blockIdx.x % parts * JT * 16;
-  const int c = min(c0 + slot_chunk(col), nch - 1);  // chunks past the end repeat the last and are not stored
+  const int c = min(c0 + col, nch - 1);  // chunks past the end repeat the last and are not stored
   const int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
   f32x4 acc[JT][V];
 #pragma unroll
@@ -492,7 +533,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
     for (int i = 0; i < V; ++i) part[wave][i][lane] = acc[jt][i];
     __syncthreads();
     const int j = j0 + jt * 16 + col;
-    if (wave < 4) {  // wave s stores the chunks of quad s
+    if (wave < 4) {  // wave s stores the s-th of every lane's four chunks
       float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -501,7 +542,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
 #pragma unroll
         for (int k = 1; k < kWgradWaves; ++k) o[i] += f[(size_t)k * V * kWave * 4];
       }
-      const int cc = c0 + wave * 4 + q;
+      const int cc = c0 + q * 4 + wave;
       if (j < a.r && cc < nch) static_cast<u32x4*>(a.out)[((size_t)e * a.r + j) * nch + cc] = pack_rows<DT>(o);
     }
   }
@@ -527,11 +568,13 @@ hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
   const bool far = (int64_t)a.T * a.wch * 16 >= (int64_t(1) << 31);
   const int rt = !far && a.r <= 64 && a.R >= 2 * kTile * 256 ? 2 : 1;
   const int tiles = (a.R + kTile * rt - 1) / (kTile * rt);
-  const dim3 grid(tiles, slots_for(tiles, a.E)), block(kShrinkWaves * kWave);
-#define MOE_SHRINK(J, T, F)                                                                            \
-  return launched([&] {                                                                                \
-    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T, F>), grid, block, 0, s, a);  \
-    else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T, F>), grid, block, 0, s, a);                    \
+  const dim3 grid(tiles, slots_for(tiles, a.E));
+#define MOE_SHRINK(J, T, F)                                                                             \
+  return launched([&] {                                                                                 \
+    const dim3 block((Shrink<J, T>::kWaves * kWave));                                                   \
+    const size_t lds = (Shrink<J, T>::kLds);                                                            \
+    if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T, F>), grid, block, lds, s, a); \
+    else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T, F>), grid, block, lds, s, a);                   \
   })
   if (far) {
     if (a.r <= 32) MOE_SHRINK(2, 1, true);
