@@ -454,15 +454,23 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
 // grad[e][j][c] = sum over the adapter's rows p of coef[p][j] rows[t_p][c],
 // coef = u (times w for grad_B).  One workgroup per (COLS columns, adapter, 16
 // JT of the rank): its waves take the adapter's rows in turn, each a block of
-// KB rows at a time with the next block's rows on their way, and meet in LDS.
-// An adapter without rows gets zeros.
+// KB rows at a time with the next block's on its way, and meet in LDS.  A
+// block's rows of u pass through the wave's own piece of LDS, loaded 16 bytes a
+// lane: four bytes a lane, as the operand takes them, cost the address unit
+// twice what the wide rows do.  An adapter without rows gets zeros.
 constexpr int kWgradWaves = 8;
 
 template <int DT, int JT>
 __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a) {
   using S = Shape<DT>;
   constexpr int V = S::V;
-  __shared__ f32x4 part[kWgradWaves][V][kWave];
+  constexpr int kStride = JT * 16 + 4;                  // floats of a row of u in LDS
+  constexpr int kLoads = S::KB * JT * 4 / kWave;        // a block's u, 16 bytes a lane
+  __shared__ __align__(16) union {
+    float u[kWgradWaves][S::KB * kStride];
+    f32x4 part[kWgradWaves][V][kWave];
+  } sh;
+  auto& part = sh.part;
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
   const int col = lane & 15, q = lane >> 4;
   const int e = blockIdx.y;
@@ -477,53 +485,65 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[jt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // lane l < KB knows the block's row l: its token, -1 without one
+  auto tokens = [&](int p0) {
+    const int p = p0 + lane;
+    const int v = a.recv_token[min(p, a.R - 1)];
+    return lane < S::KB && p < hi && (unsigned)v < (unsigned)a.T ? v : -1;
+  };
   u32x4 x[V];
-  int t[V], next_t[V];
-  auto tokens = [&](int p0, int (&to)[V]) {
+  f32x4 u[kLoads];
+  float w = 1.f;
+  int t = -1, next_t = -1;
+  auto fetch = [&](int p0) {  // the rows whose tokens are in t
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int p = p0 + q * V + k;
-      const int v = a.recv_token[min(p, a.R - 1)];
-      to[k] = p < hi && (unsigned)v < (unsigned)a.T ? v : -1;
+    for (int k = 0; k < V; ++k)
+      x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(__shfl(t, q * V + k, kWave), 0) * nch + c];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = i * kWave + lane, row = at / (JT * 4), j = j0 + at % (JT * 4) * 4;
+      u[i] = *reinterpret_cast<const f32x4*>(a.u + (size_t)min(p0 + row, hi - 1) * a.r + min(j, a.r - 4));
     }
+    if (a.w) w = a.w[max(t, 0)];
   };
   constexpr int kStep = kWgradWaves * S::KB;
   int p0 = lo + wave * S::KB;
   if (p0 < hi) {
-    tokens(p0, t);
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(t[k], 0) * nch + c];
-    tokens(p0 + kStep, next_t);
+    t = tokens(p0);
+    fetch(p0);
+    next_t = tokens(p0 + kStep);
   }
   for (; p0 < hi; p0 += kStep) {
-    float f[JT][V], w[V];
+    // this block's operands leave their registers, then the next block's rows
+    // are asked for
+    float* us = sh.u[wave];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float* u = a.u + (size_t)min(p0 + q * V + k, hi - 1) * a.r;
-#pragma unroll
-      for (int jt = 0; jt < JT; ++jt) f[jt][k] = u[min(j0 + jt * 16 + col, a.r - 1)];
-      w[k] = a.w ? a.w[max(t[k], 0)] : 1.f;
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = i * kWave + lane;
+      *reinterpret_cast<f32x4*>(us + at / (JT * 4) * kStride + at % (JT * 4) * 4) = u[i];
     }
+    bool there[V];
+    float wk[V];
     u32x4 o[V];
     {
       u32x4 z[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) z[k] = t[k] >= 0 ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
+      for (int k = 0; k < V; ++k) {
+        there[k] = __shfl(t, q * V + k, kWave) >= 0;
+        wk[k] = a.w ? __shfl(w, q * V + k, kWave) : 1.f;
+        z[k] = there[k] ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
+      }
       across<DT, V>(z, o);
     }
-    bool there[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      there[k] = t[k] >= 0;
-      t[k] = next_t[k];
-      x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(t[k], 0) * nch + c];
-    }
-    tokens(p0 + 2 * kStep, next_t);
+    t = next_t;
+    fetch(p0 + kStep);
+    next_t = tokens(p0 + 2 * kStep);
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
+      float f[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[jt][k] = there[k] ? f[jt][k] * w[k] : 0.f;
-      mma_across<DT, V>(o, Factor<DT>(f[jt]), acc[jt]);
+      for (int k = 0; k < V; ++k) f[k] = there[k] ? us[(q * V + k) * kStride + jt * 16 + col] * wk[k] : 0.f;
+      mma_across<DT, V>(o, Factor<DT>(f), acc[jt]);
     }
   }
 #pragma unroll
@@ -596,9 +616,11 @@ hipError_t launch_lowrank_expand(const LowrankArgs& args, hipStream_t s) {
   LowrankArgs a = args;
   const int tiles = (a.R + kTile - 1) / kTile;
   const int cols = (a.wch + 16 * kExpandWaves - 1) / (16 * kExpandWaves);
-  // up to 4 tiles a wave while there are four workgroups a CU
+  // as many tiles a wave as leave one generation of workgroups, two a CU (8192
+  // rows of 4096 columns in bfloat16, rank 32: 46 us with one tile, 38 with
+  // four, 34 with eight)
   a.tiles = 1;
-  while (a.tiles < 4 && (int64_t)tiles * cols >= 2 * a.tiles * 1024) a.tiles *= 2;
+  while (a.tiles < 16 && (int64_t)tiles * cols >= 2 * a.tiles * 512) a.tiles *= 2;
   const int blocks = (tiles + a.tiles - 1) / a.tiles;
   const dim3 grid(blocks, cols, a.tiles > 1 ? 1 : slots_for((int64_t)tiles * cols, a.E)), block(kExpandWaves * kWave);
 #define MOE_EXPAND(D, B) \

@@ -12,10 +12,12 @@
 // One wavefront per token.  Its E values lie in registers (lane-strided, or
 // by group: L lanes per group), the choice is K rounds of a wave-wide maximum
 // over each lane's best remaining value, on integer keys that order like the
-// numbers.  Values that have to be compared after arithmetic (bias, group
-// sums) are formed and compared in 64 bits, so that a choice next to a border
-// is the definition's; the plain top-k compares the logits themselves, which
-// rounds nothing.
+// numbers.  The plain top-k compares the logits themselves, which rounds
+// nothing.  Values that have to be compared after arithmetic (bias, group
+// sums) are formed in 32 bits first; a token whose choice hangs on a difference
+// that the rounding could have turned is chosen again in 64 bits, so that a
+// choice next to a border is the definition's (16384 tokens, 256 experts: 28 us
+// in 64 bits throughout, NEW_US so).
 //
 // Logits that are NaN count as -inf in the choice and spread to the weights
 // as the formulas say.  A sum of scores that is zero (every expert masked by
@@ -89,6 +91,17 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   return ((uint64_t)hi << 32) | lo;
 }
 
+template <typename R>
+struct Key;
+template <>
+struct Key<float> {
+  typedef uint32_t T;
+};
+template <>
+struct Key<double> {
+  typedef uint64_t T;
+};
+
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* z, size_t i) {
   if constexpr (DT == kF32) return static_cast<const float*>(z)[i];
@@ -110,8 +123,9 @@ __device__ __forceinline__ double sigmoid(double z) { return 1.0 / (1.0 + exp(-z
 // key[v] belongs to expert base + step*v, so a lane's experts ascend with v.
 // Up to 4 values a lane keeps them sorted (largest first, the lower id first
 // among equals) and a winning lane shifts; more are searched again each round.
-template <int VPL, typename KEY>
-__device__ __forceinline__ int choose(KEY (&key)[VPL], int base, int step, int K) {
+// each(m) sees the winning keys in their order.
+template <int VPL, typename KEY, typename F>
+__device__ __forceinline__ int choose(KEY (&key)[VPL], int base, int step, int K, F each) {
   const int lane = lane_id();
   int id[VPL];
 #pragma unroll
@@ -144,6 +158,7 @@ __device__ __forceinline__ int choose(KEY (&key)[VPL], int base, int step, int K
         }
     }
     const KEY m = wave_max(head);
+    each(m);
     const uint64_t with = __ballot(head == m);
     const int e = __popcll(with) == 1 ? read_lane_i(hid, __builtin_ctzll(with))
                                       : (int)wave_min(head == m ? (uint32_t)hid : 0xFFFFFFFFu);
@@ -204,7 +219,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       total = wave_sum(sum);
     }
   }
-  const int e = choose<VPL>(key, lane, kWave, a.K);
+  const int e = choose<VPL>(key, lane, kWave, a.K, [](uint32_t) {});
   float s = 0.f;
   if (lane < a.K) {
     const float z = load_logit<DT>(a.z, row + e);
@@ -218,37 +233,37 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   }
 }
 
-// With a bias or a group limit: scores, sums and keys in 64 bits.  L lanes
-// (a power of two) hold one group's experts.
-template <int DT, int VPL>
-__global__ __launch_bounds__(256) void route_groups_kernel(RouteArgs a) {
-  const int lane = lane_id();
-  const int t = blockIdx.x * (256 / kWave) + (int)(threadIdx.x / kWave);
-  if (t >= a.T) return;  // wave-uniform
-  const size_t row = (size_t)t * a.E;
-  const int g = lane / a.L, l = lane & (a.L - 1);
+// The choice with a bias or a group limit, formed in R (float or double); lane
+// k gets the k-th expert.  L lanes (a power of two) hold one group's experts, g
+// and l are the lane's group and place.  In float, `sure` says whether every
+// comparison that the choice hangs on was of values further apart than their
+// errors: scores are within 2^-18 of the true ones (u = 2^-24: a sigmoid within
+// 5 u; a softmax's numerator within 0.37 u from the rounded difference and 2 u
+// of itself, its sum of at most 32 terms a lane within 38 u of itself), and a
+// bias adds u times the value.  Two values are told apart from 2^-16 on, group
+// sums from 2^-15, times the largest value where that is above 1.
+template <typename R, int VPL>
+__device__ __forceinline__ int choose_scored(const RouteArgs& a, const float (&z)[VPL], const float (&bias)[VPL], int g,
+                                             int l, bool& sure, R& m, R& all) {
+  constexpr bool kExact = sizeof(R) == 8;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  double c[VPL];
+  R c[VPL];
   bool there[VPL];
-  bool nan = false;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    const int j = l + a.L * v;
-    there[v] = g < a.groups && j < a.per;
-    c[v] = there[v] ? (double)load_logit<DT>(a.z, row + g * a.per + j) : -INFINITY;
-    nan |= c[v] != c[v];
-    if (c[v] != c[v]) c[v] = -INFINITY;
+    there[v] = g < a.groups && l + a.L * v < a.per;
+    c[v] = (R)z[v];
   }
-  const bool bad = softmax && __ballot(nan) != 0;  // a NaN anywhere reaches every softmax weight
-  double m = 0.0, all = 1.0;
+  m = 0;
+  all = 1;
   if (softmax) {
     m = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) m = fmax(m, c[v]);
+    for (int v = 0; v < VPL; ++v) m = max(m, c[v]);
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) m = fmax(m, shfl_xor_d(m, s));
-    if (m == -INFINITY) m = 0.0;
-    double sum = 0.0;
+    for (int s = 32; s >= 1; s >>= 1) m = max(m, __shfl_xor(m, s, kWave));
+    if (m == -INFINITY) m = 0;
+    R sum = 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
       if (there[v]) {
@@ -256,54 +271,108 @@ __global__ __launch_bounds__(256) void route_groups_kernel(RouteArgs a) {
         sum += c[v];
       }
     all = wave_sum(sum);
-    if (all == 0.0) all = 1.0;
+    if (all == 0) all = 1;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) c[v] /= all;
   } else {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) c[v] = sigmoid(c[v]);
   }
-  if (a.bias) {
+  R far = 1;  // the size that a bias's rounding goes by
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-      if (there[v]) c[v] += (double)a.bias[g * a.per + l + a.L * v];
+  for (int v = 0; v < VPL; ++v)
+    if (there[v]) {
+      c[v] += (R)bias[v];
+      if (c[v] != c[v]) c[v] = -INFINITY;
+      const R size = fabs(c[v]);
+      if (!kExact && size > far && size < INFINITY) far = size;
+    } else {
+      c[v] = -INFINITY;
+    }
+  R near = 0;  // two values closer than this are not told apart
+  if constexpr (!kExact) {
+    far = __uint_as_float(wave_max(__float_as_uint((float)far)));  // above 0: ordered like its bits
+    near = far * 0x1p-16f;
   }
+  sure = true;
   bool open = g < a.groups;
   if (a.topk_groups < a.groups) {
-    double b1 = -INFINITY, b2 = -INFINITY;  // this lane's two largest, then its group's
+    R b1 = -INFINITY, b2 = -INFINITY;  // this lane's two largest, then its group's
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const double x = there[v] && c[v] == c[v] ? c[v] : -INFINITY;
-      b2 = fmax(b2, fmin(b1, x));
-      b1 = fmax(b1, x);
+      b2 = max(b2, min(b1, c[v]));
+      b1 = max(b1, c[v]);
     }
     for (int s = 1; s < a.L; s <<= 1) {
-      const double o1 = shfl_xor_d(b1, s), o2 = shfl_xor_d(b2, s);
-      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-      b1 = fmax(b1, o1);
+      const R o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
+      b2 = max(min(b1, o1), max(b2, o2));
+      b1 = max(b1, o1);
     }
-    const double value = a.per > 1 ? b1 + b2 : b1;
+    const R value = a.per > 1 ? b1 + b2 : b1;
     int better = 0;
+    bool close = false;
     for (int i = 0; i < a.groups; ++i) {
-      const double other = __shfl(value, i * a.L, kWave);
+      const R other = __shfl(value, i * a.L, kWave);
       better += other > value || (other == value && i < g);
+      if (!kExact) close |= i != g && !(fabs(other - value) > 2 * near);  // also where both are infinite
     }
+    if (!kExact) sure = !__ballot(open && close);
     open = open && better < a.topk_groups;
   }
-  uint64_t key[VPL];
+  typename Key<R>::T key[VPL];
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) key[v] = open && there[v] ? key_of(c[v]) : 0ull;
-  const int e = choose<VPL>(key, g * a.per + l, a.L, a.K);
-  double s = 0.0;
+  for (int v = 0; v < VPL; ++v) key[v] = open && there[v] ? key_of(c[v]) : 0;
+  if constexpr (kExact) {
+    return choose<VPL>(key, g * a.per + l, a.L, a.K, [](uint64_t) {});
+  } else {
+    // one round more: the first that is not chosen counts too
+    float last = INFINITY;
+    return choose<VPL>(key, g * a.per + l, a.L, a.K + 1, [&](uint32_t k) {
+      if (k == 0) return;  // nothing is left
+      const float v = float_of(k);
+      sure = sure && last - v > near;
+      last = v;
+    });
+  }
+}
+
+template <int DT, int VPL>
+__global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a) {
+  const int lane = lane_id();
+  const int t = blockIdx.x * (256 / kWave) + (int)(threadIdx.x / kWave);
+  if (t >= a.T) return;  // wave-uniform
+  const size_t row = (size_t)t * a.E;
+  const int g = lane / a.L, l = lane & (a.L - 1);
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  float z[VPL], bias[VPL];
+  bool nan = false;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int j = l + a.L * v;
+    const bool there = g < a.groups && j < a.per;
+    z[v] = there ? load_logit<DT>(a.z, row + g * a.per + j) : -INFINITY;
+    bias[v] = a.bias && there ? a.bias[g * a.per + j] : 0.f;
+    nan |= z[v] != z[v];
+    if (z[v] != z[v]) z[v] = -INFINITY;
+  }
+  const bool bad = softmax && __ballot(nan) != 0;  // a NaN anywhere reaches every softmax weight
+  bool sure;
+  float m, all;
+  int e = choose_scored<float, VPL>(a, z, bias, g, l, sure, m, all);
+  if (!sure) {  // wave-uniform
+    double m64, all64;
+    e = choose_scored<double, VPL>(a, z, bias, g, l, sure, m64, all64);
+  }
+  float s = 0.f;
   if (lane < a.K) {
-    const double z = (double)load_logit<DT>(a.z, row + e);
-    s = softmax ? exp(z - m) / all : sigmoid(z);
+    const float x = load_logit<DT>(a.z, row + e);
+    s = softmax ? expf(x - m) / all : sigmoid(x);
     if (bad) s = NAN;
   }
-  const double total = a.renorm ? wave_sum(s) : 1.0;
+  const float total = a.renorm ? wave_sum(s) : 1.f;
   if (lane < a.K) {
     a.idx[(size_t)t * a.K + lane] = e;
-    a.w[(size_t)t * a.K + lane] = total == 0.0 && !bad ? 0.f : (float)(s * ((double)a.scale / total));
+    a.w[(size_t)t * a.K + lane] = total == 0.f && !bad ? 0.f : s * (a.scale / total);
   }
 }
 
@@ -422,8 +491,8 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
   while (a.L * 2 * a.groups <= kWave) a.L *= 2;
   const int need = (a.per + a.L - 1) / a.L;
 #define MOE_ROUTE(V)                                                                \
-  return a.dtype == MOE_F32 ? launch_rows(route_groups_kernel<kF32, V>, a.T, s, a)  \
-                            : launch_rows(route_groups_kernel<kBF16, V>, a.T, s, a)
+  return a.dtype == MOE_F32 ? launch_rows(route_scored_kernel<kF32, V>, a.T, s, a)  \
+                            : launch_rows(route_scored_kernel<kBF16, V>, a.T, s, a)
   if (need <= 1) MOE_ROUTE(1);
   if (need <= 2) MOE_ROUTE(2);
   if (need <= 4) MOE_ROUTE(4);

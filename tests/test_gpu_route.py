@@ -118,6 +118,21 @@ def test_ties_go_to_the_lower_index(dtype, E):
     check(z, 5, "softmax", False, 1.0, torch.zeros(E, device=DEV))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
+def test_choices_next_to_a_border(score, groups, keep):
+    """Biases that lift every expert to the same value but for their own float32
+    rounding: only 64 bits tell the experts (and groups) apart, and the choice
+    has to be the one that they tell."""
+    for seed in range(40):
+        z = draw(1, 96, F32, seed, 1.5)
+        s = scores64(z.cpu().numpy(), score)[0]
+        b = torch.from_numpy((1.0 - s).astype(np.float32)).to(DEV)
+        spread = np.abs(s + b.double().cpu().numpy() - 1.0).max()
+        assert 0 < spread < 2.0 ** -24
+        check(z, 6, score, True, 1.0, b, groups, keep)
+
+
 def test_masked_rows_and_nan():
     z = draw(40, 96, F32, 5, 2.0)
     z[0] = -math.inf                       # nothing left
