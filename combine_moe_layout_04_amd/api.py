@@ -483,11 +483,11 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     if bias is not None:
         _need(bias, "bias", dev, (E,), torch.float32)
     if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_idx = logits.new_empty((T, k), dtype=torch.int32)
     else:
         _need(topk_idx, "topk_idx", dev, (T, k), torch.int32)
     if topk_weights is None:
-        topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        topk_weights = logits.new_empty((T, k), dtype=torch.float32)
     else:
         _need(topk_weights, "topk_weights", dev, (T, k), torch.float32)
     _run(dev, "moe_route", logits.data_ptr(), dt, T, E, k,
@@ -507,7 +507,7 @@ def moe_route_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: to
     _need(topk_idx, "topk_idx", dev, (T, K), torch.int32)
     _need(grad_weights, "grad_weights", dev, (T, K), torch.float32)
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        grad_logits = torch.empty_like(logits)
     else:
         _need(grad_logits, "grad_logits", dev, (T, E), logits.dtype)
     _run(dev, "moe_route_bwd", logits.data_ptr(), dt, T, E, K,
@@ -560,7 +560,7 @@ def moe_few(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torc
     if workspace is None:
         # a call that the library refuses launches nothing: its workspace need not be allocated
         pairs = T * K if T * K <= FEW_MAX_PAIRS else 0
-        workspace = torch.empty(pairs * I, dtype=x.dtype, device=dev)
+        workspace = x.new_empty(pairs * I)
     else:
         _need(workspace, "workspace", dev)
     _run(dev, "moe_few", x.data_ptr(), dt, T, H, topk_idx.data_ptr(), _itype(topk_idx), K, _ptr(topk_weights),

@@ -684,11 +684,13 @@ int moe_time_next_kernel(moe_handle_t h, hipEvent_t start, hipEvent_t stop) {
 const char* moe_strerror(int status) {
   switch (status) {
     case MOE_OK: return "ok";
-    case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size or missing companion argument)";
-    case MOE_ERR_SHAPE: return "invalid shape (K<1, K>E, E%P!=0, H<1 or a row that is not whole 16-byte chunks)";
-    case MOE_ERR_UNSUPPORTED: return "unsupported (dtype/itype, P>64, E>1024, K>32 or T*K>=2^31)";
+    case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size, option or missing companion argument)";
+    case MOE_ERR_SHAPE: return "invalid shape (K<1, K>E, E%P!=0, H<1, a row that is not whole 16-byte chunks, router groups that "
+                               "do not divide E or hold too few experts, or adapters without a layout of K=1 and enough experts)";
+    case MOE_ERR_UNSUPPORTED: return "unsupported (dtype/itype, P or groups>64, E>1024, K>32, T*K>=2^31, more than "
+                                     "MOE_FEW_MAX_PAIRS pairs in moe_few, rank>MOE_MAX_RANK or rows too wide)";
     case MOE_ERR_ALIGNMENT: return "misaligned pointer (rows need 16 bytes, workspace 256)";
-    case MOE_ERR_WORKSPACE: return "workspace smaller than moe_workspace_size()";
+    case MOE_ERR_WORKSPACE: return "workspace smaller than the call needs (moe_workspace_size() and its like)";
     case MOE_ERR_HANDLE: return "bad handle, or a row call before moe_layout";
     case MOE_ERR_HIP: return "HIP runtime error";
     case MOE_ERR_SCRATCH:
@@ -697,6 +699,6 @@ const char* moe_strerror(int status) {
   }
 }
 
-const char* moe_version(void) { return "moe_layout 0.2 (gfx950)"; }
+const char* moe_version(void) { return "moe_layout 0.3 (gfx950)"; }
 
 }  // extern "C"

@@ -349,8 +349,9 @@ int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64
  *       groups) go to the lower index;
  *   w[t,k] = scale * s of the chosen expert, divided by the sum of the token's
  *       K chosen s if renormalize.
- * Sums and comparisons that follow arithmetic (bias, groups) are made in 64
- * bits, all others in 32.  A NaN logit counts as -inf in the choice; it makes
+ * Where values are compared after arithmetic (bias, groups) the choice is that
+ * of 64-bit arithmetic: it is made in 32 bits only where that cannot differ.
+ * Weights are computed in 32 bits.  A NaN logit counts as -inf in the choice; it makes
  * its own sigmoid weight NaN (all of the token's if renormalised) and every
  * softmax weight of its token, as +inf does in a softmax.  A token whose
  * logits are all -inf (or whose chosen scores add up to zero) gets weight zero
@@ -408,8 +409,9 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
  * other ranks' experts in an expert-parallel layer); a token without an
  * expert gets a zero row.  The same id may repeat within a token.
  * MOE_ERR_UNSUPPORTED above MOE_FEW_MAX_PAIRS pairs (larger batches go through
- * moe_layout, moe_dispatch and moe_combine), MOE_ERR_SHAPE for rows of H or I
- * that are not whole 16-byte chunks.  T = 0 is valid.  K may exceed E.       */
+ * moe_layout, moe_dispatch and moe_combine) and for H or I above 2^18,
+ * MOE_ERR_SHAPE for rows of H or I that are not whole 16-byte chunks.  T = 0
+ * is valid.  K may exceed E.                                                */
 #define MOE_FEW_MAX_PAIRS 512
 enum moe_activation { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 };
 
@@ -436,7 +438,9 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
  *   [R,r] float32, written, 16-byte aligned (rows in receive order; moe_lowrank_bwd takes it).
  * MOE_ERR_SHAPE unless the layout has K = 1 and E >= num_adapters, and rows of
  * H, N and r are whole 16-byte chunks (a smaller rank is padded with zero
- * rows); MOE_ERR_UNSUPPORTED for r > MOE_MAX_RANK.                          */
+ * rows); MOE_ERR_UNSUPPORTED for r > MOE_MAX_RANK, H or N above 2^20 or more
+ * than 2^30 receive rows.  Tokens whose id the layout found outside [0, E) are
+ * an input error there, as in every call on it.                             */
 #define MOE_MAX_RANK 128
 int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
                 int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,
@@ -456,7 +460,7 @@ int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void*
  *   grad_out [T,N], x [T,H], a, b as above, grad_x, grad_base [T,H], grad_a
  *   [num_adapters,r,H], grad_b [num_adapters,r,N] dtype; u as the forward call
  *   wrote it; grad_w [T,1] float32; workspace 16-byte aligned, R * r * 4
- *   bytes (not needed for grad_b alone).  With T = 0 grad_a and grad_b are
+ *   bytes (not needed for grad_b alone; one per call in flight).  With T = 0 grad_a and grad_b are
  *   set to zero.                                                             */
 int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, const void* x, const void* a,
                     const void* b, int num_adapters, int rank, int64_t N, const float* topk_weights,

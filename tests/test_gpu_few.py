@@ -135,6 +135,16 @@ def test_rows_around_the_output_stay_and_results_repeat():
         assert torch.equal(M.moe_few(x, idx, w, w13, w2), buf[2:8])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,E", [(512, 1, 1), (64, 8, 3), (170, 3, 40)])
+def test_many_pairs_an_expert_repeat(dtype, T, K, E):
+    """Which column of a tile a pair takes is left to chance; its values are not."""
+    args = make(T, K, E, 136, 72, dtype, 4)
+    ref = M.moe_few(*args)
+    for _ in range(20):
+        assert torch.equal(M.moe_few(*args), ref)
+
+
 def test_empty_batch():
     x, idx, w, w13, w2 = make(1, 4, 10, 88, 48, BF16, 1)
     assert M.moe_few(x[:0], idx[:0], w[:0], w13, w2).shape == (0, 88)

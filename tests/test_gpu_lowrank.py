@@ -138,6 +138,54 @@ def test_all_none_one_adapter_and_sorted(dtype):
     check(ids, E, d)
 
 
+def far_check(name, got, ref, mag, terms, dtype=BF16):
+    """got against ref (float64, on the GPU): terms * U of the sum of magnitudes,
+    the halves' 2^-16 of it, and the result's rounding."""
+    tol = mag * (2 * terms * U + 2.0 ** -16) + (torch.finfo(dtype).eps / 2 + U) * ref.abs() + 1e-30
+    tol = tol * (1 + torch.finfo(dtype).eps)
+    assert bool(((got.double() - ref).abs() <= tol).all()), name
+
+
+@pytest.mark.parametrize("wide", ["x", "out"])
+def test_rows_past_two_gib(wide):
+    """More wide rows than 32-bit offsets reach, on either side; every element is
+    checked, in blocks of tokens, with float64 on the GPU."""
+    T, A, r = 70000, 3, 8
+    H, N = (16392, 64) if wide == "x" else (64, 16392)
+    assert T * max(H, N) * 2 > 1 << 31
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = lambda *s: torch.empty(s, dtype=BF16, device=DEV).normal_(generator=g)  # noqa: E731
+    x, base, go = new(T, H), new(T, N), new(T, N)
+    a, b = new(A, r, H) * H ** -0.5, new(A, r, N) * r ** -0.5
+    ids = torch.randint(0, A + 1, (T, 1), generator=g, device=DEV).to(torch.int32)
+    h = M.moe_layout(ids, A + 1, 1)
+    out, u = M.moe_lowrank(h, x, a, b, base=base)
+    gx, ga, gb, gw = M.moe_lowrank_bwd(h, go, x, a, b, u, grad_w=True)
+    ad, bd = a.double(), b.double()
+    ra, rb = torch.zeros_like(ad), torch.zeros_like(bd)
+    ma, mb = torch.zeros_like(ad), torch.zeros_like(bd)
+    for t0 in range(0, T, 5000):
+        t1 = min(t0 + 5000, T)
+        i, xs, gs = ids[t0:t1].view(-1), x[t0:t1].double(), go[t0:t1].double()
+        for e in range(A):
+            k = torch.nonzero(i == e).view(-1)
+            xe, ge = xs[k], gs[k]
+            at, bt = ad[e].t().contiguous(), bd[e].t().contiguous()
+            ue, re = xe @ at, ge @ bt
+            um, rm = xe.abs() @ at.abs(), ge.abs() @ bt.abs()
+            far_check("out", out[t0:t1][k], base[t0:t1][k].double() + ue @ bd[e], um @ bd[e].abs(), H + r)
+            far_check("grad_x", gx[t0:t1][k], re @ ad[e], rm @ ad[e].abs(), N + r)
+            far_check("grad_w", gw[t0:t1].view(-1)[k], (ue * re).sum(1), (um * rm).sum(1), H + N + r, F32)
+            ra[e] += re.t().contiguous() @ xe
+            ma[e] += rm.t().contiguous() @ xe.abs()
+            rb[e] += ue.t().contiguous() @ ge
+            mb[e] += um.t().contiguous() @ ge.abs()
+        none = i == A
+        assert torch.equal(out[t0:t1][none], base[t0:t1][none]) and (gx[t0:t1][none] == 0).all()
+    far_check("grad_a", ga, ra, ma, N + T)
+    far_check("grad_b", gb, rb, mb, H + T)
+
+
 def test_without_weights_and_base_and_in_place():
     ids, E, d = make(70, 5, 16, 136, 72, BF16, 2, weights=False)
     h = M.moe_layout(ids, E, 1)
