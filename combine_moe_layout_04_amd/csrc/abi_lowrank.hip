@@ -36,7 +36,7 @@ extern "C" {
 int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
                 int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,
                 float* u, hipStream_t stream) {
-  int st = check_lowrank(h, dtype, H, N, num_adapters, rank);
+  const int st = check_lowrank(h, dtype, H, N, num_adapters, rank);
   if (st != MOE_OK) return st;
   if (h->T == 0) return MOE_OK;  // nothing to read or write; empty arrays may be NULL
   if (!x || !a || !b || !out || !u) return MOE_ERR_INVALID_ARG;
@@ -49,14 +49,13 @@ int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void*
   k.bank = a;
   k.u = u;
   k.wch = (int)(H * es / 16);
-  st = moe::hip_status(moe::launch_lowrank_shrink(k, stream));
-  if (st != MOE_OK) return st;
-  k.bank = b;
-  k.w = topk_weights;
-  k.base = base;
-  k.out = out;
-  k.wch = (int)(N * es / 16);
-  return moe::hip_status(moe::launch_lowrank_expand(k, stream));
+  moe::LowrankArgs wide = k;
+  wide.bank = b;
+  wide.w = topk_weights;
+  wide.base = base;
+  wide.out = out;
+  wide.wch = (int)(N * es / 16);
+  return moe::hip_status(moe::launch_lowrank_pass(k, wide, stream));
 }
 
 int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, const void* x, const void* a,
@@ -90,32 +89,32 @@ int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, 
     k.dot = grad_w;
     k.wch = nch;
     k.backward = true;
-    if ((st = moe::hip_status(moe::launch_lowrank_shrink(k, stream))) != MOE_OK) return st;
+    if (grad_x) {
+      moe::LowrankArgs wide = k;
+      wide.bank = a;
+      wide.w = nullptr;  // gu holds the weight
+      wide.base = grad_base;
+      wide.out = grad_x;
+      wide.wch = hch;
+      st = moe::hip_status(moe::launch_lowrank_pass(k, wide, stream));
+    } else {
+      st = moe::hip_status(moe::launch_lowrank_shrink(k, stream));
+    }
+    if (st != MOE_OK) return st;
   }
-  if (grad_x && h->T > 0) {
-    k.bank = a;
-    k.w = nullptr;  // gu holds the weight
-    k.u = gu;
-    k.base = grad_base;
-    k.out = grad_x;
-    k.wch = hch;
-    if ((st = moe::hip_status(moe::launch_lowrank_expand(k, stream))) != MOE_OK) return st;
-  }
-  if (grad_a) {  // also for an empty batch: zeros
-    k.rows = x;
-    k.w = nullptr;
-    k.u = gu;
-    k.out = grad_a;
-    k.wch = hch;
-    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(k, stream))) != MOE_OK) return st;
-  }
-  if (grad_b) {
-    k.rows = grad_out;
-    k.w = topk_weights;
-    k.u = const_cast<float*>(u);
-    k.out = grad_b;
-    k.wch = nch;
-    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(k, stream))) != MOE_OK) return st;
+  if (grad_a || grad_b) {  // also for an empty batch: zeros
+    moe::LowrankArgs ga = k, gb = k;
+    ga.rows = x;
+    ga.w = nullptr;  // gu holds the weight
+    ga.u = gu;
+    ga.out = grad_a;
+    ga.wch = hch;
+    gb.rows = grad_out;
+    gb.w = topk_weights;
+    gb.u = const_cast<float*>(u);
+    gb.out = grad_b;
+    gb.wch = nch;
+    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(ga, gb, stream))) != MOE_OK) return st;
   }
   return MOE_OK;
 }

@@ -41,23 +41,23 @@ struct Shape {
   static constexpr int COLS = 16 * V;             // columns of a wave's tile
 };
 
-// The tile's adapters: f(e, lo, hi) for each adapter e (or e >= A: rows
-// without one) with rows [lo, hi) in the tile, of those that fall to `slot`.
-// off: the layout's expert offsets in LDS, E + 1 of them.
+// The adapters of rows [r0, r1) (at most 64): f(e, lo, hi) for each adapter e
+// (or e >= A: rows without one) with rows [lo, hi) of them, of those that fall to
+// `slot`.  off: the layout's expert offsets in LDS, E + 1 of them.  Each lane
+// finds its row's adapter by bisection, all at once: walking the adapters of a
+// tile one after another cost 0.3 us each.
 template <typename F>
 __device__ __forceinline__ void each_adapter(const int* off, int E, int r0, int r1, int slot, int slots, F f) {
-  const int lane = lane_id();
-  int e = 0;  // the first segment that ends past r0
-  for (int i = 0; i < E; i += kWave) e += __popcll(__ballot(i + lane < E && off[i + lane + 1] <= r0));
-  int n = 0;
-  for (int lo = r0; lo < r1;) {  // wave-uniform: the same values in every lane
-    const int hi = e < E ? min(__builtin_amdgcn_readfirstlane(off[e + 1]), r1) : r1;  // behind the last segment: none
-    if (hi > lo) {
-      if (n % slots == slot) f(e, lo, hi);
-      ++n;
-      lo = hi;
-    }
-    ++e;
+  const int lane = lane_id(), p = min(r0 + lane, r1 - 1);
+  int e = 0;  // the last segment that begins at or before row p: not an empty one
+  for (int s = 1 << (31 - __builtin_clz(E)); s > 0; s >>= 1)
+    if (e + s <= E && off[e + s] <= p) e += s;
+  const int before = __shfl_up(e, 1, kWave);
+  uint64_t first = __ballot(r0 + lane < r1 && (lane == 0 || e != before));
+  for (int n = 0; first; ++n) {  // wave-uniform
+    const int i = __builtin_ctzll(first);
+    first &= first - 1;
+    if (n % slots == slot) f(read_lane_i(e, i), r0 + i, first ? r0 + (int)__builtin_ctzll(first) : r1);
   }
 }
 
@@ -96,154 +96,169 @@ struct Shrink {
   static constexpr size_t kLds = (size_t)kWaves * kRows * 128;  // at most 48 KiB
 };
 
+// Rows [lo, hi) of adapter e, of the RT tiles from r0 on; the whole workgroup.
+// t, load_t: the tokens of this lane's rows as an operand and in a load.
 template <int DT, int JT, int RT, bool FAR>
-__global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kernel(LowrankArgs a) {
+__device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, int r0, int e, int lo, int hi,
+                                            const int (&t)[RT], const int (&load_t)[2 * RT]) {
   constexpr int kShrinkWaves = Shrink<JT, RT>::kWaves, kMeet = Shrink<JT, RT>::kMeet;
   constexpr int kStaged = Shrink<JT, RT>::kStaged, kRows = Shrink<JT, RT>::kRows;
   constexpr int kDepth = JT + RT <= 2 ? 3 : JT + RT <= 4 ? 2 : 1;
-  __shared__ int off[kMaxOff];
-  extern __shared__ u32x4 lds[];  // [waves][kRows][8 chunks]; then [waves][RT][kMeet][64] to meet in
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const int col = lane & 15, q = lane >> 4;  // of an operand
   const int row8 = lane >> 3, chunk = lane & 7;  // of a load: 8 rows by one line
-  u32x4* stage = lds + (size_t)wave * kRows * 8;
-  f32x4* part = reinterpret_cast<f32x4*>(lds);
+  u32x4* stage = lds + (size_t)wave * kRows * 8;      // [kRows][8 chunks], one for each wave
+  f32x4* part = reinterpret_cast<f32x4*>(lds);        // then [waves][RT][kMeet][64] to meet in
   const int nch = a.wch, lines = (nch + 7) / 8;
   const int start = (blockIdx.x + blockIdx.y) * 5 % lines;
   const uint32_t row_bytes = (uint32_t)nch * 16;
+  bool mine[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int p = r0 + rt * kTile + col;
+    mine[rt] = p >= lo && p < hi;
+  }
+  if (e >= a.A) {  // no adapter: u = 0, and no gradient
+    for (int i = threadIdx.x; i < (hi - lo) * a.r; i += kShrinkWaves * kWave) a.u[(size_t)lo * a.r + i] = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+      if (a.dot && wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = 0.f;
+    return;
+  }
+  // the columns of other adapters (and padding) are zeros, or with FAR their own
+  // rows (padding the first one); the results are dropped either way
+  uint32_t x_off[2 * RT];
+#pragma unroll
+  for (int k = 0; k < 2 * RT; ++k) {
+    const int p = r0 + k * 8 + row8;
+    x_off[k] = p >= lo && p < hi ? (uint32_t)load_t[k] * row_bytes + chunk * 16 : kOutside;
+  }
+  const auto wide = make_rows(a.rows, FAR ? 0 : (size_t)a.T * row_bytes);
+  const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
+  const uint32_t b_off = (uint32_t)row8 * row_bytes + chunk * 16;
+  u32x4 in[kDepth][2 * (RT + JT)];
+  auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
+    const int line = i + start < lines ? i + start : i + start - lines;
+    const int c = line * 8 + chunk;
+    const bool ok = i < lines && c < nch;
+#pragma unroll
+    for (int k = 0; k < 2 * RT; ++k) {
+      if constexpr (FAR) {
+        in[d][k] = static_cast<const u32x4*>(a.rows)[(size_t)load_t[k] * nch + (ok ? c : 0)];
+        // the bank's zeros alone would leave NaN where a row holds one
+        if (!ok) in[d][k] = u32x4{0u, 0u, 0u, 0u};
+      } else {
+        in[d][k] = load_rows(wide, ok ? x_off[k] : kOutside, (uint32_t)line * 128);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2 * JT; ++k)
+      in[d][2 * RT + k] = load_rows(bank, ok ? b_off + (uint32_t)k * 8 * row_bytes : kOutside, (uint32_t)line * 128);
+  };
+  f32x4 acc[RT][JT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) {
+    fetch(d, wave + d * kShrinkWaves);
+    in_order();
+  }
+  for (int i = wave; i < lines; i += kShrinkWaves * kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      // row r's chunk c stands at place c ^ (r / 2 % 8)
+      auto put = [&](int r, const u32x4 v) { stage[r * 8 + (chunk ^ (r >> 1 & 7))] = v; };
+#pragma unroll
+      for (int k = 0; k < 2 * RT; ++k) put(k * 8 + row8, in[d][k]);
+#pragma unroll
+      for (int j0 = 0; j0 < JT; j0 += kStaged) {
+#pragma unroll
+        for (int k = 0; k < 2 * kStaged; ++k) put((2 * RT + k) * 8 + row8, in[d][2 * RT + 2 * j0 + k]);
+        if (j0 + kStaged == JT) {
+          in_order();
+          fetch(d, i + (d + kDepth) * kShrinkWaves);
+          in_order();
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int place = (s * 4 + q) ^ (col >> 1);
+          u32x4 xv[RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) xv[rt] = stage[(rt * 16 + col) * 8 + place];
+#pragma unroll
+          for (int m = 0; m < kStaged; ++m) {
+            const u32x4 bv = stage[((RT + m) * 16 + col) * 8 + place];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[rt][j0 + m] = mma_chunk<DT>(bv, xv[rt], acc[rt][j0 + m]);
+          }
+        }
+      }
+      in_order();
+    }
+  }
+  float w = 1.f, dot = 0.f;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    if (wave == rt && a.w && t[rt] >= 0) w = a.w[t[rt]];
+#pragma unroll
+  for (int first = 0; first < JT; first += kMeet) {
+    __syncthreads();  // every wave is done with its stage, or with the parts before
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int m = 0; m < kMeet; ++m) part[((wave * RT + rt) * kMeet + m) * kWave + lane] = acc[rt][first + m];
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (wave != rt) continue;
+      const size_t p = r0 + rt * kTile + col;
+#pragma unroll
+      for (int m = 0; m < kMeet; ++m) {
+        f32x4 v = part[(rt * kMeet + m) * kWave + lane];
+#pragma unroll
+        for (int k = 1; k < kShrinkWaves; ++k) v += part[((k * RT + rt) * kMeet + m) * kWave + lane];
+        const int j = (first + m) * 16 + q * 4;
+        if (mine[rt] && j < a.r) {
+          if (t[rt] < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
+          if (a.backward) {
+            if (a.dot) {
+              const f32x4 u = *reinterpret_cast<const f32x4*>(a.saved + p * a.r + j);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dot += v[i] * u[i];
+            }
+            v *= w;
+          }
+          *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = v;
+        }
+      }
+    }
+  }
+  if (a.dot) {
+    dot += __shfl_xor(dot, 16, kWave);
+    dot += __shfl_xor(dot, 32, kWave);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+      if (wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = dot;
+  }
+  __syncthreads();  // the parts have been read
+}
+
+template <int DT, int JT, int RT, bool FAR>
+__global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kernel(LowrankArgs a) {
+  __shared__ int off[kMaxOff];
+  extern __shared__ u32x4 lds[];
+  const int lane = lane_id();
   const int r0 = blockIdx.x * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
   int t[RT], load_t[2 * RT];
 #pragma unroll
-  for (int i = 0; i < 2 * RT; ++i) load_t[i] = max(row_token(a, r0 + i * 8 + row8), 0);
+  for (int i = 0; i < 2 * RT; ++i) load_t[i] = max(row_token(a, r0 + i * 8 + (lane >> 3)), 0);
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + col);
+  for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + (lane & 15));
   load_offsets(off, a);
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
-    bool mine[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int p = r0 + rt * kTile + col;
-      mine[rt] = p >= lo && p < hi;
-    }
-    if (e >= a.A) {  // no adapter: u = 0, and no gradient
-      for (int i = threadIdx.x; i < (hi - lo) * a.r; i += kShrinkWaves * kWave) a.u[(size_t)lo * a.r + i] = 0.f;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (a.dot && wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = 0.f;
-      return;
-    }
-    // columns of other adapters take their rows (padding the first one); the
-    // results are dropped
-    const auto wide = make_rows(a.rows, FAR ? 0 : (size_t)a.T * row_bytes);
-    const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
-    const uint32_t b_off = (uint32_t)row8 * row_bytes + chunk * 16;
-    u32x4 in[kDepth][2 * (RT + JT)];
-    auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
-      const int line = i + start < lines ? i + start : i + start - lines;
-      const int c = line * 8 + chunk;
-      const bool ok = i < lines && c < nch;
-#pragma unroll
-      for (int k = 0; k < 2 * RT; ++k) {
-        if constexpr (FAR) {
-          in[d][k] = static_cast<const u32x4*>(a.rows)[(size_t)load_t[k] * nch + (ok ? c : 0)];
-          // the bank's zeros alone would leave NaN where a row holds one
-          if (!ok) in[d][k] = u32x4{0u, 0u, 0u, 0u};
-        } else {
-          in[d][k] = load_rows(wide, ok ? (uint32_t)load_t[k] * row_bytes + chunk * 16 : kOutside, (uint32_t)line * 128);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2 * JT; ++k)
-        in[d][2 * RT + k] = load_rows(bank, ok ? b_off + (uint32_t)k * 8 * row_bytes : kOutside, (uint32_t)line * 128);
-    };
-    f32x4 acc[RT][JT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      fetch(d, wave + d * kShrinkWaves);
-      in_order();
-    }
-    for (int i = wave; i < lines; i += kShrinkWaves * kDepth) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        // row r's chunk c stands at place c ^ (r / 2 % 8)
-        auto put = [&](int r, const u32x4 v) { stage[r * 8 + (chunk ^ (r >> 1 & 7))] = v; };
-#pragma unroll
-        for (int k = 0; k < 2 * RT; ++k) put(k * 8 + row8, in[d][k]);
-#pragma unroll
-        for (int j0 = 0; j0 < JT; j0 += kStaged) {
-#pragma unroll
-          for (int k = 0; k < 2 * kStaged; ++k) put((2 * RT + k) * 8 + row8, in[d][2 * RT + 2 * j0 + k]);
-          if (j0 + kStaged == JT) {
-            in_order();
-            fetch(d, i + (d + kDepth) * kShrinkWaves);
-            in_order();
-          }
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int place = (s * 4 + q) ^ (col >> 1);
-            u32x4 xv[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) xv[rt] = stage[(rt * 16 + col) * 8 + place];
-#pragma unroll
-            for (int m = 0; m < kStaged; ++m) {
-              const u32x4 bv = stage[((RT + m) * 16 + col) * 8 + place];
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) acc[rt][j0 + m] = mma_chunk<DT>(bv, xv[rt], acc[rt][j0 + m]);
-            }
-          }
-        }
-        in_order();
-      }
-    }
-    float w = 1.f, dot = 0.f;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      if (wave == rt && a.w && t[rt] >= 0) w = a.w[t[rt]];
-#pragma unroll
-    for (int first = 0; first < JT; first += kMeet) {
-      __syncthreads();  // every wave is done with its stage, or with the parts before
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int m = 0; m < kMeet; ++m) part[((wave * RT + rt) * kMeet + m) * kWave + lane] = acc[rt][first + m];
-      __syncthreads();
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (wave != rt) continue;
-        const size_t p = r0 + rt * kTile + col;
-#pragma unroll
-        for (int m = 0; m < kMeet; ++m) {
-          f32x4 v = part[(rt * kMeet + m) * kWave + lane];
-#pragma unroll
-          for (int k = 1; k < kShrinkWaves; ++k) v += part[((k * RT + rt) * kMeet + m) * kWave + lane];
-          const int j = (first + m) * 16 + q * 4;
-          if (mine[rt] && j < a.r) {
-            if (t[rt] < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
-            if (a.backward) {
-              if (a.dot) {
-                const f32x4 u = *reinterpret_cast<const f32x4*>(a.saved + p * a.r + j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dot += v[i] * u[i];
-              }
-              v *= w;
-            }
-            *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = v;
-          }
-        }
-      }
-    }
-    if (a.dot) {
-      dot += __shfl_xor(dot, 16, kWave);
-      dot += __shfl_xor(dot, 32, kWave);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (wave == rt && q == 0 && mine[rt] && t[rt] >= 0) a.dot[t[rt]] = dot;
-    }
-    __syncthreads();  // the parts have been read
+    shrink_rows<DT, JT, RT, FAR>(a, lds, r0, e, lo, hi, t, load_t);
   });
 }
 
@@ -328,63 +343,39 @@ __device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const Factor<DT>
 
 // ---- expand ---------------------------------------------------------------------
 //
-// One wave per (a.tiles tiles of 16 receive rows, COLS columns, slot); it keeps
-// its columns of an adapter's bank in registers from tile to tile, and has the
-// next tile's rows of base on their way.  BLOCKS blocks of KB ranks.  The
-// products pass through LDS, so that base is read and out is written with 16
-// lanes to a row.
-constexpr int kExpandWaves = 4;
-
+// The columns of a wave: 16 chunks from c0 on.  A lane reads base and writes
+// out at chunk c0 + lane % 16 of rows lane / 16, + 4, + 8, + 12, the products pass
+// through LDS, so that 16 lanes share a row's 256 bytes.
 template <int DT, int BLOCKS>
-__global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(LowrankArgs a) {
+struct Expand {
   using S = Shape<DT>;
-  constexpr int V = S::V;
-  constexpr int kStride = 16 * V + 4;  // floats of a row in LDS: rows shifted by four banks
-  __shared__ int off[kMaxOff];
-  __shared__ __align__(16) float products[kExpandWaves][kTile * kStride];
-  const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
-  const int col = lane & 15, q = lane >> 4;
-  float* prod = products[wave];
-  const int nch = a.wch;
-  const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
-  const uint32_t row_bytes = (uint32_t)nch * 16;
-  const int my_c = c0 + col;
-  const bool in = my_c < nch;
-  // ranks and columns past the end are outside the bank and read as zeros
-  const uint32_t b_off = in ? (uint32_t)my_c * 16 : kOutside;
+  static constexpr int V = S::V;
+  static constexpr int kStride = 16 * V + 4;          // floats of a row in LDS: rows shifted by four banks
+  static constexpr int kProducts = kTile * kStride;   // floats of a wave
+  u32x4 bank[BLOCKS][V];                              // its columns of an adapter's bank, as operands
 
-  // a tile's rows: the token of row `col`, and base where this lane adds it
-  // (rows q, 4 + q, ..., chunk `col`)
-  struct Rows {
-    int t;
-    u32x4 base[4];
-  } now, next;
-  auto fetch = [&](Rows& r, int t) {
-    r.t = t;
-    if (a.base) {
+  __device__ __forceinline__ void load_bank(const LowrankArgs& a, int e, int c0) {
+    const int col = lane_id() & 15, q = lane_id() >> 4;
+    const uint32_t row_bytes = (uint32_t)a.wch * 16;
+    const auto rows = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * a.wch, (size_t)a.r * row_bytes);
+    // ranks and columns past the end are outside the bank and read as zeros
+    const uint32_t off = c0 + col < a.wch ? (uint32_t)(c0 + col) * 16 : kOutside;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int tt = max(__shfl(t, s * 4 + q, kWave), 0);
-        r.base[s] = static_cast<const u32x4*>(a.base)[(size_t)tt * nch + min(my_c, nch - 1)];
+    for (int k = 0; k < BLOCKS; ++k) {
+      u32x4 b[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int jj = k * S::KB + q * V + j;
+        b[j] = load_rows(rows, jj < a.r ? off + (uint32_t)jj * row_bytes : kOutside, 0);
       }
+      across<DT, V>(b, bank[k]);
     }
-  };
-  int tile = blockIdx.x * a.tiles;
-  const int tile_end = min(tile + a.tiles, (a.R + kTile - 1) / kTile);
-  int next_t = row_token(a, tile * kTile + col);
-  load_offsets(off, a);
-  if (c0 >= nch) return;
-  fetch(next, next_t);
-  next_t = row_token(a, (tile + 1) * kTile + col);
+  }
 
-  u32x4 bank[BLOCKS][V];
-  int held = -1;  // the adapter whose bank is held
-  for (; tile < tile_end; ++tile) {
-    now = next;
-    const int r0 = tile * kTile, r1 = min(r0 + kTile, a.R);
-    const float w = a.w ? a.w[max(now.t, 0)] : 1.f;
-    float f[BLOCKS][V];
-    const float* u = a.u + (size_t)min(r0 + col, a.R - 1) * a.r;
+  // w times row p of u, this lane's part of every block
+  static __device__ __forceinline__ void load_u(const LowrankArgs& a, int p, float w, float (&f)[BLOCKS][V]) {
+    const int q = lane_id() >> 4;
+    const float* u = a.u + (size_t)p * a.r;
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
 #pragma unroll
@@ -394,59 +385,151 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[k][j + i] = jj < a.r ? v[i] * w : 0.f;
       }
-    if (tile + 1 < tile_end) fetch(next, next_t);
-    next_t = row_token(a, (tile + 2) * kTile + col);
-    each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
+  }
+
+  static __device__ __forceinline__ void load_base(const LowrankArgs& a, int t, int c0, u32x4 (&base)[4]) {
+    const int col = lane_id() & 15, q = lane_id() >> 4;
+    if (!a.base) return;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      base[s] = static_cast<const u32x4*>(a.base)[(size_t)max(__shfl(t, s * 4 + q, kWave), 0) * a.wch + min(c0 + col, a.wch - 1)];
+  }
+
+  // Rows [lo, hi) of adapter e (e >= A: none) of the tile at r0; t: the token of
+  // row lane % 16.  The rows of other adapters are dropped.
+  __device__ __forceinline__ void rows(const LowrankArgs& a, float* prod, int r0, int e, int lo, int hi, int t, int c0,
+                                       const float (&f)[BLOCKS][V], const u32x4 (&base)[4]) const {
+    const int col = lane_id() & 15, q = lane_id() >> 4;
+    if (e < a.A) {
+      f32x4 acc[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
+      // row `col`, chunks 4q .. 4q+3
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          *reinterpret_cast<f32x4*>(prod + col * kStride + (q * 4 + s) * V + i) =
+              f32x4{acc[i][s], acc[i + 1][s], acc[i + 2][s], acc[i + 3][s]};
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int row = s * 4 + q, tt = __shfl(t, row, kWave);
+      float o[V];
+      if (a.base) unpack<DT>(base[s], o);
       if (e < a.A) {
-        if (e != held) {
-          held = e;
-          const auto rows = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
 #pragma unroll
-          for (int k = 0; k < BLOCKS; ++k) {
-            u32x4 b[V];
+        for (int i = 0; i < V; i += 4) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(prod + row * kStride + col * V + i);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const int jj = k * S::KB + q * V + j;
-              b[j] = load_rows(rows, jj < a.r ? b_off + (uint32_t)jj * row_bytes : kOutside, 0);
-            }
-            across<DT, V>(b, bank[k]);
-          }
+          for (int k = 0; k < 4; ++k) o[i + k] = a.base ? o[i + k] + v[k] : v[k];
         }
-        f32x4 acc[V];
+      } else if (!a.base) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
-        // row `col`, chunks 4q .. 4q+3
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<f32x4*>(prod + col * kStride + (q * 4 + s) * V + i) =
-                f32x4{acc[i][s], acc[i + 1][s], acc[i + 2][s], acc[i + 3][s]};
+        for (int i = 0; i < V; ++i) o[i] = 0.f;
       }
-      // the rows of other adapters are dropped
+      if (tt >= 0 && r0 + row >= lo && r0 + row < hi && c0 + col < a.wch)
+        static_cast<u32x4*>(a.out)[(size_t)tt * a.wch + c0 + col] = pack_rows<DT>(o);
+    }
+  }
+};
+
+// One wave per (a.tiles tiles of 16 receive rows, 16 chunks of columns, slot);
+// it keeps its columns of an adapter's bank in registers from tile to tile, and
+// has the next tile's rows of base on their way.  BLOCKS blocks of KB ranks.
+constexpr int kExpandWaves = 4;
+
+template <int DT, int BLOCKS>
+__global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(LowrankArgs a) {
+  using X = Expand<DT, BLOCKS>;
+  __shared__ int off[kMaxOff];
+  __shared__ __align__(16) float products[kExpandWaves][X::kProducts];
+  const int col = lane_id() & 15, wave = (int)(threadIdx.x / kWave);
+  const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
+  int tile = blockIdx.x * a.tiles;
+  const int tile_end = min(tile + a.tiles, (a.R + kTile - 1) / kTile);
+  int next_t = row_token(a, tile * kTile + col), t = next_t;
+  load_offsets(off, a);
+  if (c0 >= a.wch) return;
+  X x;
+  u32x4 base[4], next_base[4];
+  X::load_base(a, next_t, c0, next_base);
+  int after_t = row_token(a, (tile + 1) * kTile + col);
+  int held = -1;  // the adapter whose bank is held
+  for (; tile < tile_end; ++tile) {
+    t = next_t;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int row = s * 4 + q, t = __shfl(now.t, row, kWave);
-        float o[V];
-        if (a.base) unpack<DT>(now.base[s], o);
-        if (e < a.A) {
-#pragma unroll
-          for (int i = 0; i < V; i += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(prod + row * kStride + col * V + i);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[i + k] = a.base ? o[i + k] + v[k] : v[k];
-          }
-        } else if (!a.base) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = 0.f;
-        }
-        if (t >= 0 && r0 + row >= lo && r0 + row < hi && in)
-          static_cast<u32x4*>(a.out)[(size_t)t * nch + my_c] = pack_rows<DT>(o);
+    for (int s = 0; s < 4; ++s) base[s] = next_base[s];
+    const int r0 = tile * kTile, r1 = min(r0 + kTile, a.R);
+    float f[BLOCKS][X::V];
+    X::load_u(a, min(r0 + col, a.R - 1), a.w ? a.w[max(t, 0)] : 1.f, f);
+    next_t = after_t;
+    if (tile + 1 < tile_end) X::load_base(a, next_t, c0, next_base);
+    after_t = row_token(a, (tile + 2) * kTile + col);
+    each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
+      if (e < a.A && e != held) {
+        held = e;
+        x.load_bank(a, e, c0);
       }
+      x.rows(a, products[wave], r0, e, lo, hi, t, c0, f, base);
     });
   }
+}
+
+// ---- shrink and expand in one -----------------------------------------------------
+//
+// For few tokens with small banks: one workgroup per (tile, slot) does both for
+// the adapter's rows, where two launches would each pay for starting, reading
+// the offsets and the tokens.  It walks the wide columns with its own waves, so
+// it is for banks that one CU reads in the time of a launch.
+template <int DT, int JT>
+struct Both {
+  static constexpr int kBlocks = DT == kBF16 ? (JT + 1) / 2 : JT;
+  using X = Expand<DT, kBlocks>;
+  static constexpr int kWaves = Shrink<JT, 1>::kWaves;
+  static constexpr size_t kProducts = (size_t)kWaves * X::kProducts * 4;
+  static constexpr size_t kLds = Shrink<JT, 1>::kLds > kProducts ? Shrink<JT, 1>::kLds : kProducts;
+};
+
+template <int DT, int JT>
+__global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_kernel(LowrankArgs s, LowrankArgs a) {
+  using X = typename Both<DT, JT>::X;
+  constexpr int kWaves = Both<DT, JT>::kWaves;
+  __shared__ int off[kMaxOff];
+  extern __shared__ u32x4 lds[];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+  const int r0 = blockIdx.x * kTile, r1 = min(r0 + kTile, a.R);
+  int t[1], load_t[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_t[i] = max(row_token(a, r0 + i * 8 + (lane >> 3)), 0);
+  t[0] = row_token(a, r0 + (lane & 15));
+  load_offsets(off, a);
+  float* prod = reinterpret_cast<float*>(lds) + (size_t)wave * X::kProducts;
+  each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
+    // the first columns' bank and base, which do not wait for u, are asked for ahead
+    X x;
+    u32x4 base[4];
+    int c0 = wave * 16;
+    if (c0 < a.wch) {
+      if (e < a.A) x.load_bank(a, e, c0);
+      X::load_base(a, t[0], c0, base);
+    }
+    shrink_rows<DT, JT, 1, false>(s, lds, r0, e, lo, hi, t, load_t);
+    __syncthreads();  // u is written
+    float f[Both<DT, JT>::kBlocks][X::V];
+    X::load_u(a, min(r0 + (lane & 15), a.R - 1), a.w ? a.w[max(t[0], 0)] : 1.f, f);
+    while (c0 < a.wch) {
+      x.rows(a, prod, r0, e, lo, hi, t[0], c0, f, base);
+      c0 += kWaves * 16;
+      if (c0 < a.wch) {
+        if (e < a.A) x.load_bank(a, e, c0);
+        X::load_base(a, t[0], c0, base);
+      }
+    }
+    __syncthreads();  // the next adapter's stages take the products' place
+  });
 }
 
 // ---- gradients of the adapters ---------------------------------------------------
@@ -460,8 +543,18 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
 // twice what the wide rows do.  An adapter without rows gets zeros.
 constexpr int kWgradWaves = 8;
 
+// What the gradients of a and of b, in one launch, do not share.
+struct WgradSide {
+  const void* rows;
+  const float* w;
+  const float* u;
+  void* out;
+  int wch;
+};
+
 template <int DT, int JT>
-__global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a) {
+__global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a, WgradSide one, WgradSide two,
+                                                                  int one_blocks) {
   using S = Shape<DT>;
   constexpr int V = S::V;
   constexpr int kStride = JT * 16 + 4;                  // floats of a row of u in LDS
@@ -474,10 +567,16 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
   const int col = lane & 15, q = lane >> 4;
   const int e = blockIdx.y;
-  const int nch = a.wch;
+  const bool second = (int)blockIdx.x >= one_blocks;
+  const int block = second ? blockIdx.x - one_blocks : blockIdx.x;
+  const u32x4* rows = static_cast<const u32x4*>(second ? two.rows : one.rows);
+  const float* weights = second ? two.w : one.w;
+  const float* u_rows = second ? two.u : one.u;
+  u32x4* out = static_cast<u32x4*>(second ? two.out : one.out);
+  const int nch = second ? two.wch : one.wch;
   const int parts = (a.r + 16 * JT - 1) / (16 * JT);
-  const int c0 = blockIdx.x / parts * 16;
-  const int j0 = blockIdx.x % parts * JT * 16;
+  const int c0 = block / parts * 16;
+  const int j0 = block % parts * JT * 16;
   const int c = min(c0 + col, nch - 1);  // chunks past the end repeat the last and are not stored
   const int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
   f32x4 acc[JT][V];
@@ -498,13 +597,13 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   auto fetch = [&](int p0) {  // the rows whose tokens are in t
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      x[k] = static_cast<const u32x4*>(a.rows)[(size_t)max(__shfl(t, q * V + k, kWave), 0) * nch + c];
+      x[k] = rows[(size_t)max(__shfl(t, q * V + k, kWave), 0) * nch + c];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = i * kWave + lane, row = at / (JT * 4), j = j0 + at % (JT * 4) * 4;
-      u[i] = *reinterpret_cast<const f32x4*>(a.u + (size_t)min(p0 + row, hi - 1) * a.r + min(j, a.r - 4));
+      u[i] = *reinterpret_cast<const f32x4*>(u_rows + (size_t)min(p0 + row, hi - 1) * a.r + min(j, a.r - 4));
     }
-    if (a.w) w = a.w[max(t, 0)];
+    if (weights) w = weights[max(t, 0)];
   };
   constexpr int kStep = kWgradWaves * S::KB;
   int p0 = lo + wave * S::KB;
@@ -530,7 +629,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         there[k] = __shfl(t, q * V + k, kWave) >= 0;
-        wk[k] = a.w ? __shfl(w, q * V + k, kWave) : 1.f;
+        wk[k] = weights ? __shfl(w, q * V + k, kWave) : 1.f;
         z[k] = there[k] ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
       }
       across<DT, V>(z, o);
@@ -563,7 +662,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
         for (int k = 1; k < kWgradWaves; ++k) o[i] += f[(size_t)k * V * kWave * 4];
       }
       const int cc = c0 + q * 4 + wave;
-      if (j < a.r && cc < nch) static_cast<u32x4*>(a.out)[((size_t)e * a.r + j) * nch + cc] = pack_rows<DT>(o);
+      if (j < a.r && cc < nch) out[((size_t)e * a.r + j) * nch + cc] = pack_rows<DT>(o);
     }
   }
 }
@@ -573,6 +672,14 @@ hipError_t launched(F f) {
   f();
   return hipGetLastError();
 }
+
+// lowrank_both_kernel is taken up to so many tiles of rows and bytes of one
+// adapter's two banks (us a pass in bfloat16, one launch against two: 256 tokens,
+// 512 columns, rank 64, 128 KiB 9.3 against 11.0; 48 tokens, 2048 columns, rank
+// 16, 128 KiB 10.9 against 11.5; 48 tokens, 4096 columns, 256 KiB 15.5 against
+// 12.4; 1024 tokens, 1024 columns, rank 8, 32 KiB 8.1 against 9.9).
+constexpr int kBothTiles = 64;
+constexpr int64_t kBothBank = 128 << 10;
 
 int slots_for(int64_t workgroups, int E) {  // adapters of a tile side by side while workgroups are few
   int s = 1;
@@ -637,17 +744,46 @@ hipError_t launch_lowrank_expand(const LowrankArgs& args, hipStream_t s) {
 #undef MOE_EXPAND
 }
 
-hipError_t launch_lowrank_wgrad(const LowrankArgs& a, hipStream_t s) {
-  const dim3 block(kWgradWaves * kWave);
-  const int cols = (a.wch + 15) / 16;
-#define MOE_WGRAD(J)                                                                                   \
-  return launched([&] {                                                                                \
-    const dim3 grid(cols * ((a.r + 16 * J - 1) / (16 * J)), a.A);                                      \
-    if (a.dtype == MOE_F32) hipLaunchKernelGGL((wgrad_kernel<kF32, J>), grid, block, 0, s, a);         \
-    else hipLaunchKernelGGL((wgrad_kernel<kBF16, J>), grid, block, 0, s, a);                           \
+// Both steps of a pass: u = rows -> rank with `s`, then rank -> rows with `a`
+// (which reads s.u), in one launch where that is the faster.
+hipError_t launch_lowrank_pass(const LowrankArgs& s, const LowrankArgs& a, hipStream_t stream) {
+  const int tiles = (s.R + kTile - 1) / kTile;
+  const int64_t bank = (int64_t)s.r * ((int64_t)s.wch + a.wch) * 16;
+  const bool far = (int64_t)s.T * s.wch * 16 >= (int64_t(1) << 31);
+  if (!far && tiles <= kBothTiles && bank <= kBothBank) {
+    const dim3 grid(tiles, slots_for(tiles, s.E));
+#define MOE_BOTH(J)                                                                                           \
+  return launched([&] {                                                                                       \
+    const dim3 f32((Both<kF32, J>::kWaves * kWave)), bf16((Both<kBF16, J>::kWaves * kWave));                  \
+    if (s.dtype == MOE_F32)                                                                                   \
+      hipLaunchKernelGGL((lowrank_both_kernel<kF32, J>), grid, f32, (Both<kF32, J>::kLds), stream, s, a);     \
+    else                                                                                                      \
+      hipLaunchKernelGGL((lowrank_both_kernel<kBF16, J>), grid, bf16, (Both<kBF16, J>::kLds), stream, s, a);  \
   })
-  if (a.r <= 16) MOE_WGRAD(1);
-  MOE_WGRAD(2);
+    if (s.r <= 16) MOE_BOTH(1);
+    if (s.r <= 32) MOE_BOTH(2);
+    if (s.r <= 64) MOE_BOTH(4);
+    MOE_BOTH(8);
+#undef MOE_BOTH
+  }
+  const hipError_t e = launch_lowrank_shrink(s, stream);
+  return e != hipSuccess ? e : launch_lowrank_expand(a, stream);
+}
+
+// grad_a from `a` and grad_b from `b`, where their out is not null.
+hipError_t launch_lowrank_wgrad(const LowrankArgs& a, const LowrankArgs& b, hipStream_t s) {
+  const int width = a.r <= 16 ? 16 : 32;  // ranks of a workgroup
+  auto blocks = [&](const LowrankArgs& k) { return k.out ? (k.wch + 15) / 16 * ((k.r + width - 1) / width) : 0; };
+  const WgradSide one{a.rows, a.w, a.u, a.out, a.wch}, two{b.rows, b.w, b.u, b.out, b.wch};
+  const dim3 grid(blocks(a) + blocks(b), a.A), block(kWgradWaves * kWave);
+#define MOE_WGRAD(D, J) \
+  return launched([&] { hipLaunchKernelGGL((wgrad_kernel<D, J>), grid, block, 0, s, a, one, two, blocks(a)); })
+  if (width == 16) {
+    if (a.dtype == MOE_F32) MOE_WGRAD(kF32, 1);
+    MOE_WGRAD(kBF16, 1);
+  }
+  if (a.dtype == MOE_F32) MOE_WGRAD(kF32, 2);
+  MOE_WGRAD(kBF16, 2);
 #undef MOE_WGRAD
 }
 

@@ -95,7 +95,8 @@ def check(ids, E, d, pad=1):
 
 SHAPES = [(1, 1, 8, 64, 64), (1, 40, 16, 2048, 96), (3, 2, 8, 8, 8), (17, 3, 24, 136, 264), (64, 32, 16, 256, 512),
           (100, 7, 40, 1000, 72), (333, 5, 64, 520, 1032), (1000, 1, 128, 128, 192), (257, 200, 8, 64, 40),
-          (2000, 11, 32, 264, 136), (50, 1000, 16, 32, 24), (130, 4, 72, 96, 4096), (77, 6, 96, 168, 64)]
+          (2000, 11, 32, 264, 136), (50, 1000, 16, 32, 24), (130, 4, 72, 96, 4096), (77, 6, 96, 168, 64),
+          (60, 3, 128, 64, 72), (500, 9, 32, 520, 264), (18, 900, 16, 128, 1032), (200, 2, 120, 40, 328)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
