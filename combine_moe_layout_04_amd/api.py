@@ -613,11 +613,11 @@ def moe_lowrank(handle: Handle, x: torch.Tensor, a: torch.Tensor, b: torch.Tenso
     if base is not None:
         _need(base, "base", dev, (h.T, N), x.dtype)
     if out is None:
-        out = torch.empty((h.T, N), dtype=x.dtype, device=dev)
+        out = x.new_empty((h.T, N)) if base is None else torch.empty_like(base)
     else:
         _need(out, "out", dev, (h.T, N), x.dtype)
     if u is None:
-        u = torch.empty((h.R, r), dtype=torch.float32, device=dev)
+        u = x.new_empty((h.R, r), dtype=torch.float32)
     else:
         _need(u, "u", dev, (h.R, r), torch.float32)
     _run(dev, "moe_lowrank", h.ptr, x.data_ptr(), dt, H, a.data_ptr(), b.data_ptr(), A, r, N, _ptr(topk_weights),
@@ -646,20 +646,25 @@ def moe_lowrank_bwd(handle: Handle, grad_out: torch.Tensor, x: torch.Tensor, a: 
     if grad_base is not None:
         _need(grad_base, "grad_base", dev, (T, H), dtype)
 
-    def given(t, name, shape, dtype):
+    def given(t, name, like):  # a gradient has the shape and type of what it belongs to
         if t is False:
             return None
         if t is None or t is True:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        _need(t, name, dev, shape, dtype)
+            return torch.empty_like(like)
+        _need(t, name, dev, tuple(like.shape), like.dtype)
         return t
 
-    grad_x = given(grad_x, "grad_x", (T, H), dtype)
-    grad_a = given(grad_a, "grad_a", (A, r, H), dtype)
-    grad_b = given(grad_b, "grad_b", (A, r, N), dtype)
-    grad_w = given(grad_w, "grad_w", (T, 1), torch.float32)
+    grad_x = given(grad_x, "grad_x", x)
+    grad_a = given(grad_a, "grad_a", a)
+    grad_b = given(grad_b, "grad_b", b)
+    if grad_w is None or grad_w is True:
+        grad_w = u.new_empty((T, 1))
+    elif grad_w is False:
+        grad_w = None
+    else:
+        _need(grad_w, "grad_w", dev, (T, 1), torch.float32)
     if workspace is None:
-        workspace = torch.empty(h.R * r, dtype=torch.float32, device=dev)
+        workspace = torch.empty_like(u)
     else:
         _need(workspace, "workspace", dev)
     _run(dev, "moe_lowrank_bwd", h.ptr, grad_out.data_ptr(), dt, H, x.data_ptr(), a.data_ptr(), b.data_ptr(), A, r, N,
