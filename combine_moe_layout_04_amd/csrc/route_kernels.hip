@@ -17,7 +17,7 @@
 // sums) are formed in 32 bits first; a token whose choice hangs on a difference
 // that the rounding could have turned is chosen again in 64 bits, so that a
 // choice next to a border is the definition's (16384 tokens, 256 experts: 28 us
-// in 64 bits throughout, NEW_US so).
+// in 64 bits throughout, 21 so).
 //
 // Logits that are NaN count as -inf in the choice and spread to the weights
 // as the formulas say.  A sum of scores that is zero (every expert masked by
@@ -237,11 +237,16 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // k gets the k-th expert.  L lanes (a power of two) hold one group's experts, g
 // and l are the lane's group and place.  In float, `sure` says whether every
 // comparison that the choice hangs on was of values further apart than their
-// errors: scores are within 2^-18 of the true ones (u = 2^-24: a sigmoid within
-// 5 u; a softmax's numerator within 0.37 u from the rounded difference and 2 u
-// of itself, its sum of at most 32 terms a lane within 38 u of itself), and a
-// bias adds u times the value.  Two values are told apart from 2^-16 on, group
-// sums from 2^-15, times the largest value where that is above 1.
+// errors (u = 2^-24; a bias adds u times the largest value, `far`):
+//   softmax: scores within 41 u of the largest one, 1 / all (the numerator within
+//     0.37 u from the rounded difference and 2 u of itself, a sum of at most 32
+//     terms a lane within 38 u of itself, the division), so two values are told
+//     apart from 2^-17 / all + 2^-22 far on;
+//   sigmoid: within 4 u (the fast exponential of -z within (2 + |z|) u of itself,
+//     the reciprocal and the sum before it within 3 u; s (1 - s) |z| is at most
+//     0.23), so two values with their biases are off by less than 10 u times
+//     the larger of far and 1, and told apart from 2^-20 times it on.
+// Group sums count twice that.
 template <typename R, int VPL>
 __device__ __forceinline__ int choose_scored(const RouteArgs& a, const float (&z)[VPL], const float (&bias)[VPL], int g,
                                              int l, bool& sure, R& m, R& all) {
@@ -276,9 +281,12 @@ __device__ __forceinline__ int choose_scored(const RouteArgs& a, const float (&z
     for (int v = 0; v < VPL; ++v) c[v] /= all;
   } else {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) c[v] = sigmoid(c[v]);
+    for (int v = 0; v < VPL; ++v) {
+      if constexpr (kExact) c[v] = sigmoid(c[v]);
+      else c[v] = __builtin_amdgcn_rcpf(1.f + __expf(-c[v]));
+    }
   }
-  R far = 1;  // the size that a bias's rounding goes by
+  R far = softmax ? 0 : 1;  // the size that a bias's rounding goes by
 #pragma unroll
   for (int v = 0; v < VPL; ++v)
     if (there[v]) {
@@ -291,8 +299,8 @@ __device__ __forceinline__ int choose_scored(const RouteArgs& a, const float (&z
     }
   R near = 0;  // two values closer than this are not told apart
   if constexpr (!kExact) {
-    far = __uint_as_float(wave_max(__float_as_uint((float)far)));  // above 0: ordered like its bits
-    near = far * 0x1p-16f;
+    far = __uint_as_float(wave_max(__float_as_uint((float)far)));  // not below 0: ordered like its bits
+    near = softmax ? 0x1p-17f / all + 0x1p-22f * far : 0x1p-20f * far;
   }
   sure = true;
   bool open = g < a.groups;

@@ -99,7 +99,8 @@ def test_choice_and_weights(dtype, T, E, K, score, renormalize):
 @pytest.mark.parametrize("T,E,K,groups,keep,bias", [
     (64, 256, 8, 8, 4, True), (33, 128, 6, 4, 1, False), (9, 60, 4, 3, 2, True), (17, 64, 8, 64, 9, True),
     (5, 1023, 7, 33, 4, True), (12, 1024, 16, 16, 16, True), (31, 40, 5, 1, 1, True), (3, 992, 32, 31, 2, False),
-    (2, 1, 1, 1, 1, True)])
+    (2, 1, 1, 1, 1, True), (101, 64, 8, 1, 1, True), (50, 256, 15, 16, 8, True), (1000, 128, 8, 1, 1, True),
+    (333, 256, 8, 8, 4, False), (5, 64, 3, 4, 2, True), (1, 256, 15, 1, 1, True), (19, 64, 4, 16, 16, True)])
 def test_bias_and_groups(dtype, score, T, E, K, groups, keep, bias):
     z = draw(T, E, dtype, T + E, 2.0)
     b = torch.randn(E, generator=torch.Generator().manual_seed(7)).mul_(0.1).to(DEV) if bias else None
@@ -119,18 +120,22 @@ def test_ties_go_to_the_lower_index(dtype, E):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
-def test_choices_next_to_a_border(score, groups, keep):
+@pytest.mark.parametrize("E,groups,keep", [(96, 1, 1), (96, 8, 3), (128, 1, 1), (128, 8, 3)])
+def test_choices_next_to_a_border(score, E, groups, keep):
     """Biases that lift every expert to the same value but for their own float32
     rounding: only 64 bits tell the experts (and groups) apart, and the choice
     has to be the one that they tell."""
     for seed in range(40):
-        z = draw(1, 96, F32, seed, 1.5)
+        z = draw(1, E, F32, seed, 1.5)
         s = scores64(z.cpu().numpy(), score)[0]
         b = torch.from_numpy((1.0 - s).astype(np.float32)).to(DEV)
         spread = np.abs(s + b.double().cpu().numpy() - 1.0).max()
         assert 0 < spread < 2.0 ** -24
         check(z, 6, score, True, 1.0, b, groups, keep)
+        # among tokens that are told apart easily
+        rows = draw(7, E, F32, 1000 + seed, 1.5)
+        rows[seed % 7] = z[0]
+        check(rows, 6, score, True, 1.0, b, groups, keep)
 
 
 def test_masked_rows_and_nan():
@@ -150,6 +155,8 @@ def test_masked_rows_and_nan():
     zero = torch.zeros(96, device=DEV)
     for score in ("softmax", "sigmoid"):
         check(z, 8, score, True, 1.0, zero, 8, 3)
+        check(torch.cat([z, z[:, :32]], 1), 8, score, True, 1.0, torch.zeros(128, device=DEV), 8, 3)
+        check(torch.cat([z, z[:, :32]], 1), 8, score, False, 1.0, torch.zeros(128, device=DEV))
     _, w = M.moe_route(z, 8, score="softmax")
     assert (w[0] == 0).all() and torch.isnan(w[2]).all() and not torch.isnan(w[3:5]).any()
 
