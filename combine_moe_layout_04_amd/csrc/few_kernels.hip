@@ -97,7 +97,8 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
 //
 // What decides how near to the memory's rate this comes (64 tokens, 126 experts
 // of 768 columns and rows of 4 KiB, 0.79 GB):
-//   - the order of lanes in a load (mfma.h): BEFORE -> AFTER us;
+//   - the order of lanes in a load (mfma.h): 134 -> 125 us, the last of the three,
+//     6.3 TB/s;
 //   - workgroup b takes items b, b + grid, ..., so that all of them together
 //     move through a narrow window of the weights: 164 us with even runs of
 //     neighbouring items, 140 us in steps;
@@ -251,7 +252,7 @@ constexpr int kDownWaves = 16;
 
 template <int DT, int NT>
 __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
-  constexpr int kDepth = NT <= 2 ? 3 : 1;
+  constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 269, 256, 264 us a call with 1, 2, 3
   __shared__ Groups groups;
   __shared__ float weight[kFewMaxPairs];
   __shared__ uint8_t here[kFewMaxPairs];
@@ -388,10 +389,16 @@ hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
 
 template <int DT>
 hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
-  // pairs a chosen expert has on average, if the choice is even
+  // By the pairs an expert of the call has on average.  More tiles read fewer
+  // weights twice and multiply more zeros, which float32's matrix rate feels
+  // first (2048 x 768, 32 experts of all that are chosen from; us with 1, 2, 3, 4
+  // tiles.  bfloat16, 2 pairs: 44 44 46 48, 4: 68 55 55 61, 8: 108 75 64 66, 16:
+  // 190 123 105 98; float32, 2: 100 105 137 171, 4: 126 112 146 176, 8: 221 159
+  // 158 180, 16: 404 279 270 297).
   if (a.pairs <= 2 * a.E) return launch_few_typed<DT, 1>(a, s);
-  if (a.pairs <= 5 * a.E) return launch_few_typed<DT, 2>(a, s);
-  return launch_few_typed<DT, 8>(a, s);
+  if (a.pairs <= (DT == kF32 ? 8 : 4) * a.E) return launch_few_typed<DT, 2>(a, s);
+  if (DT == kF32 || a.pairs <= 8 * a.E) return launch_few_typed<DT, 3>(a, s);
+  return launch_few_typed<DT, 4>(a, s);
 }
 
 }  // namespace
