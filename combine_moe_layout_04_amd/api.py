@@ -451,15 +451,17 @@ _ROUTE_OPTIONS = {}  # options -> the struct the library reads (a handful in any
 
 
 def _route_options(score, renormalize, num_groups, topk_groups, scale):
-    key = (score, renormalize, num_groups, topk_groups, scale)
+    # plain values, so that a changed tensor or array is not taken for what it was
+    key = (score, bool(renormalize), int(num_groups), int(topk_groups), float(scale))
     o = _ROUTE_OPTIONS.get(key)
     if o is None:
         if score not in SCORES:
             raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+        if not 0 <= key[2] < 2 ** 31 or not 0 <= key[3] < 2 ** 31:
+            raise ValueError(f"num_groups and topk_groups are no counts: {num_groups}, {topk_groups}")
         if len(_ROUTE_OPTIONS) >= 256:
             _ROUTE_OPTIONS.clear()
-        o = _ROUTE_OPTIONS[key] = ctypes.byref(MoeRouteOptions(
-            SCORES[score], int(bool(renormalize)), int(num_groups), int(topk_groups), float(scale)))
+        o = _ROUTE_OPTIONS[key] = ctypes.byref(MoeRouteOptions(SCORES[score], int(key[1]), *key[2:]))
     return o
 
 

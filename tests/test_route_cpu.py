@@ -18,7 +18,7 @@ CASES = [
     (dict(T=-1), {}, "MOE_ERR_INVALID_ARG"), (dict(K=0), {}, "MOE_ERR_SHAPE"), (dict(K=17), {}, "MOE_ERR_SHAPE"),
     (dict(E=0), {}, "MOE_ERR_SHAPE"), (dict(E=1025), {}, "MOE_ERR_UNSUPPORTED"),
     (dict(E=64, K=33), {}, "MOE_ERR_UNSUPPORTED"), (dict(T=1 << 31), {}, "MOE_ERR_UNSUPPORTED"),
-    (dict(T=1 << 29), {}, "MOE_ERR_UNSUPPORTED"), (dict(dtype=2), {}, "MOE_ERR_UNSUPPORTED"),
+    (dict(T=1 << 29), {}, "MOE_ERR_UNSUPPORTED"), (dict(T=1 << 26, K=1), {}, "MOE_ERR_UNSUPPORTED"), (dict(dtype=2), {}, "MOE_ERR_UNSUPPORTED"),
     ({}, dict(score=2), "MOE_ERR_INVALID_ARG"), ({}, dict(renormalize=2), "MOE_ERR_INVALID_ARG"),
     ({}, dict(scale=float("nan")), "MOE_ERR_INVALID_ARG"), ({}, dict(num_groups=0), "MOE_ERR_SHAPE"),
     ({}, dict(num_groups=4, topk_groups=5), "MOE_ERR_SHAPE"), ({}, dict(num_groups=3), "MOE_ERR_SHAPE"),
@@ -45,3 +45,19 @@ def test_route_null_options_bias_and_empty(L):  # noqa: F811
     assert L.moe_route_bwd(FAKE, 0, 4, 16, 4, options(), FAKE, FAKE, None, None) == C["MOE_ERR_INVALID_ARG"]
     assert L.moe_route(None, 0, 0, 16, 4, options(), None, None, None, None) == C["MOE_OK"]
     assert L.moe_route_bwd(None, 0, 0, 16, 4, options(), None, None, None, None) == C["MOE_OK"]
+
+
+def test_options_go_by_value():
+    import torch
+    from combine_moe_layout_04_amd import api
+
+    def scale(o):
+        return o._obj.scale
+
+    s = torch.tensor(1.5)
+    assert scale(api._route_options("softmax", True, 1, 1, s)) == 1.5
+    s += 1
+    assert scale(api._route_options("softmax", True, 1, 1, s)) == 2.5
+    for bad in (2 ** 32 + 1, -1):
+        with pytest.raises(ValueError):
+            api._route_options("softmax", True, bad, 1, 1.0)
