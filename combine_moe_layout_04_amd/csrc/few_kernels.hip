@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
       x_off[c] = (uint32_t)(list[min(first + c * 4 + at.row, n - 1)] / a.K) * row_bytes + at.chunk * 16;
   };
   auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
-    const int line = i + start < lines ? i + start : i + start - lines;
+    const int line = i >= lines ? 0 : i + start < lines ? i + start : i + start - lines;
     const bool in = i < lines && line * 16 + at.chunk < nch;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -293,8 +293,9 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     for (int c = 0; c < NT; ++c)
       m_off[c] = (uint32_t)list[min(first + c * 4 + at.row, n - 1)] * row_bytes + at.chunk * 16;
   };
-  auto fetch = [&](int d, int line) {
-    const bool in = line < hi && line * 16 + at.chunk < nch;
+  auto fetch = [&](int d, int i) {  // past the part's last line: zeros
+    const int line = min(i, hi - 1);
+    const bool in = i < hi && line * 16 + at.chunk < nch;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       w[d][r] = load_rows<true>(w2, in ? w_off + r * 4 * row_bytes : kOutside, (uint32_t)line * 256);

@@ -49,7 +49,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rows(const void* p, size_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
 }
 
-// The chunk at byte `lane_off` (per lane) + `off` (uniform).  ONCE: read by
+// The chunk at byte `lane_off` (per lane) + `off` (uniform, inside the buffer:
+// it is the lane's part that is held against the end).  ONCE: read by
 // nobody else, so marked non-temporal; that pays only where one instruction
 // takes whole 128-byte lines.
 template <bool ONCE = false>
