@@ -11,7 +11,7 @@ int check_lowrank(const moe_handle_s* h, int dtype, int64_t H, int64_t N, int A,
   if (eb == 0) return MOE_ERR_UNSUPPORTED;
   if (h->K != 1 || A < 1 || A > h->E || r < 1 || H < 1 || N < 1) return MOE_ERR_SHAPE;
   if (r > MOE_MAX_RANK || H > (int64_t(1) << 20) || N > (int64_t(1) << 20)) return MOE_ERR_UNSUPPORTED;
-  if (h->R > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;  // the kernels look a few tiles past a row in 32 bits
+  if (h->R > (int64_t(1) << 26)) return MOE_ERR_UNSUPPORTED;  // 32 threads a row: a grid has fewer than 2^32
   if ((H * eb) % 16 != 0 || (N * eb) % 16 != 0 || (r * eb) % 16 != 0) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

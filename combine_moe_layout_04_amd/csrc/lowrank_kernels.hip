@@ -43,10 +43,11 @@ struct Shape {
 };
 
 // The adapters of rows [r0, r1) (at most 64): f(e, lo, hi) for each adapter e
-// (or e >= A: rows without one) with rows [lo, hi) of them, of those that fall to
-// `slot`.  off: the layout's expert offsets in LDS, E + 1 of them.  Each lane
-// finds its row's adapter by bisection, all at once: walking the adapters of a
-// tile one after another cost 0.3 us each.
+// (or A <= e < E: rows without one) with rows [lo, hi) of them, of those that fall
+// to `slot`.  Rows after the last segment belong to nobody, and what the layout
+// holds for them is not defined: they are left out.  off: the layout's expert
+// offsets in LDS, E + 1 of them.  Each lane finds its row's adapter by bisection,
+// all at once: walking the adapters of a tile one after another cost 0.3 us each.
 template <typename F>
 __device__ __forceinline__ void each_adapter(const int* off, int E, int r0, int r1, int slot, int slots, F f) {
   const int lane = lane_id(), p = min(r0 + lane, r1 - 1);
@@ -58,6 +59,7 @@ __device__ __forceinline__ void each_adapter(const int* off, int E, int r0, int 
   for (int n = 0; first; ++n) {  // wave-uniform
     const int i = __builtin_ctzll(first);
     first &= first - 1;
+    if (read_lane_i(e, i) == E) return;
     if (n % slots == slot) f(read_lane_i(e, i), r0 + i, first ? r0 + (int)__builtin_ctzll(first) : r1);
   }
 }
@@ -141,7 +143,7 @@ __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, in
   const uint32_t b_off = (uint32_t)row8 * row_bytes + chunk * 16;
   u32x4 in[kDepth][2 * (RT + JT)];
   auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
-    const int line = i + start < lines ? i + start : i + start - lines;
+    const int line = i >= lines ? 0 : i + start < lines ? i + start : i + start - lines;
     const int c = line * 8 + chunk;
     const bool ok = i < lines && c < nch;
 #pragma unroll

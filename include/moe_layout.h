@@ -370,8 +370,8 @@ typedef struct moe_route_options {
  * element's), bias [E] float32 or NULL; topk_idx [T,K] int32 and topk_weights
  * [T,K] float32 are written.  MOE_ERR_INVALID_ARG for options out of range,
  * MOE_ERR_SHAPE for K > E, groups that do not divide E or hold fewer than K
- * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above.  T = 0 is
- * valid.                                                                     */
+ * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above and from 2^26
+ * tokens on.  T = 0 is valid.                                                */
 int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
               const float* bias, int32_t* topk_idx, float* topk_weights, hipStream_t stream);
 
@@ -439,8 +439,10 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
  * MOE_ERR_SHAPE unless the layout has K = 1 and E >= num_adapters, and rows of
  * H, N and r are whole 16-byte chunks (a smaller rank is padded with zero
  * rows); MOE_ERR_UNSUPPORTED for r > MOE_MAX_RANK, H or N above 2^20 or more
- * than 2^30 receive rows.  Tokens whose id the layout found outside [0, E) are
- * an input error there, as in every call on it.                             */
+ * than 2^26 receive rows.  A token whose id the layout found outside [0, E) is
+ * an input error there; its rows of out (and of grad_x and grad_w below) are
+ * not written, and the other tokens' are what they would be without it.  Rows
+ * of u past expert_offset[E] are not written.                               */
 #define MOE_MAX_RANK 128
 int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
                 int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,

@@ -288,6 +288,30 @@ def test_empty_batch():
     assert gx.shape == (0, 16) and (ga == 0).all() and (gb == 0).all()
 
 
+@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ids_outside_the_layout_touch_no_other_token(dtype, T):
+    ids, E, d = make(T, 6, 16, 256, 264, dtype, 8)
+    h = M.Handle()
+    M.moe_layout(ids, E, 1, handle=h)  # leaves every row's token behind
+    bad = ids.clone()
+    off = torch.arange(T, device=DEV) % 3 == 0
+    bad[off] = E
+    bad[0] = -1
+    M.moe_layout(bad, E, 1, handle=h)
+    ref = reference(torch.where(off.view(-1, 1), E, ids), d)
+    out, gx = torch.full_like(d["base"], 7), torch.full_like(d["x"], 7)
+    gw = torch.full((T, 1), 7.0, device=DEV)
+    _, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"], out=out)
+    _, ga, gb, _ = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_base=d["gbase"], grad_x=gx, grad_w=gw)
+    keep = ~off.cpu()
+    for n, t in (("out", out), ("grad_x", gx), ("grad_w", gw)):
+        near(t[~off], tuple(v[keep] for v in ref[n]), n)
+        assert (t[off] == 7).all()
+    near(ga, ref["grad_a"], "grad_a")
+    near(gb, ref["grad_b"], "grad_b")
+
+
 def test_results_repeat_and_neighbours_stay():
     ids, E, d = make(700, 6, 32, 264, 520, BF16, 3)
     h, u, out, got = check(ids, E, d)
