@@ -84,6 +84,17 @@ def test_against_the_formula(dtype, act, T, K, E, H, I):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,E", [(16, 2, 16), (17, 2, 16), (32, 2, 16), (33, 2, 16), (64, 2, 16), (65, 2, 16)])
+def test_both_sides_of_the_borders_between_tile_counts(dtype, T, K, E):
+    """2, 4 and 8 pairs an expert; experts whose load is far from the average among them."""
+    x, idx, w, w13, w2 = make(T, K, E, 328, 136, dtype, T)
+    compare(x, idx, w, w13, w2)
+    idx[:, 0] = 3
+    idx[0, 0], idx[1, 0] = 4, -1
+    compare(x, idx, w, w13, w2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("itype", [torch.int32, torch.int64])
 def test_ids_outside_the_experts_add_nothing(dtype, itype):
     x, idx, w, w13, w2 = make(20, 4, 12, 64, 40, dtype, 3, itype, of=48)
