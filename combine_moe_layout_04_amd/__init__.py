@@ -28,6 +28,7 @@ from .api import (  # noqa: F401
     moe_few,
     moe_lowrank,
     moe_lowrank_bwd,
+    moe_lowrank_bwd_workspace_size,
     moe_few_workspace_size,
     FEW_MAX_PAIRS,
 )

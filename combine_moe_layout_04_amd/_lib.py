@@ -62,6 +62,8 @@ SIGNATURES = {
                         c_void_p, c_int, c_int64, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_lowrank": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p, c_int, c_int, c_int64,
                             c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_lowrank_bwd_workspace_size": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int, c_int,
+                                               ctypes.POINTER(c_size_t)]),
     "moe_lowrank_bwd": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                 c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                 c_void_p, c_size_t, c_void_p]),

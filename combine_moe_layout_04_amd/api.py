@@ -627,6 +627,24 @@ def moe_lowrank(handle: Handle, x: torch.Tensor, a: torch.Tensor, b: torch.Tenso
     return out, u
 
 
+def moe_lowrank_bwd_workspace_size(handle: Handle, dtype: torch.dtype, H: int, N: int, A: int, r: int) -> int:
+    n = ctypes.c_size_t(0)
+    code = MOE_F32 if dtype == torch.float32 else MOE_BF16 if dtype == torch.bfloat16 else -1
+    _check(lib().moe_lowrank_bwd_workspace_size(handle.ptr, code, H, N, A, r, ctypes.byref(n)),
+           "moe_lowrank_bwd_workspace_size")
+    return n.value
+
+
+def _lowrank_workspace_bytes(h, dtype, H, N, A, r):
+    key = (h.R, dtype, H, N, A, r)
+    v = _SIZES.get(key)
+    if v is None:
+        if len(_SIZES) >= _SIZES_MAX:
+            _SIZES.clear()
+        v = _SIZES[key] = moe_lowrank_bwd_workspace_size(h, dtype, H, N, A, r)
+    return v
+
+
 def moe_lowrank_bwd(handle: Handle, grad_out: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
                     u: torch.Tensor, topk_weights: Optional[torch.Tensor] = None,
                     grad_base: Optional[torch.Tensor] = None, grad_x=None, grad_a=None, grad_b=None, grad_w=False,
@@ -666,7 +684,7 @@ def moe_lowrank_bwd(handle: Handle, grad_out: torch.Tensor, x: torch.Tensor, a: 
     else:
         _need(grad_w, "grad_w", dev, (T, 1), torch.float32)
     if workspace is None:
-        workspace = torch.empty_like(u)
+        workspace = u.new_empty(_lowrank_workspace_bytes(h, dtype, H, N, A, r) // 4)
     else:
         _need(workspace, "workspace", dev)
     _run(dev, "moe_lowrank_bwd", h.ptr, grad_out.data_ptr(), dt, H, x.data_ptr(), a.data_ptr(), b.data_ptr(), A, r, N,

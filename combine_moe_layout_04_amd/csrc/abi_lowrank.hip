@@ -29,9 +29,27 @@ moe::LowrankArgs lowrank_args(const moe_handle_s* h, int dtype, int A, int r) {
   return a;
 }
 
+// Bytes of the backward's workspace: gu, then the parts of grad_a and grad_b.
+size_t gu_bytes(const moe_handle_s* h, int r) { return (size_t)h->R * r * sizeof(float); }
+
+size_t parts_bytes(int64_t H, int64_t N, int A, int r, int splits) {
+  return splits > 1 ? (size_t)splits * A * r * (H + N) * sizeof(float) : 0;
+}
+
 }  // namespace
 
 extern "C" {
+
+int moe_lowrank_bwd_workspace_size(moe_handle_t h, int dtype, int64_t H, int64_t N, int num_adapters, int rank,
+                                   size_t* bytes) {
+  const int st = check_lowrank(h, dtype, H, N, num_adapters, rank);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int es = moe::elem_bytes(dtype);
+  const int splits = moe::lowrank_wgrad_splits(h->R, num_adapters, rank, (int)(H * es / 16), (int)(N * es / 16), dtype);
+  *bytes = gu_bytes(h, rank) + parts_bytes(H, N, num_adapters, rank, splits);
+  return MOE_OK;
+}
 
 int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void* a, const void* b,
                 int num_adapters, int rank, int64_t N, const float* topk_weights, const void* base, void* out,
@@ -75,7 +93,7 @@ int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, 
       !moe::aligned(grad_a, 16) || !moe::aligned(grad_b, 16) || !moe::aligned(topk_weights, 4) ||
       !moe::aligned(grad_w, 4) || !moe::aligned(workspace, 16))
     return MOE_ERR_ALIGNMENT;
-  if (through && workspace_bytes < (size_t)h->R * rank * sizeof(float)) return MOE_ERR_WORKSPACE;
+  if (through && workspace_bytes < gu_bytes(h, rank)) return MOE_ERR_WORKSPACE;
   const int es = moe::elem_bytes(dtype);
   const int hch = (int)(H * es / 16), nch = (int)(N * es / 16);
   moe::LowrankArgs k = lowrank_args(h, dtype, num_adapters, rank);
@@ -114,7 +132,10 @@ int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, 
     gb.u = const_cast<float*>(u);
     gb.out = grad_b;
     gb.wch = nch;
-    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(ga, gb, stream))) != MOE_OK) return st;
+    int splits = moe::lowrank_wgrad_splits(h->R, num_adapters, rank, hch, nch, dtype);
+    if (!workspace || workspace_bytes < gu_bytes(h, rank) + parts_bytes(H, N, num_adapters, rank, splits)) splits = 1;
+    float* parts = splits > 1 ? gu + (size_t)h->R * rank : nullptr;
+    if ((st = moe::hip_status(moe::launch_lowrank_wgrad(ga, gb, parts, splits, stream))) != MOE_OK) return st;
   }
   return MOE_OK;
 }

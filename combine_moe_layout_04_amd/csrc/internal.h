@@ -263,7 +263,8 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s);
 hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s);
 hipError_t launch_lowrank_expand(const LowrankArgs& a, hipStream_t s);
 hipError_t launch_lowrank_pass(const LowrankArgs& shrink, const LowrankArgs& expand, hipStream_t s);
-hipError_t launch_lowrank_wgrad(const LowrankArgs& a, const LowrankArgs& b, hipStream_t s);
+hipError_t launch_lowrank_wgrad(const LowrankArgs& a, const LowrankArgs& b, float* parts, int splits, hipStream_t s);
+int lowrank_wgrad_splits(int64_t R, int A, int r, int hch, int nch, int dtype);
 hipError_t launch_copy(void* dst, const void* src, size_t bytes, hipStream_t s);
 
 }  // namespace moe

@@ -547,9 +547,11 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
 // block's rows of u pass through the wave's own piece of LDS, loaded 16 bytes a
 // lane: four bytes a lane, as the operand takes them, cost the address unit
 // twice what the wide rows do.  An adapter without rows gets zeros.  (Both sides
-// of 4096 rows of 2048 and 4096 bfloat16, 4 adapters of rank 64: 29 us; every 32
-// ranks read the rows again, 100 MB at 3.5 TB/s.)
-constexpr int kWgradWaves = 8;
+// of 4096 rows of 2048 and 4096 bfloat16, 4 adapters of rank 64: 25 us; every 32
+// ranks read the rows again, 100 MB at 4 TB/s.)
+//
+// With few adapters the rows of one are split over gridDim.z workgroups, whose
+// sums wgrad_sum_kernel adds in their order.
 
 // What the gradients of a and of b, in one launch, do not share.
 struct WgradSide {
@@ -558,18 +560,19 @@ struct WgradSide {
   const float* u;
   void* out;
   int wch;
+  float* parts;  // [gridDim.z][A, r, W] with split rows
 };
 
-template <int DT, int JT>
-__global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a, WgradSide one, WgradSide two,
+template <int DT, int JT, int W>
+__global__ __launch_bounds__((W * kWave)) void wgrad_kernel(LowrankArgs a, WgradSide one, WgradSide two,
                                                                   int one_blocks) {
   using S = Shape<DT>;
   constexpr int V = S::V;
   constexpr int kStride = JT * 16 + 4;                  // floats of a row of u in LDS
   constexpr int kLoads = S::KB * JT * 4 / kWave;        // a block's u, 16 bytes a lane
   __shared__ __align__(16) union {
-    float u[kWgradWaves][S::KB * kStride];
-    f32x4 part[kWgradWaves][V][kWave];
+    float u[W][S::KB * kStride];
+    f32x4 part[W][V][kWave];
   } sh;
   auto& part = sh.part;
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
@@ -581,12 +584,19 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
   const float* weights = second ? two.w : one.w;
   const float* u_rows = second ? two.u : one.u;
   u32x4* out = static_cast<u32x4*>(second ? two.out : one.out);
+  float* parts_out = second ? two.parts : one.parts;
   const int nch = second ? two.wch : one.wch;
   const int parts = (a.r + 16 * JT - 1) / (16 * JT);
   const int c0 = block / parts * 16;
   const int j0 = block % parts * JT * 16;
   const int c = min(c0 + col, nch - 1);  // chunks past the end repeat the last and are not stored
-  const int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
+  int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
+  const int splits = gridDim.z;
+  if (splits > 1) {
+    const int share = ((hi - lo + splits - 1) / splits + S::KB - 1) / S::KB * S::KB;
+    lo += blockIdx.z * share;
+    hi = min(hi, lo + share);
+  }
   f32x4 acc[JT][V];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
@@ -613,7 +623,7 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
     }
     if (weights) w = weights[max(t, 0)];
   };
-  constexpr int kStep = kWgradWaves * S::KB;
+  constexpr int kStep = W * S::KB;
   int p0 = lo + wave * S::KB;
   if (p0 < hi) {
     t = tokens(p0);
@@ -667,12 +677,42 @@ __global__ __launch_bounds__(kWgradWaves* kWave) void wgrad_kernel(LowrankArgs a
         const float* f = reinterpret_cast<const float*>(&part[0][i][lane]) + wave;
         o[i] = f[0];
 #pragma unroll
-        for (int k = 1; k < kWgradWaves; ++k) o[i] += f[(size_t)k * V * kWave * 4];
+        for (int k = 1; k < W; ++k) o[i] += f[(size_t)k * V * kWave * 4];
       }
       const int cc = c0 + q * 4 + wave;
-      if (j < a.r && cc < nch) out[((size_t)e * a.r + j) * nch + cc] = pack_rows<DT>(o);
+      if (j < a.r && cc < nch) {
+        const size_t to = ((size_t)e * a.r + j) * nch + cc;
+        if (splits == 1) {
+          out[to] = pack_rows<DT>(o);
+        } else {
+          f32x4* f = reinterpret_cast<f32x4*>(parts_out) + ((size_t)blockIdx.z * a.A * a.r * nch + to) * (V / 4);
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) f[i] = f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+        }
+      }
     }
   }
+}
+
+// The parts' sums, a chunk a thread; first: chunks of the first side.
+template <int DT>
+__global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradSide one, WgradSide two, int first, int chunks, int splits) {
+  constexpr int V = Shape<DT>::V;
+  int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= chunks) return;
+  const bool second = c >= first;
+  const size_t n = second ? chunks - first : first;
+  c -= second ? first : 0;
+  const f32x4* f = reinterpret_cast<const f32x4*>(second ? two.parts : one.parts) + (size_t)c * (V / 4);
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    f32x4 v = f[i];
+    for (int s = 1; s < splits; ++s) v += f[s * n * (V / 4) + i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[4 * i + k] = v[k];
+  }
+  static_cast<u32x4*>(second ? two.out : one.out)[c] = pack_rows<DT>(o);
 }
 
 template <typename F>
@@ -782,23 +822,71 @@ hipError_t launch_lowrank_pass(const LowrankArgs& s, const LowrankArgs& a, hipSt
   return e != hipSuccess ? e : launch_lowrank_expand(a, stream);
 }
 
-// grad_a from `a` and grad_b from `b`, where their out is not null.
-hipError_t launch_lowrank_wgrad(const LowrankArgs& a, const LowrankArgs& b, hipStream_t s) {
-  // ranks of a workgroup (a backward pass with 16 against 32: 1024 rows, rank 16
-  // 27 and 29 us, 4096 rows, rank 64 77 and 69, rank 128 180 and 143)
-  const int width = a.r <= 16 ? 16 : 32;
-  auto blocks = [&](const LowrankArgs& k) { return k.out ? (k.wch + 15) / 16 * ((k.r + width - 1) / width) : 0; };
-  const WgradSide one{a.rows, a.w, a.u, a.out, a.wch}, two{b.rows, b.w, b.u, b.out, b.wch};
-  const dim3 grid(blocks(a) + blocks(b), a.A), block(kWgradWaves * kWave);
-#define MOE_WGRAD(D, J) \
-  return launched([&] { hipLaunchKernelGGL((wgrad_kernel<D, J>), grid, block, 0, s, a, one, two, blocks(a)); })
-  if (width == 16) {
-    if (a.dtype == MOE_F32) MOE_WGRAD(kF32, 1);
-    MOE_WGRAD(kBF16, 1);
-  }
-  if (a.dtype == MOE_F32) MOE_WGRAD(kF32, 2);
-  MOE_WGRAD(kBF16, 2);
-#undef MOE_WGRAD
+namespace {
+
+int wgrad_width(int r) {  // ranks of a workgroup
+  // a backward pass with 16 against 32: 1024 rows, rank 16 27 and 29 us, 4096
+  // rows, rank 64 77 and 69, rank 128 180 and 143
+  return r <= 16 ? 16 : 32;
+}
+
+int64_t wgrad_blocks(int wch, int r) { return (int64_t)((wch + 15) / 16) * ((r + wgrad_width(r) - 1) / wgrad_width(r)); }
+
+template <int DT, int JT>
+hipError_t launch_wgrad(const LowrankArgs& a, const WgradSide& one, const WgradSide& two, int one_blocks, dim3 grid,
+                        hipStream_t s) {
+  // As many workgroups of 8 waves as the registers let run at once (bfloat16 one
+  // a CU, float32 two): more go with 4 waves, all at once again (a backward pass
+  // in bfloat16 with 8 and 4 waves: 512 rows of 64 adapters, rank 32, 2048
+  // columns 61 and 38 us, 4096 of 16, rank 64, 4096 columns 123 and 99, 4096 of
+  // one, 2048 columns 57 and 76).
+  const int64_t groups = (int64_t)grid.x * grid.y * grid.z;
+  return launched([&] {
+    if (groups > (DT == kBF16 ? 256 : 512))
+      hipLaunchKernelGGL((wgrad_kernel<DT, JT, 4>), grid, dim3(4 * kWave), 0, s, a, one, two, one_blocks);
+    else
+      hipLaunchKernelGGL((wgrad_kernel<DT, JT, 8>), grid, dim3(8 * kWave), 0, s, a, one, two, one_blocks);
+  });
+}
+
+}  // namespace
+
+// Parts that the rows of an adapter are split into: while the workgroups are
+// fewer than CUs and every wave keeps two blocks of rows (a backward pass of one
+// adapter in bfloat16, whole and split: 4096 rows, rank 64, 2048 columns 57 and 43
+// us, 16384 rows, rank 64, 4096 columns 220 and 182; float32, 2048 rows, rank 32,
+// 2048 columns 50 and 36).
+int lowrank_wgrad_splits(int64_t R, int A, int r, int hch, int nch, int dtype) {
+  const int64_t groups = (wgrad_blocks(hch, r) + wgrad_blocks(nch, r)) * A;
+  const int64_t rows = 8 * 2 * (dtype == MOE_F32 ? Shape<kF32>::KB : Shape<kBF16>::KB);
+  int s = 1;
+  while (s < 16 && groups * s * 2 <= 256 && R / A >= rows * s * 2) s *= 2;
+  return s;
+}
+
+// grad_a from `a` and grad_b from `b`, where their out is not null; parts: room
+// for `splits` times both in float32, with splits > 1.
+hipError_t launch_lowrank_wgrad(const LowrankArgs& a, const LowrankArgs& b, float* parts, int splits, hipStream_t s) {
+  const int64_t one_blocks = a.out ? wgrad_blocks(a.wch, a.r) : 0, two_blocks = b.out ? wgrad_blocks(b.wch, b.r) : 0;
+  const int v = a.dtype == MOE_F32 ? 4 : 8;
+  const int64_t one_chunks = a.out ? (int64_t)a.A * a.r * a.wch : 0, two_chunks = b.out ? (int64_t)b.A * b.r * b.wch : 0;
+  const WgradSide one{a.rows, a.w, a.u, a.out, a.wch, parts};
+  const WgradSide two{b.rows, b.w, b.u, b.out, b.wch, splits > 1 ? parts + splits * one_chunks * v : nullptr};
+  const dim3 grid(one_blocks + two_blocks, a.A, splits);
+  hipError_t e;
+  if (a.dtype == MOE_F32)
+    e = wgrad_width(a.r) == 16 ? launch_wgrad<kF32, 1>(a, one, two, (int)one_blocks, grid, s)
+                               : launch_wgrad<kF32, 2>(a, one, two, (int)one_blocks, grid, s);
+  else
+    e = wgrad_width(a.r) == 16 ? launch_wgrad<kBF16, 1>(a, one, two, (int)one_blocks, grid, s)
+                               : launch_wgrad<kBF16, 2>(a, one, two, (int)one_blocks, grid, s);
+  if (e != hipSuccess || splits == 1) return e;
+  const int chunks = (int)(one_chunks + two_chunks);
+  return launched([&] {
+    const dim3 blocks((chunks + 255) / 256);
+    if (a.dtype == MOE_F32) hipLaunchKernelGGL(wgrad_sum_kernel<kF32>, blocks, dim3(256), 0, s, one, two, (int)one_chunks, chunks, splits);
+    else hipLaunchKernelGGL(wgrad_sum_kernel<kBF16>, blocks, dim3(256), 0, s, one, two, (int)one_chunks, chunks, splits);
+  });
 }
 
 }  // namespace moe

@@ -461,9 +461,15 @@ int moe_lowrank(moe_handle_t h, const void* x, int dtype, int64_t H, const void*
  * grad_out itself.)
  *   grad_out [T,N], x [T,H], a, b as above, grad_x, grad_base [T,H], grad_a
  *   [num_adapters,r,H], grad_b [num_adapters,r,N] dtype; u as the forward call
- *   wrote it; grad_w [T,1] float32; workspace 16-byte aligned, R * r * 4
- *   bytes (not needed for grad_b alone; one per call in flight).  With T = 0 grad_a and grad_b are
- *   set to zero.                                                             */
+ *   wrote it; grad_w [T,1] float32; workspace 16-byte aligned, at
+ *   least R * r * 4 bytes (not needed for grad_b alone; one per call in
+ *   flight).  With T = 0 grad_a and grad_b are set to zero.
+ * moe_lowrank_bwd_workspace_size gives the size at which few adapters with
+ * many tokens each have their gradients summed in parts, which is faster (the
+ * order of the sum then depends on the shapes, not on timing); with a smaller
+ * workspace they are summed in one.  A function of the shapes only.         */
+int moe_lowrank_bwd_workspace_size(moe_handle_t h, int dtype, int64_t H, int64_t N, int num_adapters, int rank,
+                                   size_t* bytes);
 int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, const void* x, const void* a,
                     const void* b, int num_adapters, int rank, int64_t N, const float* topk_weights,
                     const float* u, const void* grad_base, void* grad_x, void* grad_a, void* grad_b,

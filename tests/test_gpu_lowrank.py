@@ -288,6 +288,37 @@ def test_empty_batch():
     assert gx.shape == (0, 16) and (ga == 0).all() and (gb == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,A,r,H,N,pad", [(4100, 1, 16, 136, 264, 1), (9001, 2, 40, 72, 520, 1), (5000, 3, 24, 64, 128, 16),
+                                           (17000, 1, 64, 24, 40, 1)])
+def test_gradients_summed_in_parts(dtype, T, A, r, H, N, pad):
+    """Long segments of few adapters: one adapter has nearly all tokens, the last
+    none; with the workspace for parts, one short of it, and the smallest."""
+    ids, E, d = make(T, A, r, H, N, dtype, 6, E=A + 2)
+    if A > 1:
+        few = (ids == 1) & (torch.arange(T, device=DEV).view(-1, 1) % 50 != 0)
+        ids[few] = 0
+        ids[ids == A - 1] = A
+    h = M.moe_layout(ids, E, 1, handle=M.Handle(pad_multiple=pad))
+    ref = reference(ids, d)
+    _, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+    n = M.moe_lowrank_bwd_workspace_size(h, dtype, H, N, A, r) // 4
+    assert n > h.R * r  # there are parts
+    ws = torch.full((n + 4,), math.nan, device=DEV)
+    for size in (n, n - 4, h.R * r):
+        for want in ((None, None), (None, False), (False, None)):
+            ws.fill_(math.nan)
+            got = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_x=False, grad_a=want[0],
+                                    grad_b=want[1], workspace=ws[:size])
+            for name, t, w in zip(("grad_a", "grad_b"), got[1:3], want):
+                if w is None:
+                    near(t, ref[name], name)
+            assert torch.isnan(ws[size:]).all()
+    one = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"])
+    two = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"])
+    assert all(torch.equal(p, q) for p, q in zip(one[:3], two[:3]))
+
+
 @pytest.mark.parametrize("T", [40, 3000])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_ids_outside_the_layout_touch_no_other_token(dtype, T):
