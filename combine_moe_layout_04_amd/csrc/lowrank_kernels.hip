@@ -97,8 +97,8 @@ __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
 // bank twice.  Workgroups start at different lines (and go round): rows a
 // power of two apart, read at the same place at once, meet in a few memory
 // channels.  FAR: the wide rows reach past what a buffer's 32-bit offsets do (2
-// GiB).  (8192 rows of 4096 bfloat16, 16 adapters of rank 32: 25 us, 67 MB of rows
-// at 2.7 TB/s and as much again of the banks from L2; what is left of the bound is
+// GiB).  (8192 rows of 4096 bfloat16, 16 adapters of rank 32: 21 us, 67 MB of rows
+// at 3.2 TB/s and as much again of the banks from L2; what is left of the bound is
 // the wait for the first lines and for the adapters of a tile.)
 template <int JT, int RT>
 struct Shrink {
@@ -385,8 +385,8 @@ struct Expand {
     }
   }
 
-  // w times row p of u, this lane's part of every block
-  static __device__ __forceinline__ void load_u(const LowrankArgs& a, int p, float w, float (&f)[BLOCKS][V]) {
+  // row p of u, this lane's part of every block (ranks past the last: other ranks')
+  static __device__ __forceinline__ void load_u(const LowrankArgs& a, int p, f32x4 (&u4)[BLOCKS][V / 4]) {
     const int q = lane_id() >> 4;
     const float* u = a.u + (size_t)p * a.r;
 #pragma unroll
@@ -394,10 +394,18 @@ struct Expand {
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
         const int jj = k * S::KB + q * V + j;
-        const f32x4 v = *reinterpret_cast<const f32x4*>(u + (jj < a.r ? jj : 0));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[k][j + i] = jj < a.r ? v[i] * w : 0.f;
+        u4[k][j / 4] = *reinterpret_cast<const f32x4*>(u + (jj < a.r ? jj : 0));
       }
+  }
+
+  // w times it; zeros past the last rank
+  static __device__ __forceinline__ void weigh(const LowrankArgs& a, const f32x4 (&u4)[BLOCKS][V / 4], float w,
+                                               float (&f)[BLOCKS][V]) {
+    const int q = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[k][j] = k * S::KB + q * V + j < a.r ? u4[k][j / 4][j % 4] * w : 0.f;
   }
 
   static __device__ __forceinline__ void load_base(const LowrankArgs& a, int t, int c0, u32x4 (&base)[4]) {
@@ -451,12 +459,15 @@ struct Expand {
 
 // One wave per (a.tiles tiles of 16 receive rows, 16 chunks of columns, slot);
 // it keeps its columns of an adapter's bank in registers from tile to tile, and
-// has the next tile's rows of base on their way.  BLOCKS blocks of KB ranks.
-// (8192 rows of 4096 bfloat16, rank 32: 34 us, 134 MB read and written at 3.9 TB/s.)
+// has the next tile's rows of base and u on their way.  BLOCKS blocks of KB ranks.
+// (8192 rows of 4096 bfloat16, rank 32: 33 us, 134 MB read and written at 4.1 TB/s;
+// 34 us when u is asked for as it is needed.  What is left is the first tile's
+// wait, for tokens, base, offsets and bank one after another, and a mixture of
+// reads and writes in pieces of 256 bytes.)
 constexpr int kExpandWaves = 4;
 
 template <int DT, int BLOCKS>
-__global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(LowrankArgs a) {
+__global__ __launch_bounds__(kExpandWaves* kWave, BLOCKS <= 2 ? 2 : 1) void expand_lowrank_kernel(LowrankArgs a) {
   using X = Expand<DT, BLOCKS>;
   __shared__ int off[kMaxOff];
   __shared__ __align__(16) float products[kExpandWaves][X::kProducts];
@@ -469,7 +480,11 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
   if (c0 >= a.wch) return;
   X x;
   u32x4 base[4], next_base[4];
+  f32x4 next_u[BLOCKS][X::V / 4];
+  float next_w = 1.f;
   X::load_base(a, next_t, c0, next_base);
+  X::load_u(a, min(tile * kTile + col, a.R - 1), next_u);
+  if (a.w) next_w = a.w[max(next_t, 0)];
   int after_t = row_token(a, (tile + 1) * kTile + col);
   int held = -1;  // the adapter whose bank is held
   for (; tile < tile_end; ++tile) {
@@ -478,9 +493,13 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void expand_lowrank_kernel(Low
     for (int s = 0; s < 4; ++s) base[s] = next_base[s];
     const int r0 = tile * kTile, r1 = min(r0 + kTile, a.R);
     float f[BLOCKS][X::V];
-    X::load_u(a, min(r0 + col, a.R - 1), a.w ? a.w[max(t, 0)] : 1.f, f);
+    X::weigh(a, next_u, next_w, f);
     next_t = after_t;
-    if (tile + 1 < tile_end) X::load_base(a, next_t, c0, next_base);
+    if (tile + 1 < tile_end) {
+      X::load_base(a, next_t, c0, next_base);
+      X::load_u(a, min(r0 + kTile + col, a.R - 1), next_u);
+      if (a.w) next_w = a.w[max(next_t, 0)];
+    }
     after_t = row_token(a, (tile + 2) * kTile + col);
     each_adapter(off, a.E, r0, r1, blockIdx.z, gridDim.z, [&](int e, int lo, int hi) {
       if (e < a.A && e != held) {
@@ -533,7 +552,9 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
     shrink_rows<DT, JT, 1, false>(s, lds, r0, e, lo, hi, t, load_t);
     __syncthreads();  // u is written
     float f[Both<DT, JT>::kBlocks][X::V];
-    X::load_u(a, min(r0 + (lane & 15), a.R - 1), a.w ? a.w[max(t[0], 0)] : 1.f, f);
+    f32x4 u4[Both<DT, JT>::kBlocks][X::V / 4];
+    X::load_u(a, min(r0 + (lane & 15), a.R - 1), u4);
+    X::weigh(a, u4, a.w ? a.w[max(t[0], 0)] : 1.f, f);
     while (c0 < a.wch) {
       x.rows(a, prod, r0, e, lo, hi, t[0], c0, f, base);
       c0 += kWaves * 16;
