@@ -85,7 +85,7 @@ __device__ __forceinline__ int row_token(const LowrankArgs& a, int p) {
 
 // ---- shrink ---------------------------------------------------------------------
 //
-// One workgroup per (RT tiles of 16 rows, slot).  Its waves split the sum over
+// One workgroup per (RT tiles of 16 rows, slot, 16 JT of the rank).  Its waves split the sum over
 // the row, a 128-byte line of every row each in turn, kDepth lines in flight,
 // and meet in LDS; wave rt adds the parts of tile rt and writes its 16 rows of
 // r float32.
@@ -109,11 +109,11 @@ struct Shrink {
   static constexpr size_t kLds = (size_t)kWaves * kRows * 128;  // at most 48 KiB
 };
 
-// Rows [lo, hi) of adapter e, of the RT tiles from r0 on; the whole workgroup.
-// t, load_t: the tokens of this lane's rows as an operand and in a load.
+// Rows [lo, hi) of adapter e, of the RT tiles from r0 on, ranks [j0, j0 + 16 JT);
+// the whole workgroup.  t, load_t: the tokens of this lane's rows as an operand and in a load.
 template <int DT, int JT, int RT, bool FAR>
-__device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, int r0, int e, int lo, int hi,
-                                            const int (&t)[RT], const int (&load_t)[2 * RT]) {
+__device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, int r0, int j0, int e, int lo,
+                                            int hi, const int (&t)[RT], const int (&load_t)[2 * RT]) {
   constexpr int kShrinkWaves = Shrink<JT, RT>::kWaves, kMeet = Shrink<JT, RT>::kMeet;
   constexpr int kStaged = Shrink<JT, RT>::kStaged, kRows = Shrink<JT, RT>::kRows;
   constexpr int kDepth = JT + RT <= 2 ? 3 : JT + RT <= 4 ? 2 : 1;
@@ -132,6 +132,7 @@ __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, in
     mine[rt] = p >= lo && p < hi;
   }
   if (e >= a.A) {  // no adapter: u = 0, and no gradient
+    if (j0 > 0) return;
     for (int i = threadIdx.x; i < (hi - lo) * a.r; i += kShrinkWaves * kWave) a.u[(size_t)lo * a.r + i] = 0.f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -147,7 +148,7 @@ __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, in
     x_off[k] = p >= lo && p < hi ? (uint32_t)load_t[k] * row_bytes + chunk * 16 : kOutside;
   }
   const auto wide = make_rows(a.rows, FAR ? 0 : (size_t)a.T * row_bytes);
-  const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + (size_t)e * a.r * nch, (size_t)a.r * row_bytes);
+  const auto bank = make_rows(static_cast<const u32x4*>(a.bank) + ((size_t)e * a.r + j0) * nch, (size_t)(a.r - j0) * row_bytes);
   const uint32_t b_off = (uint32_t)row8 * row_bytes + chunk * 16;
   u32x4 in[kDepth][2 * (RT + JT)];
   auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
@@ -232,7 +233,7 @@ __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, in
         f32x4 v = part[(rt * kMeet + m) * kWave + lane];
 #pragma unroll
         for (int k = 1; k < kShrinkWaves; ++k) v += part[((k * RT + rt) * kMeet + m) * kWave + lane];
-        const int j = (first + m) * 16 + q * 4;
+        const int j = j0 + (first + m) * 16 + q * 4;
         if (mine[rt] && j < a.r) {
           if (t[rt] < 0) v = f32x4{0.f, 0.f, 0.f, 0.f};  // padding
           if (a.backward) {
@@ -271,7 +272,7 @@ __global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kerne
   for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + (lane & 15));
   load_offsets(off, a);
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
-    shrink_rows<DT, JT, RT, FAR>(a, lds, r0, e, lo, hi, t, load_t);
+    shrink_rows<DT, JT, RT, FAR>(a, lds, r0, blockIdx.z * JT * 16, e, lo, hi, t, load_t);
   });
 }
 
@@ -549,7 +550,7 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
       if (e < a.A) x.load_bank(a, e, c0);
       X::load_base(a, t[0], c0, base);
     }
-    shrink_rows<DT, JT, 1, false>(s, lds, r0, e, lo, hi, t, load_t);
+    shrink_rows<DT, JT, 1, false>(s, lds, r0, 0, e, lo, hi, t, load_t);
     __syncthreads();  // u is written
     float f[Both<DT, JT>::kBlocks][X::V];
     f32x4 u4[Both<DT, JT>::kBlocks][X::V / 4];
@@ -778,7 +779,15 @@ hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
   const bool far = (int64_t)a.T * a.wch * 16 >= (int64_t(1) << 31);
   const int rt = !far && a.r <= 64 && a.R >= 2 * kTile * 256 ? 2 : 1;
   const int tiles = (a.R + kTile * rt - 1) / (kTile * rt);
-  const dim3 grid(tiles, slots_for(tiles, a.E));
+  // Few tiles: the rank in parts of 16 or more, since one CU reads a bank slowly
+  // (the kernel in one part and in parts, us: 4 float32 rows of 3936, rank 52 26
+  // and 10; bfloat16 rows of 4096, rank 64, 8 of them 9.9 and 6.4, 48 11.8 and
+  // 6.9; 700 of 2048, rank 32 6.1 and 6.4).  Not with grad_w, a sum over the rank.
+  int width = a.r <= 16 ? 1 : a.r <= 32 ? 2 : a.r <= 64 ? 4 : 8;
+  auto parts = [&] { return (a.r + 16 * width - 1) / (16 * width); };  // every part has ranks
+  if (!far && !a.dot)
+    while (width > 1 && tiles * parts() * 2 <= 128) width /= 2;
+  const dim3 grid(tiles, slots_for(tiles, a.E), parts());
 #define MOE_SHRINK(J, T, F)                                                                             \
   return launched([&] {                                                                                 \
     const dim3 block((Shrink<J, T>::kWaves * kWave));                                                   \
@@ -795,9 +804,9 @@ hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
     if (a.r <= 32) MOE_SHRINK(2, 2, false);
     MOE_SHRINK(4, 2, false);
   }
-  if (a.r <= 16) MOE_SHRINK(1, 1, false);
-  if (a.r <= 32) MOE_SHRINK(2, 1, false);
-  if (a.r <= 64) MOE_SHRINK(4, 1, false);
+  if (width == 1) MOE_SHRINK(1, 1, false);
+  if (width == 2) MOE_SHRINK(2, 1, false);
+  if (width == 4) MOE_SHRINK(4, 1, false);
   MOE_SHRINK(8, 1, false);
 #undef MOE_SHRINK
 }
