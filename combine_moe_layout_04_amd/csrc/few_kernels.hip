@@ -12,8 +12,8 @@
 // No layout runs before: a call has at most 512 pairs, and every workgroup
 // groups them by expert in its LDS as it starts.  A workgroup of the first
 // kernel takes (expert, 8 columns of act) after another; its waves split the
-// sum over H.  A workgroup of the second owns 8 columns of out for all pairs:
-// its waves share out the experts, leave each pair's 8 values in LDS, and the
+// sum over H.  A workgroup of the second owns 4 or 8 columns of out for all pairs:
+// its waves share out the experts, leave each pair's values in LDS, and the
 // top-k sum is formed there in k order, so that no second pass over pairs and
 // no order left to chance remain.  An id outside [0, E) belongs to no expert
 // here and adds nothing.
@@ -244,19 +244,20 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
   }
 }
 
-// 8 columns of out, for every pair.  A wave's item is (expert, part of the sum
-// over I); it leaves its pairs' 8 values in y[part][pair].  The waves stream
+// 4 NR columns of out, for every pair.  A wave's item is (expert, part of the sum
+// over I); it leaves its pairs' values in y[part][pair].  The waves stream
 // their items' weights in rounds of kDepth lines, the next round's (of the same
 // item or the next) under way during this one.
 constexpr int kDownWaves = 16;
 
-template <int DT, int NT>
+template <int DT, int NT, int NR>
 __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
   constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 269, 256, 264 us a call with 1, 2, 3
   __shared__ Groups groups;
   __shared__ float weight[kFewMaxPairs];
   __shared__ uint8_t here[kFewMaxPairs];
-  extern __shared__ float y[];  // [split][pairs][8]
+  constexpr int kCols = 4 * NR;
+  extern __shared__ float y[];  // [split][pairs][kCols]
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
@@ -270,14 +271,14 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
 
   const int nch = a.ich;  // chunks of an act or w2 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
-  const int h0 = blockIdx.x * 8;
-  const size_t tile_bytes = (size_t)min(8, a.H - h0) * row_bytes;
+  const int h0 = blockIdx.x * kCols;
+  const size_t tile_bytes = (size_t)min(kCols, a.H - h0) * row_bytes;
   const auto mid = make_rows(a.mid, (size_t)a.pairs * row_bytes);
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
   const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 15) / 16);
   const int rounds = (a.part_lines + kDepth - 1) / kDepth;
 
-  u32x4 w[kDepth][2], b[kDepth][NT];
+  u32x4 w[kDepth][NR], b[kDepth][NT];
   auto w2 = make_rows(a.w2, 0);
   uint32_t m_off[NT];
   int n = 0;  // pairs of the fetched item
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     const int line = min(i, hi - 1);
     const bool in = i < hi && line * 16 + at.chunk < nch;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < NR; ++r)
       w[d][r] = load_rows<true>(w2, in ? w_off + r * 4 * row_bytes : kOutside, (uint32_t)line * 256);
 #pragma unroll
     for (int c = 0; c < NT; ++c) b[d][c] = load_rows(mid, in ? m_off[c] : kOutside, (uint32_t)line * 256);
@@ -311,11 +312,11 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
       in_order();
     }
   }
-  f32x4 acc[NT][2];
+  f32x4 acc[NT][NR];
 #pragma unroll
   for (int c = 0; c < NT; ++c)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < NR; ++r) acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int j = wave, first = 0, round = 0; j < items;) {
     const uint16_t* this_list = list;
     const int this_n = n;
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c], acc[c][r]);
+        for (int r = 0; r < NR; ++r) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c], acc[c][r]);
       in_order();
       fetch(d, next_line + d);  // past the end: zeros
       in_order();
@@ -346,11 +347,11 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
       for (int c = 0; c < NT; ++c) {
         const int pos = first + c * 4 + at.second();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < NR; ++r) {
           const float v = join_parts(acc[c][r]);
           acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
           if ((lane_id() & 3) == 0 && pos < this_n)
-            y[((size_t)part * a.pairs + this_list[pos]) * 8 + r * 4 + at.first()] = v;
+            y[((size_t)part * a.pairs + this_list[pos]) * kCols + r * 4 + at.first()] = v;
         }
       }
     }
@@ -360,15 +361,15 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   }
   __syncthreads();
 
-  for (int o = threadIdx.x; o < a.T * 8; o += kDownWaves * kWave) {
-    const int t = o >> 3, c = o & 7;
+  for (int o = threadIdx.x; o < a.T * kCols; o += kDownWaves * kWave) {
+    const int t = o / kCols, c = o % kCols;
     if (h0 + c >= a.H) continue;
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k) {
       const int p = t * a.K + k;
       if (!here[p]) continue;
-      float v = y[(size_t)p * 8 + c];
-      for (int i = 1; i < a.split; ++i) v += y[((size_t)i * a.pairs + p) * 8 + c];
+      float v = y[(size_t)p * kCols + c];
+      for (int i = 1; i < a.split; ++i) v += y[((size_t)i * a.pairs + p) * kCols + c];
       sum = __fadd_rn(sum, __fmul_rn(weight[p], v));
     }
     const size_t pos = (size_t)t * a.H + h0 + c;
@@ -383,8 +384,15 @@ hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((few_up_kernel<DT, NT>), dim3(up), dim3(kUpWaves * kWave), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((few_down_kernel<DT, NT>), dim3((a.H + 7) / 8), dim3(kDownWaves * kWave),
-                     (size_t)a.split * a.pairs * 32, s, a);
+  const dim3 block(kDownWaves * kWave);
+  const size_t column = (size_t)a.split * a.pairs * sizeof(float);
+  // 4 columns of out a workgroup where 8 would leave CUs without one (the kernel with
+  // 8 and 4, us: 57 tokens, top 6 of 60, 288 x 140 float32 26.6 and 15.2; 30, top 8 of
+  // 40, 1024 x 400 bfloat16 18.2 and 14.0; 1, top 4 of 64, 512 x 256 5.7 and 5.1)
+  if (a.H < 8 * 256)
+    hipLaunchKernelGGL((few_down_kernel<DT, NT, 1>), dim3((a.H + 3) / 4), block, column * 4, s, a);
+  else
+    hipLaunchKernelGGL((few_down_kernel<DT, NT, 2>), dim3((a.H + 7) / 8), block, column * 8, s, a);
   return hipGetLastError();
 }
 
