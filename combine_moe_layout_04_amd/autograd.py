@@ -11,12 +11,18 @@ every step is a library call.
 The C handle keeps only its latest layout.  A backward pass whose handle was
 laid out again after its forward (for example a per-layer handle reused by a
 later forward pass) raises instead of using the newer routing.
+
+The router and the adapters have a first derivative only; a second raises.  To
+capture a backward pass into a HIP graph, run its forward inside the capture and
+let no earlier eager graph of the same leaves live: torch accumulates into a leaf
+on the stream of the first graph that used it, which a capture must not wait for.
 """
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -90,6 +96,7 @@ class _Route(torch.autograd.Function):
         return idx, w
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _grad_idx, grad_w):
         logits, idx = ctx.saved_tensors
         grad = api.moe_route_bwd(logits, idx, grad_w.contiguous(), *ctx.options)
@@ -113,6 +120,7 @@ class _Lowrank(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         _same_layout(ctx, "lowrank")
         x, a, b, w, u = ctx.saved_tensors

@@ -117,3 +117,54 @@ def test_calls_on_another_stream_than_the_default():
         got = chain()
     side.synchronize()
     assert torch.equal(got, ref)
+
+
+def test_a_second_derivative_raises():
+    d = make(24, 128, 16, 4, 40, 3, 8, torch.float32, 3)
+    logits = torch.randn(24, 16, device=DEV, requires_grad=True)
+    _, w = M.autograd.route(logits, 4, renormalize=False)
+    g, = torch.autograd.grad((w * w).sum(), logits, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+    x = d["x"].clone().requires_grad_()
+    out = M.autograd.lowrank(x, d["a"], d["b"], None, M.moe_layout(d["ids"], 4, 1))
+    g, = torch.autograd.grad((out * out).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+@pytest.mark.parametrize("T,A", [(48, 3), (4200, 1)])
+def test_training_pass_in_a_graph(T, A):
+    """Forward and backward of router and adapters captured together, replayed on new values."""
+    E, K = 16, 4
+    d = make(T, 128, E, K, 40, A, 16, torch.bfloat16, 5)
+    h = M.moe_layout(d["ids"], A + 1, 1)
+    base = torch.zeros_like(d["x"])
+    gw = torch.randn(T, K, device=DEV)
+    logits = torch.randn(T, E, device=DEV)
+    static = [d["x"], d["a"], d["b"], base, logits]
+
+    def step():
+        x, a, b, c, z = (t.detach().requires_grad_() for t in static)
+        _, w = M.autograd.route(z, K, renormalize=False)
+        out = M.autograd.lowrank(x, a, b, None, h, c)
+        return (out, w) + torch.autograd.grad((out, w), (x, a, b, c, z), (d["g"], gw))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(3):
+        torch.manual_seed(seed)
+        for t in static:
+            t.normal_()
+        ref = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
