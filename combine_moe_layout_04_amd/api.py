@@ -66,6 +66,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device) -> int:
@@ -82,7 +83,7 @@ def _need(t: torch.Tensor, name: str, device, shape=None, dtype=None):
         raise ValueError(f"{name} must be on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -440,11 +441,13 @@ def _run(dev, where: str, *args) -> None:
     """The library call `where` on torch's current stream of `dev`, with `dev`
     current while it launches."""
     f = getattr(lib(), where)
-    if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(dev)), where)
+    if dev.index == _CURRENT_DEVICE():  # a tensor on it exists: the device is initialised
+        rc = f(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(dev)), where)
+            rc = f(*args, _stream(dev))
+    if rc != 0:
+        raise MoeError(rc, where)
 
 
 _ROUTE_OPTIONS = {}  # options -> the struct the library reads (a handful in any program)
