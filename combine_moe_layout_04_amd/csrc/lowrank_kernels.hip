@@ -107,13 +107,14 @@ struct Shrink {
   static constexpr int kRows = 16 * (RT + kStaged);            // rows of a stage: the tokens', then the bank's
   static constexpr int kWaves = JT + RT <= 3 ? 8 : 4;
   static constexpr size_t kLds = (size_t)kWaves * kRows * 128;  // at most 48 KiB
+  static constexpr int kKeep = JT * 16 + 4;                     // floats of a row of u kept in LDS
 };
 
 // Rows [lo, hi) of adapter e, of the RT tiles from r0 on, ranks [j0, j0 + 16 JT);
-// the whole workgroup.  t, load_t: the tokens of this lane's rows as an operand and in a load.
+// the whole workgroup.  keep: where the rows' u go as well, [16][kKeep], or null.  t, load_t: the tokens of this lane's rows as an operand and in a load.
 template <int DT, int JT, int RT, bool FAR>
 __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, int r0, int j0, int e, int lo,
-                                            int hi, const int (&t)[RT], const int (&load_t)[2 * RT]) {
+                                            int hi, const int (&t)[RT], const int (&load_t)[2 * RT], float* keep) {
   constexpr int kShrinkWaves = Shrink<JT, RT>::kWaves, kMeet = Shrink<JT, RT>::kMeet;
   constexpr int kStaged = Shrink<JT, RT>::kStaged, kRows = Shrink<JT, RT>::kRows;
   constexpr int kDepth = JT + RT <= 2 ? 3 : JT + RT <= 4 ? 2 : 1;
@@ -245,6 +246,7 @@ __device__ __forceinline__ void shrink_rows(const LowrankArgs& a, u32x4* lds, in
             v *= w;
           }
           *reinterpret_cast<f32x4*>(a.u + p * a.r + j) = v;
+          if (keep) *reinterpret_cast<f32x4*>(keep + col * Shrink<JT, RT>::kKeep + j) = v;
         }
       }
     }
@@ -272,7 +274,7 @@ __global__ __launch_bounds__((Shrink<JT, RT>::kWaves * kWave)) void shrink_kerne
   for (int rt = 0; rt < RT; ++rt) t[rt] = row_token(a, r0 + rt * kTile + (lane & 15));
   load_offsets(off, a);
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
-    shrink_rows<DT, JT, RT, FAR>(a, lds, r0, blockIdx.z * JT * 16, e, lo, hi, t, load_t);
+    shrink_rows<DT, JT, RT, FAR>(a, lds, r0, blockIdx.z * JT * 16, e, lo, hi, t, load_t, nullptr);
   });
 }
 
@@ -386,10 +388,9 @@ struct Expand {
     }
   }
 
-  // row p of u, this lane's part of every block (ranks past the last: other ranks')
-  static __device__ __forceinline__ void load_u(const LowrankArgs& a, int p, f32x4 (&u4)[BLOCKS][V / 4]) {
+  // a row of u, this lane's part of every block (ranks past the last: other ranks')
+  static __device__ __forceinline__ void load_u(const LowrankArgs& a, const float* u, f32x4 (&u4)[BLOCKS][V / 4]) {
     const int q = lane_id() >> 4;
-    const float* u = a.u + (size_t)p * a.r;
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
 #pragma unroll
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(kExpandWaves* kWave, BLOCKS <= 2 ? 2 : 1) void expa
   f32x4 next_u[BLOCKS][X::V / 4];
   float next_w = 1.f;
   X::load_base(a, next_t, c0, next_base);
-  X::load_u(a, min(tile * kTile + col, a.R - 1), next_u);
+  X::load_u(a, a.u + (size_t)min(tile * kTile + col, a.R - 1) * a.r, next_u);
   if (a.w) next_w = a.w[max(next_t, 0)];
   int after_t = row_token(a, (tile + 1) * kTile + col);
   int held = -1;  // the adapter whose bank is held
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(kExpandWaves* kWave, BLOCKS <= 2 ? 2 : 1) void expa
     next_t = after_t;
     if (tile + 1 < tile_end) {
       X::load_base(a, next_t, c0, next_base);
-      X::load_u(a, min(r0 + kTile + col, a.R - 1), next_u);
+      X::load_u(a, a.u + (size_t)min(r0 + kTile + col, a.R - 1) * a.r, next_u);
       if (a.w) next_w = a.w[max(next_t, 0)];
     }
     after_t = row_token(a, (tile + 2) * kTile + col);
@@ -517,14 +518,17 @@ __global__ __launch_bounds__(kExpandWaves* kWave, BLOCKS <= 2 ? 2 : 1) void expa
 // For few tokens with small banks: one workgroup per (tile, slot) does both for
 // the adapter's rows, where two launches would each pay for starting, reading
 // the offsets and the tokens.  It walks the wide columns with its own waves, so
-// it is for banks that one CU reads in the time of a launch.
+// it is for banks that one CU reads in the time of a launch.  (48 tokens of 2048
+// bfloat16, 32 adapters of rank 16: 11.0 us, 11.5 with u read back from memory; a
+// wave issues 1050 instructions in 3 us and waits for loads half of the time.)
 template <int DT, int JT>
 struct Both {
   static constexpr int kBlocks = DT == kBF16 ? (JT + 1) / 2 : JT;
   using X = Expand<DT, kBlocks>;
   static constexpr int kWaves = Shrink<JT, 1>::kWaves;
   static constexpr size_t kProducts = (size_t)kWaves * X::kProducts * 4;
-  static constexpr size_t kLds = Shrink<JT, 1>::kLds > kProducts ? Shrink<JT, 1>::kLds : kProducts;
+  static constexpr size_t kStage = Shrink<JT, 1>::kLds > kProducts ? Shrink<JT, 1>::kLds : kProducts;
+  static constexpr size_t kLds = kStage + (size_t)kTile * Shrink<JT, 1>::kKeep * 4;
 };
 
 template <int DT, int JT>
@@ -541,6 +545,7 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
   t[0] = row_token(a, r0 + (lane & 15));
   load_offsets(off, a);
   float* prod = reinterpret_cast<float*>(lds) + (size_t)wave * X::kProducts;
+  float* keep = reinterpret_cast<float*>(lds) + Both<DT, JT>::kStage / 4;  // u, from one step to the other
   each_adapter(off, a.E, r0, r1, blockIdx.y, gridDim.y, [&](int e, int lo, int hi) {
     // the first columns' bank and base, which do not wait for u, are asked for ahead
     X x;
@@ -550,11 +555,10 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
       if (e < a.A) x.load_bank(a, e, c0);
       X::load_base(a, t[0], c0, base);
     }
-    shrink_rows<DT, JT, 1, false>(s, lds, r0, 0, e, lo, hi, t, load_t);
-    __syncthreads();  // u is written
+    shrink_rows<DT, JT, 1, false>(s, lds, r0, 0, e, lo, hi, t, load_t, keep);
     float f[Both<DT, JT>::kBlocks][X::V];
     f32x4 u4[Both<DT, JT>::kBlocks][X::V / 4];
-    X::load_u(a, min(r0 + (lane & 15), a.R - 1), u4);
+    X::load_u(a, keep + (lane & 15) * Shrink<JT, 1>::kKeep, u4);
     X::weigh(a, u4, a.w ? a.w[max(t[0], 0)] : 1.f, f);
     while (c0 < a.wch) {
       x.rows(a, prod, r0, e, lo, hi, t[0], c0, f, base);
