@@ -565,7 +565,7 @@ def moe_few(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional[torc
     if workspace is None:
         # a call that the library refuses launches nothing: its workspace need not be allocated
         pairs = T * K if T * K <= FEW_MAX_PAIRS else 0
-        workspace = x.new_empty(pairs * I)
+        workspace = x.new_empty(pairs * I if dt == MOE_F32 else 2 * pairs * I)
     else:
         _need(workspace, "workspace", dev)
     _run(dev, "moe_few", x.data_ptr(), dt, T, H, topk_idx.data_ptr(), _itype(topk_idx), K, _ptr(topk_weights),

@@ -24,7 +24,7 @@ int moe_few_workspace_size(int dtype, int64_t T, int K, int64_t I, size_t* bytes
   if (!bytes) return MOE_ERR_INVALID_ARG;
   const int st = check_few(dtype, T, K, K, 16, I);
   if (st != MOE_OK) return st;
-  *bytes = (size_t)T * K * I * moe::elem_bytes(dtype);
+  *bytes = (size_t)T * K * I * sizeof(float);  // float32, or two bfloat16 parts
   return MOE_OK;
 }
 
@@ -43,7 +43,7 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
   if (!moe::aligned(topk_idx, itype == MOE_I32 ? 4 : 8) || (topk_weights && !moe::aligned(topk_weights, 4)))
     return MOE_ERR_ALIGNMENT;
   const size_t es = moe::elem_bytes(dtype);
-  if (workspace_bytes < (size_t)T * K * I * es) return MOE_ERR_WORKSPACE;
+  if (workspace_bytes < (size_t)T * K * I * sizeof(float)) return MOE_ERR_WORKSPACE;
   moe::FewArgs a{};
   a.x = x;
   a.idx = topk_idx;

@@ -17,6 +17,12 @@
 // top-k sum is formed there in k order, so that no second pass over pairs and
 // no order left to chance remain.  An id outside [0, E) belongs to no expert
 // here and adds nothing.
+//
+// act goes from one kernel to the other as float32, or for bfloat16's matrix
+// instructions as two parts, hi + lo, within 2^-16 of the value: rounded to one
+// bfloat16 it would make the result half as wrong again (against the formula in 64
+// bits 2.4e-3 instead of 1.7e-3, which is the result's own rounding).  It costs 189
+// -> 206 us at 64 tokens of 128 experts, 18.9 -> 19.5 us at one token.
 #include <algorithm>
 
 #include "device_common.h"
@@ -32,6 +38,9 @@ __device__ __forceinline__ int pair_expert(const FewArgs& a, int p) {  // -1: no
                                        : static_cast<const int64_t*>(a.idx)[p];
   return e >= 0 && e < a.E ? (int)e : -1;
 }
+
+template <int DT>
+constexpr int kActParts = DT == kBF16 ? 2 : 1;  // rows of the workspace a pair has
 
 // The pairs of a call grouped by expert, in a workgroup's LDS.
 struct Groups {
@@ -147,10 +156,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
     gate = make_rows(static_cast<const char*>(a.w13) + first * row_bytes, bytes);
     up = make_rows(static_cast<const char*>(a.w13) + (first + a.I) * row_bytes, bytes);
   };
-  auto tokens = [&](int first) {  // columns past the last pair repeat it and are not stored
+  auto tokens = [&](int first) {  // columns past the last pair are zeros and not stored
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-      x_off[c] = (uint32_t)(list[min(first + c * 4 + at.row, n - 1)] / a.K) * row_bytes + at.chunk * 16;
+    for (int c = 0; c < NT; ++c) {
+      const int pos = first + c * 4 + at.row;
+      const uint32_t off = (uint32_t)(list[min(pos, n - 1)] / a.K) * row_bytes + at.chunk * 16;
+      x_off[c] = pos < n ? off : kOutside;
+    }
   };
   auto fetch = [&](int d, int i) {  // the i-th line after `start`; past the last: zeros
     const int line = i >= lines ? 0 : i + start < lines ? i + start : i + start - lines;
@@ -233,11 +245,16 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
         const int pos = this_first + c * 4 + t;
         if (pos < this_n && this_i + column < a.I) {
           const float v = gated(sg, su, a.act);
-          const size_t to = (size_t)this_list[pos] * a.I + this_i + column;
-          // act is rounded to the element type: the second product's operand,
-          // as between two separate products
-          if constexpr (DT == kF32) static_cast<float*>(a.mid)[to] = v;
-          else static_cast<uint16_t*>(a.mid)[to] = (uint16_t)f32_to_bf16(v);
+          const size_t to = (size_t)this_list[pos] * kActParts<DT> * a.I + this_i + column;
+          if constexpr (DT == kF32) {
+            static_cast<float*>(a.mid)[to] = v;
+          } else {  // the part that is left is none of a number beyond the finite ones
+            const uint32_t hi = round_bf16x2(v, 0.f);
+            const float rest = v - __uint_as_float(hi << 16);
+            uint16_t* mid = static_cast<uint16_t*>(a.mid) + to;
+            mid[0] = (uint16_t)hi;
+            mid[a.I] = (uint16_t)round_bf16x2(fabsf(rest) < INFINITY ? rest : 0.f, 0.f);
+          }
         }
       }
     }
@@ -256,7 +273,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   __shared__ Groups groups;
   __shared__ float weight[kFewMaxPairs];
   __shared__ uint8_t here[kFewMaxPairs];
-  constexpr int kCols = 4 * NR;
+  constexpr int kCols = 4 * NR, kParts = kActParts<DT>;
   extern __shared__ float y[];  // [split][pairs][kCols]
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
@@ -273,12 +290,12 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
   const uint32_t row_bytes = (uint32_t)nch * 16;
   const int h0 = blockIdx.x * kCols;
   const size_t tile_bytes = (size_t)min(kCols, a.H - h0) * row_bytes;
-  const auto mid = make_rows(a.mid, (size_t)a.pairs * row_bytes);
+  const auto mid = make_rows(a.mid, (size_t)a.pairs * kParts * row_bytes);
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
   const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 15) / 16);
   const int rounds = (a.part_lines + kDepth - 1) / kDepth;
 
-  u32x4 w[kDepth][NR], b[kDepth][NT];
+  u32x4 w[kDepth][NR], b[kDepth][NT][kParts];
   auto w2 = make_rows(a.w2, 0);
   uint32_t m_off[NT];
   int n = 0;  // pairs of the fetched item
@@ -289,19 +306,25 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     n = (int)(group & 1023);
     w2 = make_rows(static_cast<const char*>(a.w2) + ((size_t)(group >> 20) * a.H + h0) * row_bytes, tile_bytes);
   };
-  auto pairs_of = [&](int first) {  // columns past the last pair repeat it and are not stored
+  auto pairs_of = [&](int first) {  // columns past the last pair are zeros and not stored
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-      m_off[c] = (uint32_t)list[min(first + c * 4 + at.row, n - 1)] * row_bytes + at.chunk * 16;
+    for (int c = 0; c < NT; ++c) {
+      const int pos = first + c * 4 + at.row;
+      const uint32_t off = (uint32_t)list[min(pos, n - 1)] * kParts * row_bytes + at.chunk * 16;
+      m_off[c] = pos < n ? off : kOutside;
+    }
   };
-  auto fetch = [&](int d, int i) {  // past the part's last line: zeros
-    const int line = min(i, hi - 1);
-    const bool in = i < hi && line * 16 + at.chunk < nch;
+  auto fetch = [&](int d, int next) {  // past the part's last line: zeros
+    const int line = min(next, hi - 1);
+    const bool in = next < hi && line * 16 + at.chunk < nch;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
       w[d][r] = load_rows<true>(w2, in ? w_off + r * 4 * row_bytes : kOutside, (uint32_t)line * 256);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) b[d][c] = load_rows(mid, in ? m_off[c] : kOutside, (uint32_t)line * 256);
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        b[d][c][i] = load_rows(mid, in ? m_off[c] : kOutside, (uint32_t)line * 256 + i * row_bytes);
   };
   if (wave < items) {
     item(wave);
@@ -337,7 +360,9 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int r = 0; r < NR; ++r) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c], acc[c][r]);
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c][i], acc[c][r]);
       in_order();
       fetch(d, next_line + d);  // past the end: zeros
       in_order();

@@ -35,7 +35,7 @@ def test_few_empty_and_workspace(L):  # noqa: F811
     a = dict(GOOD, T=0, x=None, idx=None, w=None, w13=None, w2=None, out=None, ws=None, ws_bytes=0)
     assert L.moe_few(*(a[n] for n in ORDER), None) == C["MOE_OK"]
     n = ctypes.c_size_t()
-    assert L.moe_few_workspace_size(1, 4, 2, 32, ctypes.byref(n)) == 0 and n.value == 512
+    assert L.moe_few_workspace_size(1, 4, 2, 32, ctypes.byref(n)) == 0 and n.value == 1024
     assert L.moe_few_workspace_size(0, 512, 1, 4, ctypes.byref(n)) == 0 and n.value == 8192
     assert L.moe_few_workspace_size(0, 513, 1, 4, ctypes.byref(n)) == C["MOE_ERR_UNSUPPORTED"]
     assert L.moe_few_workspace_size(3, 4, 1, 4, ctypes.byref(n)) == C["MOE_ERR_UNSUPPORTED"]
