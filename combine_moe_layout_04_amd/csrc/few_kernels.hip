@@ -21,8 +21,8 @@
 // act goes from one kernel to the other as float32, or for bfloat16's matrix
 // instructions as two parts, hi + lo, within 2^-16 of the value: rounded to one
 // bfloat16 it would make the result half as wrong again (against the formula in 64
-// bits 2.4e-3 instead of 1.7e-3, which is the result's own rounding).  It costs 189
-// -> 206 us at 64 tokens of 128 experts, 18.9 -> 19.5 us at one token.
+// bits 2.4e-3 instead of 1.7e-3, which is the result's own rounding).  It costs 10
+// of 193 us at 64 tokens of 128 experts, 0.6 of 19.5 us at one token.
 #include <algorithm>
 
 #include "device_common.h"
@@ -99,6 +99,13 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return 0.5f * g * (1.f + tanhf(y)) * u;
 }
 
+// Workgroups go to the 8 XCDs in turn: of every 64, 8 neighbouring places go to
+// one, whose L2 joins what they write to the same lines.
+__device__ __forceinline__ int place_of_block() {
+  const int b = blockIdx.x;
+  return b < (int)(gridDim.x & ~63u) ? (b & ~63) + (b & 7) * 8 + (b >> 3 & 7) : b;
+}
+
 // act, in items of (expert, 8 columns).  A workgroup's waves take the 256-byte
 // lines of the item's rows in turn and meet in LDS; they work in rounds of
 // kDepth lines each and ask for the next round's while they multiply this
@@ -128,7 +135,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 
   const int slabs = (a.I + 7) / 8;
   const int items = group_pairs<kFewMaxPairs / (kUpWaves * kWave)>(a, groups) * slabs;
-  int item = blockIdx.x;
+  int item = place_of_block();
   if (item >= items) return;  // the whole workgroup
 
   const int nch = a.hch;  // chunks of an x or w13 row
@@ -136,7 +143,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
   const int lines = (nch + 15) / 16;
   const int rounds = (lines + kUpWaves * kDepth - 1) / (kUpWaves * kDepth);
-  const int start = blockIdx.x * 2 % lines;
+  const int start = item * 2 % lines;
   const auto xs = make_rows(a.x, (size_t)a.T * row_bytes);
 
   u32x4 wg[kDepth][2], wu[kDepth][2], b[kDepth][NT];
@@ -248,12 +255,15 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
           const size_t to = (size_t)this_list[pos] * kActParts<DT> * a.I + this_i + column;
           if constexpr (DT == kF32) {
             static_cast<float*>(a.mid)[to] = v;
-          } else {  // the part that is left is none of a number beyond the finite ones
-            const uint32_t hi = round_bf16x2(v, 0.f);
-            const float rest = v - __uint_as_float(hi << 16);
-            uint16_t* mid = static_cast<uint16_t*>(a.mid) + to;
-            mid[0] = (uint16_t)hi;
-            mid[a.I] = (uint16_t)round_bf16x2(fabsf(rest) < INFINITY ? rest : 0.f, 0.f);
+          } else {
+            // two columns a lane: hi in the even lanes, lo in the odd ones (none
+            // of a number beyond the finite ones); I is a multiple of 8
+            float rest = v - __uint_as_float(round_bf16x2(v, 0.f) << 16);
+            rest = fabsf(rest) < INFINITY ? rest : 0.f;
+            const bool odd = column & 1;
+            const float next = quad_move<0xB1>(odd ? v : rest);
+            const uint32_t two = odd ? round_bf16x2(next, rest) : round_bf16x2(v, next);
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.mid) + to + (odd ? a.I - 1 : 0)) = two;
           }
         }
       }
@@ -269,7 +279,7 @@ constexpr int kDownWaves = 16;
 
 template <int DT, int NT, int NR>
 __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
-  constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 269, 256, 264 us a call with 1, 2, 3
+  constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 274, 271, 279 us a call with 1, 2, 3
   __shared__ Groups groups;
   __shared__ float weight[kFewMaxPairs];
   __shared__ uint8_t here[kFewMaxPairs];
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
 
   const int nch = a.ich;  // chunks of an act or w2 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
-  const int h0 = blockIdx.x * kCols;
+  const int h0 = place_of_block() * kCols;
   const size_t tile_bytes = (size_t)min(kCols, a.H - h0) * row_bytes;
   const auto mid = make_rows(a.mid, (size_t)a.pairs * kParts * row_bytes);
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
@@ -426,9 +436,9 @@ hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
   // By the pairs an expert of the call has on average.  More tiles read fewer
   // weights twice and multiply more zeros, which float32's matrix rate feels
   // first (2048 x 768, 32 experts of all that are chosen from; us with 1, 2, 3, 4
-  // tiles.  bfloat16, 2 pairs: 44 44 46 48, 4: 68 55 55 61, 8: 108 75 64 66, 16:
-  // 190 123 105 98; float32, 2: 100 105 137 171, 4: 126 112 146 176, 8: 221 159
-  // 158 180, 16: 404 279 270 297).
+  // tiles.  bfloat16, 1 pair: 24 26 28 31, 4: 70 57 60 66, 8: 113 81 69 73, 16: 197
+  // 134 113 109; float32, 1: 42 41 52 64, 4: 127 109 137 168, 8: 221 154 151 175, 16:
+  // 400 270 264 281).
   if (a.pairs <= 2 * a.E) return launch_few_typed<DT, 1>(a, s);
   if (a.pairs <= (DT == kF32 ? 8 : 4) * a.E) return launch_few_typed<DT, 2>(a, s);
   if (DT == kF32 || a.pairs <= 8 * a.E) return launch_few_typed<DT, 3>(a, s);
