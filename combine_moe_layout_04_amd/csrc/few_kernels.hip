@@ -99,6 +99,16 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
   return 0.5f * g * (1.f + tanhf(y)) * u;
 }
 
+// Whether one tile of 4 pairs does: the host goes by all pairs of a call, of which
+// many may belong to other ranks' experts (13 tokens, top 8 of 256, 32 of them here,
+// 7168 x 2048, bfloat16: the second kernel 67 us with the two tiles that the pairs
+// call for, 59 with one; float32 gains nothing, and the choice costs it 3%).
+__device__ __forceinline__ bool one_tile(const Groups& g, int experts) {
+  if (experts == 0) return true;
+  const uint32_t last = (uint32_t)__builtin_amdgcn_readfirstlane((int)g.used[experts - 1]);
+  return 4 * (int)((last >> 10 & 1023) + (last & 1023)) <= 9 * experts;
+}
+
 // Workgroups go to the 8 XCDs in turn: of every 64, 8 neighbouring places go to
 // one, whose L2 joins what they write to the same lines.
 __device__ __forceinline__ int place_of_block() {
@@ -113,30 +123,29 @@ __device__ __forceinline__ int place_of_block() {
 //
 // What decides how near to the memory's rate this comes (64 tokens, 126 experts
 // of 768 columns and rows of 4 KiB, 0.79 GB):
-//   - the order of lanes in a load (mfma.h): 134 -> 125 us, the last of the three,
-//     6.3 TB/s;
+//   - the order of lanes in a load (mfma.h): 134 -> 125 us;
+//   - neighbouring places to one XCD: 132 -> 120 us, the last of the four (act's
+//     lines, written in pieces from 8 L2s, had cost 6 us by then), 6.6 TB/s;
 //   - workgroup b takes items b, b + grid, ..., so that all of them together
 //     move through a narrow window of the weights: 164 us with even runs of
 //     neighbouring items, 140 us in steps;
 //   - each workgroup starts at another line of its rows (and goes round): rows
 //     4 KiB apart read at the same place at the same time meet in a few memory
-//     channels.  140 -> 134 us.  The order of the sum depends on the item
-//     through its workgroup alone, so it is the same in every run.
+//     channels.  140 -> 134 us.  The order of the sum depends on the workgroup
+//     alone, so it is the same in every run.
 constexpr int kUpWaves = 8;
 constexpr int kUpGroups = 512;  // workgroups at most: two a CU
 
 template <int DT, int NT>
-__global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
+__device__ __forceinline__ void few_up(const FewArgs& a, const Groups& groups, int items, float* parts) {
   constexpr int kDepth = 1;  // the other waves' lines are in flight meanwhile
-  __shared__ Groups groups;
-  __shared__ float part[kUpWaves][NT][2][2][16];  // wave, tile of pairs, tile of rows, gate or up, row * 4 + pair
+  // wave, tile of pairs, tile of rows, gate or up, row * 4 + pair
+  auto& part = *reinterpret_cast<float(*)[kUpWaves][NT][2][2][16]>(parts);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
   const int slabs = (a.I + 7) / 8;
-  const int items = group_pairs<kFewMaxPairs / (kUpWaves * kWave)>(a, groups) * slabs;
   int item = place_of_block();
-  if (item >= items) return;  // the whole workgroup
 
   const int nch = a.hch;  // chunks of an x or w13 row
   const uint32_t row_bytes = (uint32_t)nch * 16;
@@ -271,28 +280,32 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
   }
 }
 
+template <int DT, int NT>
+__global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
+  __shared__ Groups groups;
+  __shared__ float parts[kUpWaves * NT * 64];
+  const int experts = group_pairs<kFewMaxPairs / (kUpWaves * kWave)>(a, groups);
+  const int items = experts * ((a.I + 7) / 8);
+  if (place_of_block() >= items) return;  // the whole workgroup
+  if (DT == kBF16 && NT > 1 && one_tile(groups, experts)) few_up<DT, 1>(a, groups, items, parts);
+  else few_up<DT, NT>(a, groups, items, parts);
+}
+
 // 4 NR columns of out, for every pair.  A wave's item is (expert, part of the sum
 // over I); it leaves its pairs' values in y[part][pair].  The waves stream
 // their items' weights in rounds of kDepth lines, the next round's (of the same
-// item or the next) under way during this one.
+// item or the next) under way during this one.  (64 tokens, 126 experts of 768
+// columns, rows of 1.5 KiB, 0.4 GB: 76 us, 5.2 TB/s; 66 us with act in one part.)
 constexpr int kDownWaves = 16;
 
 template <int DT, int NT, int NR>
-__global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
+__device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups, int experts, float* y) {
   constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 274, 271, 279 us a call with 1, 2, 3
-  __shared__ Groups groups;
-  __shared__ float weight[kFewMaxPairs];
-  __shared__ uint8_t here[kFewMaxPairs];
   constexpr int kCols = 4 * NR, kParts = kActParts<DT>;
-  extern __shared__ float y[];  // [split][pairs][kCols]
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
-  if (threadIdx.x < a.pairs) {
-    weight[threadIdx.x] = a.w ? a.w[threadIdx.x] : 1.f;
-    here[threadIdx.x] = pair_expert(a, threadIdx.x) >= 0;
-  }
-  const int items = group_pairs<1>(a, groups) * a.split;
+  const int items = experts * a.split;
   // the split divides the number of waves: a wave has one part of all its experts
   const int part = wave % a.split;
 
@@ -394,6 +407,23 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     first = next_first;
     round = next_round;
   }
+}
+
+template <int DT, int NT, int NR>
+__global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) {
+  constexpr int kCols = 4 * NR;
+  __shared__ Groups groups;
+  __shared__ float weight[kFewMaxPairs];
+  __shared__ uint8_t here[kFewMaxPairs];
+  extern __shared__ float y[];  // [split][pairs][kCols]
+  if (threadIdx.x < a.pairs) {
+    weight[threadIdx.x] = a.w ? a.w[threadIdx.x] : 1.f;
+    here[threadIdx.x] = pair_expert(a, threadIdx.x) >= 0;
+  }
+  const int experts = group_pairs<1>(a, groups);
+  if (DT == kBF16 && NT > 1 && one_tile(groups, experts)) few_down<DT, 1, NR>(a, groups, experts, y);
+  else few_down<DT, NT, NR>(a, groups, experts, y);
+  const int h0 = place_of_block() * kCols;
   __syncthreads();
 
   for (int o = threadIdx.x; o < a.T * kCols; o += kDownWaves * kWave) {
@@ -438,7 +468,9 @@ hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
   // first (2048 x 768, 32 experts of all that are chosen from; us with 1, 2, 3, 4
   // tiles.  bfloat16, 1 pair: 24 26 28 31, 4: 70 57 60 66, 8: 113 81 69 73, 16: 197
   // 134 113 109; float32, 1: 42 41 52 64, 4: 127 109 137 168, 8: 221 154 151 175, 16:
-  // 400 270 264 281).
+  // 400 270 264 281).  Each a kernel of its own: the registers of the most tiles
+  // would cost the others their second workgroup on a CU (32 tokens, top 2 of 16,
+  // 512 x 256, bfloat16: 12.2 us so, 14.0 with all in one).
   if (a.pairs <= 2 * a.E) return launch_few_typed<DT, 1>(a, s);
   if (a.pairs <= (DT == kF32 ? 8 : 4) * a.E) return launch_few_typed<DT, 2>(a, s);
   if (DT == kF32 || a.pairs <= 8 * a.E) return launch_few_typed<DT, 3>(a, s);
