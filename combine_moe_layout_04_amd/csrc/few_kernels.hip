@@ -452,8 +452,8 @@ hipError_t launch_few_typed(const FewArgs& a, hipStream_t s) {
   const dim3 block(kDownWaves * kWave);
   const size_t column = (size_t)a.split * a.pairs * sizeof(float);
   // 4 columns of out a workgroup where 8 would leave CUs without one (the kernel with
-  // 8 and 4, us: 57 tokens, top 6 of 60, 288 x 140 float32 26.6 and 15.2; 30, top 8 of
-  // 40, 1024 x 400 bfloat16 18.2 and 14.0; 1, top 4 of 64, 512 x 256 5.7 and 5.1)
+  // 8 and 4, us: 57 tokens, top 6 of 60, 288 x 140 float32 24.0 and 15.4; 30, top 8 of
+  // 40, 1024 x 400 bfloat16 23.4 and 19.3; 1, top 4 of 64, 512 x 256 5.8 and 5.3)
   if (a.H < 8 * 256)
     hipLaunchKernelGGL((few_down_kernel<DT, NT, 1>), dim3((a.H + 3) / 4), block, column * 4, s, a);
   else
