@@ -24,7 +24,7 @@ int moe_few_workspace_size(int dtype, int64_t T, int K, int64_t I, size_t* bytes
   if (!bytes) return MOE_ERR_INVALID_ARG;
   const int st = check_few(dtype, T, K, K, 16, I);
   if (st != MOE_OK) return st;
-  *bytes = (size_t)T * K * I * sizeof(float);  // float32, or two bfloat16 parts
+  *bytes = (size_t)T * K * I * sizeof(float);
   return MOE_OK;
 }
 
@@ -50,7 +50,7 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
   a.w = topk_weights;
   a.w13 = w13;
   a.w2 = w2;
-  a.mid = workspace;
+  a.mid = static_cast<float*>(workspace);
   a.out = out;
   a.T = (int)T;
   a.K = K;

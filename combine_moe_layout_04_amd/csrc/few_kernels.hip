@@ -18,11 +18,13 @@
 // no order left to chance remain.  An id outside [0, E) belongs to no expert
 // here and adds nothing.
 //
-// act goes from one kernel to the other as float32, or for bfloat16's matrix
-// instructions as two parts, hi + lo, within 2^-16 of the value: rounded to one
-// bfloat16 it would make the result half as wrong again (against the formula in 64
-// bits 2.4e-3 instead of 1.7e-3, which is the result's own rounding).  It costs 10
-// of 193 us at 64 tokens of 128 experts, 0.6 of 19.5 us at one token.
+// act goes from one kernel to the other as float32; for bfloat16's matrix
+// instructions the second kernel cuts it into three parts (Parts in mfma.h), which
+// lose nothing.  Rounded to one bfloat16 it would make the result half as wrong
+// again (against the formula in 64 bits 2.4e-3 instead of 1.7e-3, the result's own
+// rounding); in two rounded parts it lost the last 8 bits, and cost, with two and
+// three parts, 193 and 197 us at 64 tokens of 128 experts, 19.6 and 19.8 at one
+// token, 106 and 116 at 16 pairs for each of 32 experts.
 #include <algorithm>
 
 #include "device_common.h"
@@ -39,8 +41,11 @@ __device__ __forceinline__ int pair_expert(const FewArgs& a, int p) {  // -1: no
   return e >= 0 && e < a.E ? (int)e : -1;
 }
 
+// Chunks of act for one of w2: act is float32, and stands in the workspace so
+// that the loads of both go alike.  For bfloat16 a pair's row is the first four
+// of every eight columns, then the last four.
 template <int DT>
-constexpr int kActParts = DT == kBF16 ? 2 : 1;  // rows of the workspace a pair has
+constexpr int kActChunks = DT == kBF16 ? 2 : 1;
 
 // The pairs of a call grouped by expert, in a workgroup's LDS.
 struct Groups {
@@ -261,19 +266,9 @@ __device__ __forceinline__ void few_up(const FewArgs& a, const Groups& groups, i
         const int pos = this_first + c * 4 + t;
         if (pos < this_n && this_i + column < a.I) {
           const float v = gated(sg, su, a.act);
-          const size_t to = (size_t)this_list[pos] * kActParts<DT> * a.I + this_i + column;
-          if constexpr (DT == kF32) {
-            static_cast<float*>(a.mid)[to] = v;
-          } else {
-            // two columns a lane: hi in the even lanes, lo in the odd ones (none
-            // of a number beyond the finite ones); I is a multiple of 8
-            float rest = v - __uint_as_float(round_bf16x2(v, 0.f) << 16);
-            rest = fabsf(rest) < INFINITY ? rest : 0.f;
-            const bool odd = column & 1;
-            const float next = quad_move<0xB1>(odd ? v : rest);
-            const uint32_t two = odd ? round_bf16x2(next, rest) : round_bf16x2(v, next);
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.mid) + to + (odd ? a.I - 1 : 0)) = two;
-          }
+          // (bfloat16: I is a multiple of 8)
+          const int place = DT == kF32 ? this_i + column : (column >> 2) * (a.I / 2) + this_i / 2 + (column & 3);
+          a.mid[(size_t)this_list[pos] * a.I + place] = v;
         }
       }
     }
@@ -295,13 +290,16 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 // over I); it leaves its pairs' values in y[part][pair].  The waves stream
 // their items' weights in rounds of kDepth lines, the next round's (of the same
 // item or the next) under way during this one.  (64 tokens, 126 experts of 768
-// columns, rows of 1.5 KiB, 0.4 GB: 76 us, 5.2 TB/s; 66 us with act in one part.)
+// columns, rows of 1.5 KiB, 0.4 GB: 76 us, 5.2 TB/s; 66 us with act rounded to one
+// part.)
 constexpr int kDownWaves = 16;
 
 template <int DT, int NT, int NR>
 __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups, int experts, float* y) {
-  constexpr int kDepth = 2;  // 13 tokens, 32 experts of 4096 x 2048: 274, 271, 279 us a call with 1, 2, 3
-  constexpr int kCols = 4 * NR, kParts = kActParts<DT>;
+  // 13 tokens, 32 experts of 4096 x 2048: 274, 271, 279 us a call with 1, 2, 3; the
+  // most tiles have no registers for two
+  constexpr int kDepth = NT * NR < 8 ? 2 : 1;
+  constexpr int kCols = 4 * NR, kChunks = kActChunks<DT>;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
   const Lane at;
 
@@ -313,12 +311,12 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
   const uint32_t row_bytes = (uint32_t)nch * 16;
   const int h0 = place_of_block() * kCols;
   const size_t tile_bytes = (size_t)min(kCols, a.H - h0) * row_bytes;
-  const auto mid = make_rows(a.mid, (size_t)a.pairs * kParts * row_bytes);
+  const auto mid = make_rows(a.mid, (size_t)a.pairs * kChunks * row_bytes);
   const uint32_t w_off = (uint32_t)at.row * row_bytes + at.chunk * 16;
   const int lo = part * a.part_lines, hi = min(lo + a.part_lines, (nch + 15) / 16);
   const int rounds = (a.part_lines + kDepth - 1) / kDepth;
 
-  u32x4 w[kDepth][NR], b[kDepth][NT][kParts];
+  u32x4 w[kDepth][NR], b[kDepth][NT][kChunks];
   auto w2 = make_rows(a.w2, 0);
   uint32_t m_off[NT];
   int n = 0;  // pairs of the fetched item
@@ -333,7 +331,7 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       const int pos = first + c * 4 + at.row;
-      const uint32_t off = (uint32_t)list[min(pos, n - 1)] * kParts * row_bytes + at.chunk * 16;
+      const uint32_t off = (uint32_t)list[min(pos, n - 1)] * kChunks * row_bytes + at.chunk * 16;
       m_off[c] = pos < n ? off : kOutside;
     }
   };
@@ -346,7 +344,7 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int i = 0; i < kParts; ++i)
+      for (int i = 0; i < kChunks; ++i)
         b[d][c][i] = load_rows(mid, in ? m_off[c] : kOutside, (uint32_t)line * 256 + i * row_bytes);
   };
   if (wave < items) {
@@ -381,11 +379,23 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
 #pragma unroll
-      for (int c = 0; c < NT; ++c)
+      for (int c = 0; c < NT; ++c) {
+        if constexpr (DT == kF32) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
+          for (int r = 0; r < NR; ++r) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c][0], acc[c][r]);
+        } else {
+          float f[8];
+          unpack<kF32>(b[d][c][0], *reinterpret_cast<float(*)[4]>(f));
+          unpack<kF32>(b[d][c][1], *reinterpret_cast<float(*)[4]>(f + 4));
+          const Parts act(f);
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) acc[c][r] = mma_chunk<DT>(w[d][r], b[d][c][i], acc[c][r]);
+          for (int r = 0; r < NR; ++r) {
+            acc[c][r] = mma_chunk<DT>(w[d][r], act.hi, acc[c][r]);
+            acc[c][r] = mma_chunk<DT>(w[d][r], act.mid, acc[c][r]);
+            acc[c][r] = mma_chunk<DT>(w[d][r], act.lo, acc[c][r]);
+          }
+        }
+      }
       in_order();
       fetch(d, next_line + d);  // past the end: zeros
       in_order();

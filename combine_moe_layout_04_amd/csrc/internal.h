@@ -186,7 +186,7 @@ struct FewArgs {
   const float* w;         // [T, K] or null (plain sum)
   const void* w13;        // [E, 2I, H]: gate rows, then up rows
   const void* w2;         // [E, H, I]
-  void* mid;              // workspace, the activations: float32 [T*K, I], or bfloat16 [T*K, 2, I], hi and lo
+  float* mid;             // workspace, the activations [T*K, I], in an order of the kernels' own
   void* out;              // [T, H]
   int T, K, E, H, I;
   int itype, dtype, act;

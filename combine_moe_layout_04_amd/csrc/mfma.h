@@ -39,6 +39,36 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
+// Eight floats as operands of three bfloat16 products: their sign and exponent
+// with 8 bits of the significand each, cut off, not rounded, so that hi + mid + lo
+// is the float itself and a product keeps all of its 24 bits.
+struct Parts {
+  u32x4 hi, mid, lo;
+  __device__ __forceinline__ explicit Parts(const float (&f)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      float v[2], r[2], l[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[i] = f[2 * d + i];
+        r[i] = v[i] - high_half(v[i]);
+        // beyond the finite numbers the difference is not a number: no more parts
+        r[i] = r[i] - r[i] == 0.f ? r[i] : 0.f;
+        l[i] = r[i] - high_half(r[i]);
+      }
+      hi[d] = high_halves(v[0], v[1]);
+      mid[d] = high_halves(r[0], r[1]);
+      lo[d] = high_halves(l[0], l[1]);
+    }
+  }
+
+ private:
+  static __device__ __forceinline__ float high_half(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+  static __device__ __forceinline__ uint32_t high_halves(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  }
+};
+
 // Rows in memory as a buffer of `bytes` from p (uniform over the wave): a load
 // whose offset is past the end gives zeros and touches no memory, so the ends
 // of rows and tiles need no branches.  Offsets are 32 bits; kOutside lies past

@@ -397,9 +397,8 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
  *   out[t]   = round(sum_k w[t,k] * (W2_e act[t,k]))
  * with Wg the first I and Wu the last I rows of w13[e], f(g) = g / (1 +
  * exp(-g)) (MOE_ACT_SILU) or the tanh form of gelu (MOE_ACT_GELU_TANH).
- * float32 sums; act stays float32 (in bfloat16 it takes part in the product as
- * two bfloat16 halves, 16 bits of it); the sum over k runs in k order
- * from +0.0, products and sums rounded on their own.  Results are bitwise
+ * float32 sums; act stays float32, in the second product too; the sum over k
+ * runs in k order from +0.0, products and sums rounded on their own.  Results are bitwise
  * reproducible.  Only the chosen experts' weights are read.
  *
  *   x [T,H], w13 [E,2I,H], w2 [E,H,I], out [T,H] dtype, 16-byte aligned;

@@ -252,3 +252,31 @@ def test_refusals():
     with pytest.raises(M.MoeError) as e:
         M.moe_few(x, idx, w, w13, w2, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     assert e.value.code == -5
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,E", [(1, 1, 1), (3, 2, 40), (33, 2, 16), (70, 3, 16), (150, 2, 16)])
+def test_every_bit_of_act_counts(dtype, T, K, E):
+    """Columns of act in pairs, 1 + 2^-9 + 2^-s and 1 + 2^-9 with s = 10 ... 23,
+    subtracted by the second product, which leaves exactly 2^-s.  Every step is
+    exact: the gate is 64, whose sigmoid is 1 in 24 bits; the up products have three
+    terms with 24 bits between them, the other sums two; the results, powers of two,
+    need no rounding."""
+    H, I, steps = 64, 40, range(10, 24)
+    x = torch.zeros(T, H)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -4, 2.0 ** -4
+    w13, w2 = torch.zeros(E, 2 * I, H), torch.zeros(E, H, I)
+    w13[:, :I, 0] = 64.0
+    want = torch.zeros(H)
+    for n, s in enumerate(steps):
+        sign = -1.0 if n % 2 else 1.0
+        w13[:, I + 2 * n, 0] = w13[:, I + 2 * n + 1, 0] = sign
+        w13[:, I + 2 * n, 2] = w13[:, I + 2 * n + 1, 2] = sign * 2.0 ** -5
+        w13[:, I + 2 * n, 1] = sign * 2.0 ** (4 - s)
+        w2[:, n, 2 * n], w2[:, n, 2 * n + 1] = 1.0, -1.0
+        want[n] = sign * 64.0 * 2.0 ** -s
+    idx = (torch.arange(T * K) % E).view(T, K).to(torch.int32)
+    w = torch.ones(T, K)
+    w[:, 1:] = 0.0
+    got = M.moe_few(x.to(dtype).to(DEV), idx.to(DEV), w.to(DEV), w13.to(dtype).to(DEV), w2.to(dtype).to(DEV))
+    assert torch.equal(got.cpu().float(), want.expand(T, H))
