@@ -430,8 +430,8 @@ int moe_few(const void* x, int dtype, int64_t T, int64_t H, const void* topk_idx
  *   out[t] = round(base[t] + w[t] * (u[p] b_e))
  * w = topk_weights, or 1 where NULL; base, the shared projection's output, or
  * 0 where NULL; for a token without an adapter out = base and u = 0.  Sums and
- * u in float32 (u takes part in products as two bfloat16 halves, 16 bits of
- * it), one rounding at the end; results are bitwise reproducible.
+ * u in float32, in the second product too, one rounding at the end; results
+ * are bitwise reproducible.
  *
  *   x [T,H], a [num_adapters,r,H], b [num_adapters,r,N], base and out [T,N]
  *   dtype, 16-byte aligned (out may be base); topk_weights [T,1] float32; u

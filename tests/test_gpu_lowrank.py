@@ -427,3 +427,65 @@ def test_refusals():
     with pytest.raises(M.MoeError) as e:
         M.moe_lowrank_bwd(h, d["g"], x, a, b, u, grad_x=False, grad_a=False, grad_b=False)
     assert e.value.code == -1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,A,r,H,N", [(3, 2, 32, 64, 72), (40, 3, 32, 2048, 2048), (200, 2, 64, 1040, 2056),
+                                       (1100, 1, 128, 264, 264), (8300, 2, 32, 136, 136)])
+def test_every_bit_of_the_rank_space_counts(dtype, T, A, r, H, N):
+    """Ranks (and rows) in pairs with the values 1 + 2^-9 + 2^-s and 1 + 2^-9, s = 10
+    ... 23, subtracted by the second product, which leaves exactly 2^-s.  Every step
+    is exact: the values in rank space have three terms with 24 bits between them,
+    sums of the rest one or two that are not zero; the results, powers of two, need
+    no rounding.  One launch, two, and several tiles a wave."""
+    steps = list(range(10, 24))
+    n = len(steps)
+    wide = torch.tensor([2.0 ** (4 - s) for s in steps])
+
+    def pairs(W):  # [r, W]: rows 2k and 2k + 1 give 1 + 2^-9 + 2^-s_k and 1 + 2^-9 on the row `probe`
+        m = torch.zeros(r, W)
+        m[:2 * n, 0], m[:2 * n, 2] = 1.0, 2.0 ** -5
+        m[0:2 * n:2, 1] = wide
+        return m
+
+    def probe(W):
+        v = torch.zeros(T, W)
+        v[:, 0], v[:, 1], v[:, 2] = 1.0, 2.0 ** -4, 2.0 ** -4
+        return v
+
+    def minus(W):  # [r, W]: column k is rank 2k minus rank 2k + 1
+        m = torch.zeros(r, W)
+        m[torch.arange(0, 2 * n, 2), torch.arange(n)] = 1.0
+        m[torch.arange(1, 2 * n, 2), torch.arange(n)] = -1.0
+        return m
+
+    dev = lambda t: t.to(dtype).to(DEV)  # noqa: E731
+    bank = lambda m: dev(m.expand(A, *m.shape)).contiguous()  # noqa: E731
+    ids = (torch.arange(T) % A).to(torch.int32).view(T, 1).to(DEV)
+    h = M.moe_layout(ids, A, 1)
+    left = torch.tensor([2.0 ** -s for s in steps])
+    # forward: out = u b
+    out, u = M.moe_lowrank(h, dev(probe(H)), bank(pairs(H)), bank(minus(N)))
+    assert torch.equal(out.cpu().float()[:, :n], left.expand(T, n)) and (out[:, n:] == 0).all()
+    # backward: grad_x = gu a
+    gx, _, _, _ = M.moe_lowrank_bwd(h, dev(probe(N)), dev(probe(H)), bank(minus(H)), bank(pairs(N)), u, grad_a=False,
+                                    grad_b=False)
+    assert torch.equal(gx.cpu().float()[:, :n], left.expand(T, n)) and (gx[:, n:] == 0).all()
+    # two tokens of adapter 0 whose rows cancel: a weight of 1 + 2^-9 + 2^-s
+    # against one of 1 + 2^-9 for grad_a and grad_b, at rank k
+    for k, s in ((0, 10), (5, 18), (11, 20), (14, 23)):
+        x, g = torch.zeros(T, H), torch.zeros(T, N)
+        w = torch.full((T, 1), 1.0 + 2.0 ** -9)
+        last = (T - 1) // A * A  # the last token of adapter 0
+        x[0, 0], x[last, 0], g[0, 0], g[last, 0] = 1.0, -1.0, 1.0, 1.0
+        w[0] += 2.0 ** -s
+        ones = torch.zeros(r, 1)
+        ones[k] = 1.0
+        a, b = torch.zeros(r, H), torch.zeros(r, N)
+        a[:, :1], b[:, :1] = ones, ones
+        _, u = M.moe_lowrank(h, dev(x), bank(a), bank(b), w.to(DEV))
+        _, ga, gb, _ = M.moe_lowrank_bwd(h, dev(g), dev(x), bank(a), bank(b), u, w.to(DEV), grad_x=False)
+        for got in (ga, gb):
+            want = torch.zeros(got.shape)
+            want[0, k, 0] = 2.0 ** -s
+            assert torch.equal(got.cpu().float(), want), (k, s)
