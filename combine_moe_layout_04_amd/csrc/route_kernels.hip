@@ -19,6 +19,13 @@
 // choice next to a border is the definition's (16384 tokens, 256 experts: 28 us
 // in 64 bits throughout, 21 so).
 //
+// Renormalised weights need the chosen scores only up to a factor, and are formed
+// from such, relative to the largest chosen logit where their sum is small.  So no
+// sum is too small for 32 bits, however far below zero the logits lie or below the
+// others a bias takes the choice.  Sigmoids below 2^-1022 (z <
+// -708), where 64 bits begin to lose them, count as zero: masks of the type's lowest
+// value get no weight.
+//
 // Logits that are NaN count as -inf in the choice and spread to the weights
 // as the formulas say.  A sum of scores that is zero (every expert masked by
 // -inf) gives zero weights, not 0/0.
@@ -114,8 +121,32 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) {  // for small ones as exact as for large ones
+  const float e = expf(-fabsf(z));
+  return (z > 0.f ? 1.f : e) / (1.f + e);
+}
 __device__ __forceinline__ double sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
+
+// The largest chosen logit, of lanes with `mine`; 0 where there is none above -inf.
+__device__ __forceinline__ float largest_chosen(float z, bool mine) {
+  const float m = float_of(wave_max(mine ? key_of(z) : 1u));
+  return m >= -3.402823466e38f ? m : 0.f;
+}
+
+// The scores of the chosen experts (lanes with `mine`, logits z) up to a common
+// factor, and their sum: a softmax's relative to m, a sigmoid's as they are.  Where
+// that sum is small, relative to the largest chosen logit.
+__device__ __forceinline__ float chosen_scores(bool softmax, float z, bool mine, float m, float& total) {
+  float s = mine ? softmax ? expf(z - m) : sigmoid(z) : 0.f;
+  total = wave_sum(s);
+  if (total < 0x1p-20f) {  // wave-uniform; above it 32 bits hold every share that is not below 2^-106
+    const float top = largest_chosen(z, mine);
+    s = mine ? expf(z - top) : 0.f;
+    if (!softmax) s = z < -708.f ? 0.f : s / (1.f + expf(z));
+    total = wave_sum(s);
+  }
+  return s;
+}
 
 // ---- forward ----------------------------------------------------------------------
 
@@ -220,16 +251,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     }
   }
   const int e = choose<VPL>(key, lane, kWave, a.K, [](uint32_t) {});
-  float s = 0.f;
-  if (lane < a.K) {
-    const float z = load_logit<DT>(a.z, row + e);
-    s = softmax ? expf(z - m) : sigmoid(z);
-    if (bad) s = NAN;
-  }
-  if (a.renorm) total = wave_sum(s);
-  if (lane < a.K) {
+  const bool mine = lane < a.K;
+  const float z = mine ? load_logit<DT>(a.z, row + e) : -INFINITY;
+  float s = a.renorm ? chosen_scores(softmax, z, mine, m, total) : softmax ? expf(z - m) : sigmoid(z);
+  if (bad) s = NAN;
+  if (mine) {
     a.idx[(size_t)t * a.K + lane] = e;
-    a.w[(size_t)t * a.K + lane] = total == 0.f && !bad ? 0.f : s * (a.scale / total);
+    a.w[(size_t)t * a.K + lane] = total == 0.f && !bad ? 0.f : s / total * a.scale;
   }
 }
 
@@ -363,7 +391,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a) {
     nan |= z[v] != z[v];
     if (z[v] != z[v]) z[v] = -INFINITY;
   }
-  const bool bad = softmax && __ballot(nan) != 0;  // a NaN anywhere reaches every softmax weight
+  bool bad = softmax && __ballot(nan) != 0;  // a NaN anywhere reaches every softmax weight
   bool sure;
   float m, all;
   int e = choose_scored<float, VPL>(a, z, bias, g, l, sure, m, all);
@@ -371,16 +399,15 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a) {
     double m64, all64;
     e = choose_scored<double, VPL>(a, z, bias, g, l, sure, m64, all64);
   }
-  float s = 0.f;
-  if (lane < a.K) {
-    const float x = load_logit<DT>(a.z, row + e);
-    s = softmax ? expf(x - m) / all : sigmoid(x);
-    if (bad) s = NAN;
-  }
-  const float total = a.renorm ? wave_sum(s) : 1.f;
-  if (lane < a.K) {
+  bad = bad || all != all;  // +inf among the logits, chosen or not
+  const bool mine = lane < a.K;
+  const float x = mine ? load_logit<DT>(a.z, row + e) : -INFINITY;
+  float total = 1.f;
+  float s = a.renorm ? chosen_scores(softmax, x, mine, m, total) : softmax ? expf(x - m) / all : sigmoid(x);
+  if (bad) s = NAN;
+  if (mine) {
     a.idx[(size_t)t * a.K + lane] = e;
-    a.w[(size_t)t * a.K + lane] = total == 0.f && !bad ? 0.f : s * (a.scale / total);
+    a.w[(size_t)t * a.K + lane] = total == 0.f && !bad ? 0.f : s / total * a.scale;
   }
 }
 
@@ -443,14 +470,10 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
     d = G;
   } else {
     float s = 0.f;
-    if (softmax) {
-      const float m0 = float_of(wave_max(id >= 0 ? key_of(z) : 1u));
-      const float m = m0 >= -3.402823466e38f ? m0 : 0.f;
-      if (id >= 0) s = expf(z - m);
-    } else if (id >= 0) {
-      s = sigmoid(z);
-    }
-    float total = a.renorm ? wave_sum(s) : 1.f;
+    float total = 1.f;
+    const float m = softmax ? largest_chosen(z, id >= 0) : 0.f;
+    if (a.renorm) s = chosen_scores(softmax, z, id >= 0, m, total);
+    else if (id >= 0) s = sigmoid(z);
     if (total == 0.f) total = 1.f;
     const float q = s / total;  // s itself when not renormalised
     const float mean = a.renorm ? wave_sum(id >= 0 ? q * G : 0.f) : 0.f;

@@ -351,7 +351,9 @@ int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64
  *       K chosen s if renormalize.
  * Where values are compared after arithmetic (bias, groups) the choice is that
  * of 64-bit arithmetic: it is made in 32 bits only where that cannot differ.
- * Weights are computed in 32 bits.  A NaN logit counts as -inf in the choice; it makes
+ * Weights are computed in 32 bits; renormalised ones (and their gradient) from
+ * scores relative to each other, so that they are right however small the scores
+ * are.  A sigmoid below 2^-1022 counts as zero there.  A NaN logit counts as -inf in the choice; it makes
  * its own sigmoid weight NaN (all of the token's if renormalised) and every
  * softmax weight of its token, as +inf does in a softmax.  A token whose
  * logits are all -inf (or whose chosen scores add up to zero) gets weight zero

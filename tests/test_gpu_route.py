@@ -312,3 +312,79 @@ def test_graph_replays_match_eager():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(idx, ri) and torch.equal(w, rw) and torch.equal(gz, rg)
+
+
+def shares64(z, idx, score):
+    """Renormalised scores of the chosen experts in float64, formed from their
+    logarithms, so that no score is too small; sigmoids below 2^-1022 count as zero."""
+    z = np.take_along_axis(np.asarray(z, np.float64), idx, 1)
+    log = z if score == "softmax" else np.where(z < -708.0, -np.inf, -np.logaddexp(0.0, -z))
+    top = log.max(1, keepdims=True)
+    s = np.exp(log - np.where(np.isneginf(top), 0.0, top))
+    return s / np.maximum(s.sum(1, keepdims=True), 1e-300)
+
+
+def check_shares(z, K, score, scale, bias=None, groups=1, keep=1):
+    """Weights and gradients of a renormalised router against shares64.  With logits
+    d <= 104 below the largest chosen one (further ones' shares are below 1e-45) the
+    module's bound is 2 * (104 + 2 + 22 + 2) u, and 2 * 3 u more for the sigmoid's
+    other factor: below 272 u.  1e-37: what is rounded below the normal numbers."""
+    rel = 272 * 2.0 ** -24
+    idx, w = M.moe_route(z, K, bias, score, True, groups, keep, scale)
+    z64 = z.double().cpu().numpy()
+    ref = choice64(z64, K, score, None if bias is None else bias.cpu().numpy(), groups, keep)
+    assert np.array_equal(idx.cpu().numpy(), ref)
+    q = shares64(z64, ref, score)
+    assert np.all(np.abs(w.double().cpu().numpy() - scale * q) <= rel * scale * q + 1e-37)
+    gw = torch.randn(*w.shape, generator=torch.Generator().manual_seed(5)).to(DEV)
+    G = scale * gw.double().cpu().numpy()
+    rest = 1.0 if score == "softmax" else 1.0 / (1.0 + np.exp(np.take_along_axis(z64, ref, 1)))
+    g = np.zeros(z64.shape)
+    mag = np.zeros(z64.shape)
+    np.put_along_axis(g, ref, (G - (q * G).sum(1, keepdims=True)) * q * rest, 1)
+    np.put_along_axis(mag, ref, (np.abs(G) + (q * np.abs(G)).sum(1, keepdims=True)) * q * rest, 1)
+    got = M.moe_route_bwd(z, idx, gw, score, True, scale).double().cpu().numpy()
+    half = torch.finfo(z.dtype).eps / 2 if z.dtype == BF16 else 0.0
+    assert np.all(np.abs(got - g) <= rel * mag + half * np.abs(g) * (1 + rel) + 1e-37)
+    return w
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("K", [1, 8])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 1e-3])
+@pytest.mark.parametrize("lo,hi", [(-110, -85), (-95, -80), (-700, -60), (-130, 3)])
+def test_renormalised_sigmoids_far_below_zero(dtype, K, scale, lo, hi):
+    """Scores whose sum, or its quotient with the scale, 32 bits do not hold."""
+    g = torch.Generator().manual_seed(K - lo)
+    z = torch.empty(60, 64).uniform_(lo, hi, generator=g).to(dtype).to(DEV)
+    z[0] = -88.2
+    b = torch.randn(64, generator=g).to(DEV)
+    for bias, groups, keep in ((None, 1, 1), (b, 1, 1), (b, 4, 2)):
+        w = check_shares(z, K, "sigmoid", scale, bias, groups, keep)
+        assert float((w.sum(1) - scale).abs().max()) <= 2e-5 * scale
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("K", [1, 8])
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+@pytest.mark.parametrize("depth", [60, 85, 100, 600])
+def test_softmax_with_a_bias_towards_experts_far_below_the_largest(dtype, K, scale, depth):
+    g = torch.Generator().manual_seed(depth)
+    z = torch.empty(60, 64).uniform_(-35 - depth, -depth, generator=g)
+    z[:, ::8] = torch.randn(60, 8, generator=g)
+    b = torch.rand(64, generator=g)
+    b[::8] = -3.0
+    for groups, keep in ((1, 1), (4, 2)):
+        w = check_shares(z.to(dtype).to(DEV), K, "softmax", scale, b.to(DEV), groups, keep)
+        assert float((w.sum(1) - scale).abs().max()) <= 2e-5 * scale
+
+
+def test_scores_that_count_as_zero():
+    """Sigmoids below 2^-1022, as of a mask of the type's lowest value, and -inf."""
+    z = torch.full((4, 32), -800.0)
+    z[1, 3] = -600.0
+    z[2] = torch.finfo(F32).min
+    z[3] = -math.inf
+    for bias in (None, torch.zeros(32, device=DEV)):
+        w = check_shares(z.to(DEV), 4, "sigmoid", 2.0, bias)
+        assert (w[[0, 2, 3]] == 0).all() and w[1].sum() == 2
