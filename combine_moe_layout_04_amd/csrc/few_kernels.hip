@@ -294,8 +294,9 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 // part.)
 constexpr int kDownWaves = 16;
 
-template <int DT, int NT, int NR>
-__device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups, int experts, float* y) {
+// FINITE: see Parts.  Returns whether this wave's values hold a NaN.
+template <int DT, int NT, int NR, bool FINITE>
+__device__ __forceinline__ bool few_down(const FewArgs& a, const Groups& groups, int experts, float* y) {
   // 13 tokens, 32 experts of 4096 x 2048: 274, 271, 279 us a call with 1, 2, 3; the
   // most tiles have no registers for two
   constexpr int kDepth = NT * NR < 8 ? 2 : 1;
@@ -361,6 +362,7 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
   for (int c = 0; c < NT; ++c)
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  bool nan = false;
   for (int j = wave, first = 0, round = 0; j < items;) {
     const uint16_t* this_list = list;
     const int this_n = n;
@@ -387,13 +389,9 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
           float f[8];
           unpack<kF32>(b[d][c][0], *reinterpret_cast<float(*)[4]>(f));
           unpack<kF32>(b[d][c][1], *reinterpret_cast<float(*)[4]>(f + 4));
-          const Parts act(f);
+          const Parts<FINITE> act(f);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            acc[c][r] = mma_chunk<DT>(w[d][r], act.hi, acc[c][r]);
-            acc[c][r] = mma_chunk<DT>(w[d][r], act.mid, acc[c][r]);
-            acc[c][r] = mma_chunk<DT>(w[d][r], act.lo, acc[c][r]);
-          }
+          for (int r = 0; r < NR; ++r) acc[c][r] = mma_parts(w[d][r], act, acc[c][r]);
         }
       }
       in_order();
@@ -408,8 +406,10 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
         for (int r = 0; r < NR; ++r) {
           const float v = join_parts(acc[c][r]);
           acc[c][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if ((lane_id() & 3) == 0 && pos < this_n)
+          if ((lane_id() & 3) == 0 && pos < this_n) {
             y[((size_t)part * a.pairs + this_list[pos]) * kCols + r * 4 + at.first()] = v;
+            nan |= v != v;
+          }
         }
       }
     }
@@ -417,6 +417,13 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const Groups& groups,
     first = next_first;
     round = next_round;
   }
+  return __ballot(nan) != 0;
+}
+
+template <int DT, int NT, int NR>
+__device__ __forceinline__ void down(const FewArgs& a, const Groups& groups, int experts, float* y) {
+  const bool nan = few_down<DT, NT, NR, true>(a, groups, experts, y);
+  if (DT == kBF16 && nan) few_down<DT, NT, NR, false>(a, groups, experts, y);  // a wave writes what it wrote before
 }
 
 template <int DT, int NT, int NR>
@@ -431,8 +438,8 @@ __global__ __launch_bounds__(kDownWaves* kWave) void few_down_kernel(FewArgs a) 
     here[threadIdx.x] = pair_expert(a, threadIdx.x) >= 0;
   }
   const int experts = group_pairs<1>(a, groups);
-  if (DT == kBF16 && NT > 1 && one_tile(groups, experts)) few_down<DT, 1, NR>(a, groups, experts, y);
-  else few_down<DT, NT, NR>(a, groups, experts, y);
+  if (DT == kBF16 && NT > 1 && one_tile(groups, experts)) down<DT, 1, NR>(a, groups, experts, y);
+  else down<DT, NT, NR>(a, groups, experts, y);
   const int h0 = place_of_block() * kCols;
   __syncthreads();
 

@@ -317,7 +317,7 @@ template <int DT>
 struct Factor;
 template <>
 struct Factor<kBF16> {
-  Parts p;
+  Parts<false> p;
   __device__ __forceinline__ explicit Factor(const float (&f)[8]) : p(f) {}
 };
 template <>

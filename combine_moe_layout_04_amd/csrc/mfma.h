@@ -42,6 +42,14 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
 // Eight floats as operands of three bfloat16 products: their sign and exponent
 // with 8 bits of the significand each, cut off, not rounded, so that hi + mid + lo
 // is the float itself and a product keeps all of its 24 bits.
+//
+// Beyond the finite numbers that is not so: an infinity has no remainder, and an
+// infinity in the other operand meets parts that are zero.  Either way the sum
+// becomes NaN, and never anything else that is wrong, since a float's parts have
+// one sign.  So a product is formed with FINITE parts first, and again with the
+// others where the result has a NaN: then an infinity is all in hi, and mid and lo
+// meet the other operand's finite_part.
+template <bool FINITE>
 struct Parts {
   u32x4 hi, mid, lo;
   __device__ __forceinline__ explicit Parts(const float (&f)[8]) {
@@ -52,8 +60,7 @@ struct Parts {
       for (int i = 0; i < 2; ++i) {
         v[i] = f[2 * d + i];
         r[i] = v[i] - high_half(v[i]);
-        // beyond the finite numbers the difference is not a number: no more parts
-        r[i] = r[i] - r[i] == 0.f ? r[i] : 0.f;
+        if (!FINITE && r[i] != r[i]) r[i] = 0.f;
         l[i] = r[i] - high_half(r[i]);
       }
       hi[d] = high_halves(v[0], v[1]);
@@ -68,6 +75,34 @@ struct Parts {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
   }
 };
+
+// A chunk of bfloat16 with zeros for infinities and NaN.
+__device__ __forceinline__ u32x4 finite_part(u32x4 c) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if ((c[d] & 0x00007F80u) == 0x00007F80u) c[d] &= 0xFFFF0000u;
+    if ((c[d] & 0x7F800000u) == 0x7F800000u) c[d] &= 0x0000FFFFu;
+  }
+  return c;
+}
+
+// acc += bfloat16 rows . eight floats a lane
+template <bool FINITE>
+__device__ __forceinline__ f32x4 mma_parts(const u32x4 row, const Parts<FINITE>& p, f32x4 acc) {
+  const u32x4 rest = FINITE ? row : finite_part(row);
+  acc = mma_chunk<kBF16>(row, p.hi, acc);
+  acc = mma_chunk<kBF16>(rest, p.mid, acc);
+  return mma_chunk<kBF16>(rest, p.lo, acc);
+}
+
+// Whether any lane of the wave has a NaN in these results.
+template <int N>
+__device__ __forceinline__ bool any_nan(const f32x4 (&v)[N]) {
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) nan |= __builtin_isunordered(v[i][0], v[i][1]) | __builtin_isunordered(v[i][2], v[i][3]);
+  return __ballot(nan) != 0;
+}
 
 // Rows in memory as a buffer of `bytes` from p (uniform over the wave): a load
 // whose offset is past the end gives zeros and touches no memory, so the ends

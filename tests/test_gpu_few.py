@@ -280,3 +280,25 @@ def test_every_bit_of_act_counts(dtype, T, K, E):
     w[:, 1:] = 0.0
     got = M.moe_few(x.to(dtype).to(DEV), idx.to(DEV), w.to(DEV), w13.to(dtype).to(DEV), w2.to(dtype).to(DEV))
     assert torch.equal(got.cpu().float(), want.expand(T, H))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,E,H,I", [(1, 2, 6, 64, 40), (9, 3, 12, 520, 264), (40, 2, 16, 2056, 72), (64, 4, 16, 72, 136),
+                                       (128, 2, 9, 2048, 48)])
+def test_infinities_where_they_count(dtype, T, K, E, H, I):
+    """Single infinities in chosen weights and in act come out as the formula in
+    float64 has them; everything finite stays within its bound."""
+    x, idx, w, w13, w2 = make(T, K, E, H, I, dtype, T + I)
+    e = [int(v) for v in idx.flatten()[:3]]
+    places = [(e[0], 1, 3, math.inf), (e[-1], H - 1, I - 1, -math.inf), (e[0], 5, 0, -math.inf), (e[0], 5, 1, 1.0)]
+    for a, h, i, v in places:
+        w2[a, h, i] = v
+    if E > 6:  # an infinite column of act: every output of that expert
+        w13[int(idx[T - 1, K - 1]), I + 2, 0] = math.inf
+    ref, tol = reference(x, idx, w, w13, w2, "silu")
+    got = M.moe_few(x, idx, w, w13, w2).cpu().double()
+    assert torch.isinf(ref).any()
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert bool(((got - ref).abs() <= tol)[fin].all())
