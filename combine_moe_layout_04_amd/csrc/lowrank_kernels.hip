@@ -24,6 +24,8 @@
 // the result is rounded.  (Two rounded parts, 16 bits, save little: a pass of 8192
 // rows, rank 32, 4096 columns 66.1 and 66.5 us, forward and backward of 4096 rows,
 // rank 64 97 and 101.)
+#include <type_traits>
+
 #include "device_common.h"
 #include "internal.h"
 #include "mfma.h"
@@ -312,39 +314,20 @@ __device__ __forceinline__ void across(const u32x4 (&w)[V], u32x4 (&o)[V]) {
   }
 }
 
-// The other operand: V floats along the summed index.
-template <int DT>
-struct Factor;
-template <>
-struct Factor<kBF16> {
-  Parts<false> p;
-  __device__ __forceinline__ explicit Factor(const float (&f)[8]) : p(f) {}
-};
-template <>
-struct Factor<kF32> {
-  float f[4];
-  __device__ __forceinline__ explicit Factor(const float (&g)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = g[i];
-  }
-};
-
-// acc[i] += operand i . factor over a block of the summed index.
-template <int DT, int V>
-__device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const Factor<DT>& f, f32x4 (&acc)[V]) {
+// acc[i] += operand i . the other operand, V floats along a block of the summed
+// index.  FINITE: see Parts in mfma.h.
+template <int DT, bool FINITE, int V>
+__device__ __forceinline__ void mma_across(const u32x4 (&o)[V], const float (&f)[V], f32x4 (&acc)[V]) {
   if constexpr (DT == kBF16) {
+    const Parts<FINITE> p(f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      acc[i] = mma_chunk<kBF16>(o[i], f.p.hi, acc[i]);
-      acc[i] = mma_chunk<kBF16>(o[i], f.p.mid, acc[i]);
-      acc[i] = mma_chunk<kBF16>(o[i], f.p.lo, acc[i]);
-    }
+    for (int i = 0; i < V; ++i) acc[i] = mma_parts(o[i], p, acc[i]);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(o[j][i]), f.f[j], acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(o[j][i]), f[j], acc[i], 0, 0, 0);
   }
 }
 
@@ -391,14 +374,14 @@ struct Expand {
       }
   }
 
-  // w times it; zeros past the last rank
+  // w times it; zeros past the last rank, and in a row that is not there
   static __device__ __forceinline__ void weigh(const LowrankArgs& a, const f32x4 (&u4)[BLOCKS][V / 4], float w,
-                                               float (&f)[BLOCKS][V]) {
+                                               float (&f)[BLOCKS][V], bool there = true) {
     const int q = lane_id() >> 4;
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
 #pragma unroll
-      for (int j = 0; j < V; ++j) f[k][j] = k * S::KB + q * V + j < a.r ? u4[k][j / 4][j % 4] * w : 0.f;
+      for (int j = 0; j < V; ++j) f[k][j] = there && k * S::KB + q * V + j < a.r ? u4[k][j / 4][j % 4] * w : 0.f;
   }
 
   static __device__ __forceinline__ void load_base(const LowrankArgs& a, int t, int c0, u32x4 (&base)[4]) {
@@ -409,6 +392,14 @@ struct Expand {
       base[s] = static_cast<const u32x4*>(a.base)[(size_t)max(__shfl(t, s * 4 + q, kWave), 0) * a.wch + min(c0 + col, a.wch - 1)];
   }
 
+  template <bool FINITE>
+  __device__ __forceinline__ void products(const float (&f)[BLOCKS][V], f32x4 (&acc)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k) mma_across<DT, FINITE, V>(bank[k], f[k], acc);
+  }
+
   // Rows [lo, hi) of adapter e (e >= A: none) of the tile at r0; t: the token of
   // row lane % 16.  The rows of other adapters are dropped.
   __device__ __forceinline__ void rows(const LowrankArgs& a, float* prod, int r0, int e, int lo, int hi, int t, int c0,
@@ -416,10 +407,8 @@ struct Expand {
     const int col = lane_id() & 15, q = lane_id() >> 4;
     if (e < a.A) {
       f32x4 acc[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < BLOCKS; ++k) mma_across<DT, V>(bank[k], Factor<DT>(f[k]), acc);
+      products<true>(f, acc);
+      if (DT == kBF16 && any_nan(acc)) products<false>(f, acc);
       // row `col`, chunks 4q .. 4q+3
 #pragma unroll
       for (int s = 0; s < 4; ++s)
@@ -550,7 +539,8 @@ __global__ __launch_bounds__((Both<DT, JT>::kWaves * kWave)) void lowrank_both_k
     float f[Both<DT, JT>::kBlocks][X::V];
     f32x4 u4[Both<DT, JT>::kBlocks][X::V / 4];
     X::load_u(a, keep + (lane & 15) * Shrink<JT, 1>::kKeep, u4);
-    X::weigh(a, u4, a.w ? a.w[max(t[0], 0)] : 1.f, f);
+    const int p = r0 + (lane & 15);  // only this adapter's rows have been kept
+    X::weigh(a, u4, a.w ? a.w[max(t[0], 0)] : 1.f, f, p >= lo && p < hi);
     while (c0 < a.wch) {
       x.rows(a, prod, r0, e, lo, hi, t[0], c0, f, base);
       c0 += kWaves * 16;
@@ -624,11 +614,6 @@ __global__ __launch_bounds__((W * kWave)) void wgrad_kernel(LowrankArgs a, Wgrad
     lo += blockIdx.z * share;
     hi = min(hi, lo + share);
   }
-  f32x4 acc[JT][V];
-#pragma unroll
-  for (int jt = 0; jt < JT; ++jt)
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[jt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   // lane l < KB knows the block's row l: its token, -1 without one
   auto tokens = [&](int p0) {
     const int p = p0 + lane;
@@ -651,44 +636,67 @@ __global__ __launch_bounds__((W * kWave)) void wgrad_kernel(LowrankArgs a, Wgrad
     if (weights) w = weights[max(t, 0)];
   };
   constexpr int kStep = W * S::KB;
-  int p0 = lo + wave * S::KB;
-  if (p0 < hi) {
-    t = tokens(p0);
-    fetch(p0);
-    next_t = tokens(p0 + kStep);
-  }
-  for (; p0 < hi; p0 += kStep) {
-    // this block's operands leave their registers, then the next block's rows
-    // are asked for
-    float* us = sh.u[wave];
+  f32x4 acc[JT][V];
+  // over this wave's rows; the second time, which is rare, nothing is asked for
+  // ahead (the finite parts take the registers)
+  auto sums = [&](auto pass) {
+    constexpr bool kFinite = decltype(pass)::value;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int at = i * kWave + lane;
-      *reinterpret_cast<f32x4*>(us + at / (JT * 4) * kStride + at % (JT * 4) * 4) = u[i];
+    for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[jt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int p0 = lo + wave * S::KB;
+    if (kFinite && p0 < hi) {
+      t = tokens(p0);
+      fetch(p0);
+      next_t = tokens(p0 + kStep);
     }
-    bool there[V];
-    float wk[V];
-    u32x4 o[V];
-    {
-      u32x4 z[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        there[k] = __shfl(t, q * V + k, kWave) >= 0;
-        wk[k] = weights ? __shfl(w, q * V + k, kWave) : 1.f;
-        z[k] = there[k] ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
+    for (; p0 < hi; p0 += kStep) {
+      if (!kFinite) {
+        t = tokens(p0);
+        fetch(p0);
       }
-      across<DT, V>(z, o);
-    }
-    t = next_t;
-    fetch(p0 + kStep);
-    next_t = tokens(p0 + 2 * kStep);
+      // this block's operands leave their registers, then the next block's rows
+      // are asked for
+      float* us = sh.u[wave];
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) {
-      float f[V];
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i * kWave + lane;
+        *reinterpret_cast<f32x4*>(us + at / (JT * 4) * kStride + at % (JT * 4) * 4) = u[i];
+      }
+      bool there[V];
+      float wk[V];
+      u32x4 o[V];
+      {
+        u32x4 z[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = there[k] ? us[(q * V + k) * kStride + jt * 16 + col] * wk[k] : 0.f;
-      mma_across<DT, V>(o, Factor<DT>(f), acc[jt]);
+        for (int k = 0; k < V; ++k) {
+          there[k] = __shfl(t, q * V + k, kWave) >= 0;
+          wk[k] = weights ? __shfl(w, q * V + k, kWave) : 1.f;
+          z[k] = there[k] ? x[k] : u32x4{0u, 0u, 0u, 0u};  // rows without a token
+        }
+        across<DT, V>(z, o);
+      }
+      if (kFinite) {
+        t = next_t;
+        fetch(p0 + kStep);
+        next_t = tokens(p0 + 2 * kStep);
+      }
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) {
+        float f[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = there[k] ? us[(q * V + k) * kStride + jt * 16 + col] * wk[k] : 0.f;
+        mma_across<DT, kFinite, V>(o, f, acc[jt]);
+      }
     }
+  };
+  sums(std::true_type{});
+  if constexpr (DT == kBF16) {
+    bool nan = false;
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) nan |= any_nan(acc[jt]);
+    if (nan) sums(std::false_type{});
   }
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) {

@@ -489,3 +489,34 @@ def test_every_bit_of_the_rank_space_counts(dtype, T, A, r, H, N):
             want = torch.zeros(got.shape)
             want[0, k, 0] = 2.0 ** -s
             assert torch.equal(got.cpu().float(), want), (k, s)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,A,r,H,N", [(1, 1, 8, 64, 64), (40, 3, 16, 264, 520), (200, 3, 40, 1000, 72), (1030, 2, 128, 2056, 2064),
+                                       (4100, 1, 16, 136, 264), (8300, 2, 64, 136, 136)])
+def test_infinities_where_they_count(dtype, T, A, r, H, N):
+    """Single infinities in chosen banks, in rows and in the output's gradient come
+    out as the formulas in float64 have them; everything finite stays within its
+    bound."""
+    for where in ("a", "b", "x", "g", "all"):
+        ids, E, d = make(T, A, r, H, N, dtype, T + r, none=0.0, E=A + 1)
+        last = int(ids[T - 1])
+        if where in ("b", "all"):
+            d["b"][last, 3, 5], d["b"][int(ids[0]), r - 1, N - 1] = math.inf, -math.inf
+        if where in ("a", "all"):
+            d["a"][int(ids[0]), 1, 2], d["a"][last, 2, H - 1] = -math.inf, math.inf
+        if where in ("x", "all"):
+            d["x"][T // 2, 7] = math.inf
+        if where in ("g", "all"):
+            d["g"][T // 3, N - 2] = -math.inf
+        ref = reference(ids, d)
+        h = M.moe_layout(ids, E, 1)
+        out, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+        got = M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_base=d["gbase"], grad_w=True)
+        for name, t in zip(("out", "grad_x", "grad_a", "grad_b", "grad_w"), (out, *got)):
+            v, tol = ref[name]
+            t = t.cpu().double()
+            fin, inf = torch.isfinite(v), torch.isinf(v)
+            assert torch.equal(torch.isnan(t), torch.isnan(v)), (where, name)
+            assert torch.equal(t[inf], v[inf]), (where, name)
+            assert bool(((t - v).abs() <= tol)[fin].all()), (where, name)
