@@ -520,3 +520,47 @@ def test_infinities_where_they_count(dtype, T, A, r, H, N):
             assert torch.equal(torch.isnan(t), torch.isnan(v)), (where, name)
             assert torch.equal(t[inf], v[inf]), (where, name)
             assert bool(((t - v).abs() <= tol)[fin].all()), (where, name)
+
+
+@pytest.mark.parametrize("dtype,r", [(BF16, 32), (BF16, 40), (BF16, 128), (F32, 20), (F32, 36), (F32, 128)])
+@pytest.mark.parametrize("wide", ["x", "out"])
+def test_every_form_past_two_gib(dtype, r, wide):
+    """The kernels for more wide rows than 32-bit offsets reach: both rank widths and
+    types, on either side, tiles that adapters share, tokens without one, weights and
+    grad_w.  Every element, in blocks of tokens, against float64 on the GPU."""
+    T, A = (66000 if dtype == BF16 else 33000), 3
+    H, N = (16392, 64) if wide == "x" else (64, 16392)
+    assert T * max(H, N) * torch.finfo(dtype).bits // 8 > 1 << 31
+    g = torch.Generator(device=DEV).manual_seed(r)
+    new = lambda *s: torch.empty(s, dtype=dtype, device=DEV).normal_(generator=g)  # noqa: E731
+    x, base, go = new(T, H), new(T, N), new(T, N)
+    a, b = new(A, r, H) * H ** -0.5, new(A, r, N) * r ** -0.5
+    w = torch.empty((T, 1), device=DEV).normal_(generator=g)
+    ids = torch.randint(0, A + 1, (T, 1), generator=g, device=DEV).to(torch.int32)
+    h = M.moe_layout(ids, A + 1, 1)
+    out, u = M.moe_lowrank(h, x, a, b, w, base=base)
+    gx, ga, gb, gw = M.moe_lowrank_bwd(h, go, x, a, b, u, w, grad_w=True)
+    ad, bd = a.double(), b.double()
+    ra, rb = torch.zeros_like(ad), torch.zeros_like(bd)
+    ma, mb = torch.zeros_like(ad), torch.zeros_like(bd)
+    for t0 in range(0, T, 5000):
+        t1 = min(t0 + 5000, T)
+        i, xs, gs = ids[t0:t1].view(-1), x[t0:t1].double(), go[t0:t1].double()
+        for e in range(A):
+            k = torch.nonzero(i == e).view(-1)
+            xe, ge, we = xs[k], gs[k], w[t0:t1][k].double()
+            at, bt = ad[e].t().contiguous(), bd[e].t().contiguous()
+            ue, re = xe @ at, ge @ bt
+            um, rm = xe.abs() @ at.abs(), ge.abs() @ bt.abs()
+            far_check("out", out[t0:t1][k], base[t0:t1][k].double() + we * (ue @ bd[e]), we.abs() * (um @ bd[e].abs()),
+                      H + r + 2, dtype)
+            far_check("grad_x", gx[t0:t1][k], we * (re @ ad[e]), we.abs() * (rm @ ad[e].abs()), N + r + 2, dtype)
+            far_check("grad_w", gw[t0:t1].view(-1)[k], (ue * re).sum(1), (um * rm).sum(1), H + N + r, F32)
+            ra[e] += (we * re).t().contiguous() @ xe
+            ma[e] += (we.abs() * rm).t().contiguous() @ xe.abs()
+            rb[e] += (we * ue).t().contiguous() @ ge
+            mb[e] += (we.abs() * um).t().contiguous() @ ge.abs()
+        none = i == A
+        assert torch.equal(out[t0:t1][none], base[t0:t1][none]) and (gx[t0:t1][none] == 0).all()
+    far_check("grad_a", ga, ra, ma, N + T + 2, dtype)
+    far_check("grad_b", gb, rb, mb, H + T + 2, dtype)
