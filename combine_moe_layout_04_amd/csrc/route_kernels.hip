@@ -445,13 +445,11 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
   float dot = 0.f;
   if (dense) {
     uint32_t top = 0u;
-    bool nan = false;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int e = lane + kWave * v;
       p[v] = e < a.E ? load_logit<DT>(a.z, row + e) : -INFINITY;
       if (e < a.E) top = max(top, key_of(p[v]));
-      nan |= p[v] != p[v];
     }
     float m = float_of(wave_max(top));
     if (m == -INFINITY) m = 0.f;

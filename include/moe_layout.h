@@ -353,9 +353,9 @@ int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64
  * of 64-bit arithmetic: it is made in 32 bits only where that cannot differ.
  * Weights are computed in 32 bits; renormalised ones (and their gradient) from
  * scores relative to each other, so that they are right however small the scores
- * are.  A sigmoid below 2^-1022 counts as zero there.  A NaN logit counts as -inf in the choice; it makes
- * its own sigmoid weight NaN (all of the token's if renormalised) and every
- * softmax weight of its token, as +inf does in a softmax.  A token whose
+ * are.  A sigmoid below 2^-1022 counts as zero there.  A NaN logit counts as -inf
+ * in the choice; it makes its own sigmoid weight NaN (all of the token's if
+ * renormalised) and every softmax weight of its token, as +inf does in a softmax.  A token whose
  * logits are all -inf (or whose chosen scores add up to zero) gets weight zero
  * throughout and the lowest ids that may take part.                         */
 enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
@@ -384,7 +384,9 @@ int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_
  *   softmax, renormalised: dz at idx_k = q_k (G_k - sum_m q_m G_m), q = s / sum of the chosen s
  *   sigmoid:               dz at idx_k = G_k s_k (1 - s_k)
  *   sigmoid, renormalised: dz at idx_k = (G_k - sum_m q_m G_m) q_k (1 - s_k)
- * and zero elsewhere.  float32 throughout, rounded once to dtype.  The same
+ * and zero elsewhere.  float32 throughout, rounded once to dtype.  Only the first
+ * form reads logits that were not chosen: in the others a NaN there, which makes
+ * softmax weights NaN, leaves the gradient as it is.  The same
  * options as the forward call (groups are checked, and have no other part).
  * An id that repeats within a token adds up; an id outside [0,E) has no part.
  *   logits, grad_logits [T,E] dtype; topk_idx [T,K] int32; grad_weights [T,K]

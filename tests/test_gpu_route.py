@@ -388,3 +388,28 @@ def test_scores_that_count_as_zero():
     for bias in (None, torch.zeros(32, device=DEV)):
         w = check_shares(z.to(DEV), 4, "sigmoid", 2.0, bias)
         assert (w[[0, 2, 3]] == 0).all() and w[1].sum() == 2
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_in_the_gradient(score):
+    """A NaN among the chosen logits reaches its token's gradient, every element of
+    it where the softmax is not renormalised; renormalised, the logits that were not
+    chosen have no part in it."""
+    z = draw(6, 40, F32, 3, 2.0)
+    z[:, 39] = -20.0
+    idx, _ = M.moe_route(z, 4, score=score)
+    gw = torch.randn(6, 4, generator=torch.Generator().manual_seed(2)).to(DEV)
+    clean = {r: M.moe_route_bwd(z, idx, gw, score, r) for r in (True, False)}
+    z[1, 39] = math.nan                 # not chosen
+    z[2, int(idx[2, 1])] = math.nan     # chosen
+    for r in (True, False):
+        g = M.moe_route_bwd(z, idx, gw, score, r)
+        other = [0, 3, 4, 5]
+        assert torch.equal(g[other], clean[r][other])
+        if score == "softmax" and not r:
+            assert torch.isnan(g[[1, 2]]).all()
+            continue
+        assert torch.equal(g[1], clean[r][1])
+        hit = torch.zeros(40, dtype=torch.bool, device=DEV)
+        hit[(idx[2] if r else idx[2, 1:2]).long()] = True
+        assert torch.equal(torch.isnan(g[2]), hit)
