@@ -490,8 +490,10 @@ hipError_t launch_few_tiles(const FewArgs& a, hipStream_t s) {
   // 512 x 256, bfloat16: 12.2 us so, 14.0 with all in one).
   if (a.pairs <= 2 * a.E) return launch_few_typed<DT, 1>(a, s);
   if (a.pairs <= (DT == kF32 ? 8 : 4) * a.E) return launch_few_typed<DT, 2>(a, s);
-  if (DT == kF32 || a.pairs <= 8 * a.E) return launch_few_typed<DT, 3>(a, s);
-  return launch_few_typed<DT, 4>(a, s);
+  if constexpr (DT == kBF16) {
+    if (a.pairs > 8 * a.E) return launch_few_typed<DT, 4>(a, s);
+  }
+  return launch_few_typed<DT, 3>(a, s);
 }
 
 }  // namespace
