@@ -344,7 +344,8 @@ __device__ __forceinline__ int choose_scored(const RouteArgs& a, const float (&z
       b2 = max(min(b1, o1), max(b2, o2));
       b1 = max(b1, o1);
     }
-    const R value = a.per > 1 ? b1 + b2 : b1;
+    // (a value of +inf, as a bias can give, is not to meet a -inf)
+    const R value = a.per > 1 && b1 < INFINITY ? b1 + b2 : b1;
     int better = 0;
     bool close = false;
     for (int i = 0; i < a.groups; ++i) {

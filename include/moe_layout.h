@@ -343,8 +343,8 @@ int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64
  *       a group limit the choice goes by the logits themselves);
  *   with topk_groups < num_groups: experts form num_groups groups of
  *       E/num_groups neighbours, a group's value is the sum of its two largest
- *       c (its one c if it has a single expert), and only the topk_groups
- *       groups of largest value take part;
+ *       c (its one c if it has a single expert; +inf if its largest is), and
+ *       only the topk_groups groups of largest value take part;
  *   the K largest c are chosen, in descending order; equal values (experts or
  *       groups) go to the lower index;
  *   w[t,k] = scale * s of the chosen expert, divided by the sum of the token's
@@ -354,10 +354,11 @@ int moe_combine_partitions(moe_handle_t h, const void* partial, int dtype, int64
  * Weights are computed in 32 bits; renormalised ones (and their gradient) from
  * scores relative to each other, so that they are right however small the scores
  * are.  A sigmoid below 2^-1022 counts as zero there.  A NaN logit counts as -inf
- * in the choice; it makes its own sigmoid weight NaN (all of the token's if
- * renormalised) and every softmax weight of its token, as +inf does in a softmax.  A token whose
- * logits are all -inf (or whose chosen scores add up to zero) gets weight zero
- * throughout and the lowest ids that may take part.                         */
+ * in the choice, as a c that is NaN does; it makes its own sigmoid weight NaN
+ * (all of the token's if renormalised) and every softmax weight of its token, as
+ * +inf does in a softmax.  A token whose logits are all -inf (or whose chosen
+ * scores add up to zero) gets weight zero throughout and the lowest ids that may
+ * take part.                                                                */
 enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 
 typedef struct moe_route_options {

@@ -413,3 +413,25 @@ def test_nan_in_the_gradient(score):
         hit = torch.zeros(40, dtype=torch.bool, device=DEV)
         hit[(idx[2] if r else idx[2, 1:2]).long()] = True
         assert torch.equal(torch.isnan(g[2]), hit)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases_keep_the_group_limit(score):
+    """A bias of +inf puts its expert, and so its group, in front, also where the
+    rest of the group is at -inf; one of -inf puts its expert last."""
+    z = draw(9, 16, F32, 1)
+    b = torch.zeros(16, device=DEV)
+    b[4:8] = -math.inf
+    b[5] = math.inf
+    b[15] = -math.inf
+    idx, _ = M.moe_route(z, 4, b, score, True, 4, 1)
+    assert (idx == torch.tensor([5, 4, 6, 7], dtype=torch.int32, device=DEV)).all()
+    idx, _ = M.moe_route(z, 8, b, score, True, 4, 2)  # and the best other group
+    assert (idx[:, 0] == 5).all()
+    c = scores64(z.double().cpu().numpy(), score) + np.where(np.isinf(b.cpu().numpy()), -np.inf, 0.0)
+    for t in range(9):
+        value = [-np.sort(-c[t, 4 * g:4 * g + 4])[:2].sum() for g in range(4)]
+        best = max((g for g in range(4) if g != 1), key=lambda g: value[g])
+        assert set(idx[t].tolist()) == set(range(4, 8)) | set(range(4 * best, 4 * best + 4))
+    idx, _ = M.moe_route(z, 2, b, score)
+    assert (idx[:, 0] == 5).all() and not torch.isin(idx[:, 1], torch.tensor([4, 6, 7, 15], device=DEV)).any()
