@@ -12,7 +12,7 @@ int check_route(int dtype, int64_t T, int E, int K, const moe_route_options* o) 
   if ((o->renormalize != 0 && o->renormalize != 1) || !isfinite(o->scale)) return MOE_ERR_INVALID_ARG;
   if (K < 1 || E < 1 || K > E) return MOE_ERR_SHAPE;
   if (K > MOE_MAX_K || E > MOE_MAX_E) return MOE_ERR_UNSUPPORTED;
-  if (T >= int64_t(1) << 26) return MOE_ERR_UNSUPPORTED;  // 64 lanes a token: a grid has fewer than 2^32
+  if (T > (int64_t(1) << 26) - 4) return MOE_ERR_UNSUPPORTED;  // four tokens a workgroup of 256: a grid has fewer than 2^32
   if (moe::elem_bytes(dtype) == 0) return MOE_ERR_UNSUPPORTED;
   if (o->num_groups < 1 || o->topk_groups < 1 || o->topk_groups > o->num_groups) return MOE_ERR_SHAPE;
   if (E % o->num_groups != 0 || K > o->topk_groups * (E / o->num_groups)) return MOE_ERR_SHAPE;

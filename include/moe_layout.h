@@ -373,8 +373,8 @@ typedef struct moe_route_options {
  * element's), bias [E] float32 or NULL; topk_idx [T,K] int32 and topk_weights
  * [T,K] float32 are written.  MOE_ERR_INVALID_ARG for options out of range,
  * MOE_ERR_SHAPE for K > E, groups that do not divide E or hold fewer than K
- * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above and from 2^26
- * tokens on.  T = 0 is valid.                                                */
+ * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above and for more
+ * than 2^26 - 4 tokens.  T = 0 is valid.                                                */
 int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
               const float* bias, int32_t* topk_idx, float* topk_weights, hipStream_t stream);
 

@@ -435,3 +435,18 @@ def test_infinite_biases_keep_the_group_limit(score):
         assert set(idx[t].tolist()) == set(range(4, 8)) | set(range(4 * best, 4 * best + 4))
     idx, _ = M.moe_route(z, 2, b, score)
     assert (idx[:, 0] == 5).all() and not torch.isin(idx[:, 1], torch.tensor([4, 6, 7, 15], device=DEV)).any()
+
+
+def test_the_most_tokens():
+    """One expert: nothing to choose, every weight 1; 2^26 - 4 tokens fill the largest grid."""
+    z = torch.zeros((2 ** 26 - 4, 1), dtype=BF16, device=DEV)
+    idx = torch.full((z.shape[0], 1), 7, dtype=torch.int32, device=DEV)
+    w = torch.zeros(z.shape, device=DEV)
+    M.moe_route(z, 1, topk_idx=idx, topk_weights=w)
+    assert int((idx != 0).sum()) == 0 and int((w != 1).sum()) == 0
+    g = M.moe_route_bwd(z, idx, w, renormalize=False)
+    assert int((g != 0).sum()) == 0
+    more = torch.zeros((2 ** 26 - 3, 1), dtype=BF16, device=DEV)
+    with pytest.raises(M.MoeError) as e:
+        M.moe_route(more, 1)
+    assert e.value.code == -3

@@ -61,3 +61,11 @@ def test_options_go_by_value():
     for bad in (2 ** 32 + 1, -1):
         with pytest.raises(ValueError):
             api._route_options("softmax", True, bad, 1, 1.0)
+
+
+def test_the_most_tokens(L):  # noqa: F811
+    for T, code in ((2 ** 26 - 4, "MOE_OK"), (2 ** 26 - 3, "MOE_ERR_UNSUPPORTED"), (2 ** 26 - 1, "MOE_ERR_UNSUPPORTED")):
+        # a bad pointer is refused after the sizes are
+        want = C["MOE_ERR_INVALID_ARG"] if code == "MOE_OK" else C[code]
+        assert L.moe_route(None, 0, T, 1, 1, options(), None, FAKE, FAKE, None) == want
+        assert L.moe_route_bwd(None, 0, T, 1, 1, options(), FAKE, FAKE, FAKE, None) == want
