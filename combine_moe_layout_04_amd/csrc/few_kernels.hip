@@ -7,7 +7,8 @@
 // experts' weights, 3 H I elements each, are the floor, and each is read once
 // per call.  The matrix cores take 4 weight rows against 4 of the expert's
 // tokens a tile; 1 KiB of weights costs 16 cycles of one matrix core for
-// bfloat16, about a twenty-fifth of what the bytes cost.
+// bfloat16, three times that in the second product, about a twenty-fifth and an
+// eighth of what the bytes cost.
 //
 // No layout runs before: a call has at most 512 pairs, and every workgroup
 // groups them by expert in its LDS as it starts.  A workgroup of the first
@@ -23,8 +24,8 @@
 // lose nothing.  Rounded to one bfloat16 it would make the result half as wrong
 // again (against the formula in 64 bits 2.4e-3 instead of 1.7e-3, the result's own
 // rounding); in two rounded parts it lost the last 8 bits, and cost, with two and
-// three parts, 193 and 197 us at 64 tokens of 128 experts, 19.6 and 19.8 at one
-// token, 106 and 116 at 16 pairs for each of 32 experts.
+// three parts, 193 and 198 us at 64 tokens of 128 experts, 19.6 and 19.8 at one
+// token, 106 and 113 at 16 pairs for each of 32 experts.
 #include <algorithm>
 
 #include "device_common.h"
@@ -107,7 +108,12 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
 // Whether one tile of 4 pairs does: the host goes by all pairs of a call, of which
 // many may belong to other ranks' experts (13 tokens, top 8 of 256, 32 of them here,
 // 7168 x 2048, bfloat16: the second kernel 67 us with the two tiles that the pairs
-// call for, 59 with one; float32 gains nothing, and the choice costs it 3%).
+// call for, 59 with one; float32 gains nothing, and the choice costs it 3%).  The
+// border, 9/4 pairs for an expert that has any, is the host's 2 for each there is:
+// chosen at random, 2 for each leave one in seven without.  A call with one tile
+// and with the host's, us, 2048 x 768: 64 experts of 256, 2.1 pairs 88 and 96; of 128,
+// 2.2 92 and 94, 3.2 112 and 109, 4.1 133 and 111; 2048 x 1024, 32 of 128, 2.3 64 and
+// 73, 3.1 76 and 84, 3.9 90 and 86.
 __device__ __forceinline__ bool one_tile(const Groups& g, int experts) {
   if (experts == 0) return true;
   const uint32_t last = (uint32_t)__builtin_amdgcn_readfirstlane((int)g.used[experts - 1]);
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void few_up_kernel(FewArgs a) {
 // over I); it leaves its pairs' values in y[part][pair].  The waves stream
 // their items' weights in rounds of kDepth lines, the next round's (of the same
 // item or the next) under way during this one.  (64 tokens, 126 experts of 768
-// columns, rows of 1.5 KiB, 0.4 GB: 76 us, 5.2 TB/s; 66 us with act rounded to one
+// columns, rows of 1.5 KiB, 0.4 GB: 82 us, 4.9 TB/s; 66 us with act rounded to one
 // part.)
 constexpr int kDownWaves = 16;
 

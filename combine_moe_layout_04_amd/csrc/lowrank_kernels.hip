@@ -442,8 +442,8 @@ struct Expand {
 // One wave per (a.tiles tiles of 16 receive rows, 16 chunks of columns, slot);
 // it keeps its columns of an adapter's bank in registers from tile to tile, and
 // has the next tile's rows of base and u on their way.  BLOCKS blocks of KB ranks.
-// (8192 rows of 4096 bfloat16, rank 32: 33 us, 134 MB read and written at 4.1 TB/s;
-// 34 us when u is asked for as it is needed.  What is left is the first tile's
+// (8192 rows of 4096 bfloat16, rank 32: 34 us, 134 MB read and written at 4.0 TB/s;
+// 1 us more when u is asked for as it is needed.  What is left is the first tile's
 // wait, for tokens, base, offsets and bank one after another, and a mixture of
 // reads and writes in pieces of 256 bytes.)
 constexpr int kExpandWaves = 4;
@@ -499,7 +499,7 @@ __global__ __launch_bounds__(kExpandWaves* kWave, BLOCKS <= 2 ? 2 : 1) void expa
 // the adapter's rows, where two launches would each pay for starting, reading
 // the offsets and the tokens.  It walks the wide columns with its own waves, so
 // it is for banks that one CU reads in the time of a launch.  (48 tokens of 2048
-// bfloat16, 32 adapters of rank 16: 11.0 us, 11.5 with u read back from memory; a
+// bfloat16, 32 adapters of rank 16: 11.7 us, 0.5 more with u read back from memory; a
 // wave issues 1050 instructions in 3 us and waits for loads half of the time.)
 template <int DT, int JT>
 struct Both {
