@@ -302,3 +302,20 @@ def test_infinities_where_they_count(dtype, T, K, E, H, I):
     assert torch.equal(torch.isnan(got), torch.isnan(ref))
     assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
     assert bool(((got - ref).abs() <= tol)[fin].all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_weights_past_four_gib(dtype):
+    """Experts whose weights lie past 32-bit offsets, against a call's formula on
+    those experts alone."""
+    E, H, I = 1024, 2048, (768 if dtype == BF16 else 400)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = lambda scale, *s: torch.empty(s, dtype=dtype, device=DEV).normal_(0, scale, generator=g)  # noqa: E731
+    x, w13, w2 = new(1.0, 5, H), new(H ** -0.5, E, 2 * I, H), new(I ** -0.5, E, H, I)
+    assert w13.numel() * w13.element_size() > 1 << 32
+    used = torch.tensor([0, 513, 1000, 1022, 1023], device=DEV)
+    small = torch.tensor([[4, 0], [3, 4], [2, 1], [4, 3], [0, 2]], device=DEV)
+    w = torch.rand((5, 2), generator=g, device=DEV)
+    got = M.moe_few(x, used[small], w, w13, w2)
+    ref, tol = reference(x, small, w, w13[used], w2[used], "silu")
+    assert bool(((got.cpu().double() - ref).abs() <= tol).all())

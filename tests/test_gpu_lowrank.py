@@ -564,3 +564,42 @@ def test_every_form_past_two_gib(dtype, r, wide):
         assert torch.equal(out[t0:t1][none], base[t0:t1][none]) and (gx[t0:t1][none] == 0).all()
     far_check("grad_a", ga, ra, ma, N + T + 2, dtype)
     far_check("grad_b", gb, rb, mb, H + T + 2, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ranks_of_more_rows_than_32_bits_count(dtype):
+    """u and the backward's workspace past 2^31 elements (8 GiB): every element of the
+    outputs against float64 on the GPU, in blocks of tokens."""
+    T, A, r, H, N = (1 << 24) + 999, 3, 128, 8, 16
+    g = torch.Generator(device=DEV).manual_seed(2)
+    new = lambda *s: torch.empty(s, dtype=dtype, device=DEV).normal_(generator=g)  # noqa: E731
+    x, base, go = new(T, H), new(T, N), new(T, N)
+    a, b = new(A, r, H) * H ** -0.5, new(A, r, N) * r ** -0.5
+    ids = torch.randint(0, A + 1, (T, 1), generator=g, device=DEV).to(torch.int32)
+    h = M.moe_layout(ids, A + 1, 1)
+    out, u = M.moe_lowrank(h, x, a, b, base=base)
+    assert u.numel() > 1 << 31
+    gx, ga, gb, gw = M.moe_lowrank_bwd(h, go, x, a, b, u, grad_w=True)
+    ad, bd = a.double(), b.double()
+    ra, rb = torch.zeros_like(ad), torch.zeros_like(bd)
+    ma, mb = torch.zeros_like(ad), torch.zeros_like(bd)
+    for t0 in range(0, T, 1 << 20):
+        t1 = min(t0 + (1 << 20), T)
+        i, xs, gs = ids[t0:t1].view(-1), x[t0:t1].double(), go[t0:t1].double()
+        for e in range(A):
+            k = torch.nonzero(i == e).view(-1)
+            xe, ge = xs[k], gs[k]
+            at, bt = ad[e].t().contiguous(), bd[e].t().contiguous()
+            ue, re = xe @ at, ge @ bt
+            um, rm = xe.abs() @ at.abs(), ge.abs() @ bt.abs()
+            far_check("out", out[t0:t1][k], base[t0:t1][k].double() + ue @ bd[e], um @ bd[e].abs(), H + r, dtype)
+            far_check("grad_x", gx[t0:t1][k], re @ ad[e], rm @ ad[e].abs(), N + r, dtype)
+            far_check("grad_w", gw[t0:t1].view(-1)[k], (ue * re).sum(1), (um * rm).sum(1), H + N + r, F32)
+            ra[e] += re.t().contiguous() @ xe
+            ma[e] += rm.t().contiguous() @ xe.abs()
+            rb[e] += ue.t().contiguous() @ ge
+            mb[e] += um.t().contiguous() @ ge.abs()
+        none = i == A
+        assert torch.equal(out[t0:t1][none], base[t0:t1][none]) and (gx[t0:t1][none] == 0).all()
+    far_check("grad_a", ga, ra, ma, N + T, dtype)
+    far_check("grad_b", gb, rb, mb, H + T, dtype)

@@ -450,3 +450,18 @@ def test_the_most_tokens():
     with pytest.raises(M.MoeError) as e:
         M.moe_route(more, 1)
     assert e.value.code == -3
+
+
+def test_logits_past_four_gib():
+    """2^31 logits and more: the last tokens get what they get in a call of their own."""
+    T, E, K = 2 ** 21 + 77, 1024, 2
+    z = torch.empty((T, E), dtype=BF16, device=DEV).normal_(generator=torch.Generator(device=DEV).manual_seed(1))
+    assert z.numel() > 1 << 31
+    bias = torch.rand(E, device=DEV)
+    for kw in (dict(), dict(bias=bias, score="sigmoid", num_groups=8, topk_groups=2)):
+        idx, w = M.moe_route(z, K, **kw)
+        ref = M.moe_route(z[-500:], K, **kw)
+        assert torch.equal(idx[-500:], ref[0]) and torch.equal(w[-500:], ref[1])
+    for renormalize in (True, False):
+        g = M.moe_route_bwd(z, idx, w, renormalize=renormalize)
+        assert torch.equal(g[-500:], M.moe_route_bwd(z[-500:], ref[0], ref[1], renormalize=renormalize))
