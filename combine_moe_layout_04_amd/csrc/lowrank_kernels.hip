@@ -798,7 +798,7 @@ hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s) {
     if (a.dtype == MOE_F32) hipLaunchKernelGGL((shrink_kernel<kF32, J, T, F>), grid, block, lds, s, a); \
     else hipLaunchKernelGGL((shrink_kernel<kBF16, J, T, F>), grid, block, lds, s, a);                   \
   })
-  if (far) {
+  if (far) {  // two rank widths: ranks from 33 to 64 multiply as many zeros again
     if (a.r <= 32) MOE_SHRINK(2, 1, true);
     MOE_SHRINK(8, 1, true);
   }
