@@ -22,9 +22,8 @@
 // Renormalised weights need the chosen scores only up to a factor, and are formed
 // from such, relative to the largest chosen logit where their sum is small.  So no
 // sum is too small for 32 bits, however far below zero the logits lie or below the
-// others a bias takes the choice.  Sigmoids below 2^-1022 (z <
-// -708), where 64 bits begin to lose them, count as zero: masks of the type's lowest
-// value get no weight.
+// others a bias takes the choice.  Sigmoids below 2^-1022 (z < -708), where 64 bits
+// begin to lose them, count as zero: masks of the type's lowest value get no weight.
 //
 // Logits that are NaN count as -inf in the choice and spread to the weights
 // as the formulas say.  A sum of scores that is zero (every expert masked by

@@ -374,7 +374,7 @@ typedef struct moe_route_options {
  * [T,K] float32 are written.  MOE_ERR_INVALID_ARG for options out of range,
  * MOE_ERR_SHAPE for K > E, groups that do not divide E or hold fewer than K
  * experts in all, MOE_ERR_UNSUPPORTED beyond the limits above and for more
- * than 2^26 - 4 tokens.  T = 0 is valid.                                                */
+ * than 2^26 - 4 tokens.  T = 0 is valid.                                    */
 int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
               const float* bias, int32_t* topk_idx, float* topk_weights, hipStream_t stream);
 
@@ -387,9 +387,8 @@ int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_
  *   sigmoid, renormalised: dz at idx_k = (G_k - sum_m q_m G_m) q_k (1 - s_k)
  * and zero elsewhere.  float32 throughout, rounded once to dtype.  Only the first
  * form reads logits that were not chosen: in the others a NaN there, which makes
- * softmax weights NaN, leaves the gradient as it is.  The same
- * options as the forward call (groups are checked, and have no other part).
- * An id that repeats within a token adds up; an id outside [0,E) has no part.
+ * softmax weights NaN, leaves the gradient as it is.  The same options as the
+ * forward call (groups are checked, and have no other part).  An id that repeats within a token adds up; an id outside [0,E) has no part.
  *   logits, grad_logits [T,E] dtype; topk_idx [T,K] int32; grad_weights [T,K]
  *   float32.                                                                 */
 int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,
@@ -403,8 +402,8 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
  * with Wg the first I and Wu the last I rows of w13[e], f(g) = g / (1 +
  * exp(-g)) (MOE_ACT_SILU) or the tanh form of gelu (MOE_ACT_GELU_TANH).
  * float32 sums; act stays float32, in the second product too; the sum over k
- * runs in k order from +0.0, products and sums rounded on their own.  Results are bitwise
- * reproducible.  Only the chosen experts' weights are read.
+ * runs in k order from +0.0, products and sums rounded on their own.  Results
+ * are bitwise reproducible.  Only the chosen experts' weights are read.
  *
  *   x [T,H], w13 [E,2I,H], w2 [E,H,I], out [T,H] dtype, 16-byte aligned;
  *   topk_idx [T,K] int32 or int64; topk_weights [T,K] float32, or NULL for a
