@@ -388,7 +388,8 @@ int moe_route(const void* logits, int dtype, int64_t T, int E, int K, const moe_
  * and zero elsewhere.  float32 throughout, rounded once to dtype.  Only the first
  * form reads logits that were not chosen: in the others a NaN there, which makes
  * softmax weights NaN, leaves the gradient as it is.  The same options as the
- * forward call (groups are checked, and have no other part).  An id that repeats within a token adds up; an id outside [0,E) has no part.
+ * forward call (groups are checked, and have no other part).  An id that repeats
+ * within a token adds up; an id outside [0,E) has no part.
  *   logits, grad_logits [T,E] dtype; topk_idx [T,K] int32; grad_weights [T,K]
  *   float32.                                                                 */
 int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const moe_route_options* options,

@@ -603,3 +603,16 @@ def test_ranks_of_more_rows_than_32_bits_count(dtype):
         assert torch.equal(out[t0:t1][none], base[t0:t1][none]) and (gx[t0:t1][none] == 0).all()
     far_check("grad_a", ga, ra, ma, N + T, dtype)
     far_check("grad_b", gb, rb, mb, H + T, dtype)
+
+
+def test_layouts_of_other_forms_give_the_same():
+    """Ids of 64 bits, several partitions, a layout without allocations: the adapters' rows are the same."""
+    ids, _, d = make(300, 6, 16, 136, 264, BF16, 5, E=8)
+
+    def run(h):
+        out, u = M.moe_lowrank(h, d["x"], d["a"], d["b"], d["w"], base=d["base"])
+        return (out, u) + M.moe_lowrank_bwd(h, d["g"], d["x"], d["a"], d["b"], u, d["w"], grad_w=True)
+
+    ref = run(M.moe_layout(ids, 8, 1))
+    for h in (M.moe_layout(ids.long(), 8, 1), M.moe_layout(ids, 8, 4), M.moe_layout_noalloc(ids, 8, 2)):
+        assert all(torch.equal(p, q) for p, q in zip(run(h), ref))
