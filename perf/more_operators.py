@@ -203,7 +203,7 @@ def _own_after(s, c):
                                   topk_weights=s.get("weights"), **kw)
     got = {"out": out, "n": n}
     if c["grad"]:
-        gx, gy, gw, gg, gn = M.moe_postnorm_bwd(s["grad_out"], s["grad_n"], out, s["y"], rstd, s["weight"],
+        gx, gy, gw, gg, gn = M.moe_postnorm_bwd(s["grad_out"], s["grad_n"], s["x"], s["y"], rstd, s["weight"],
                                                 next_weight=s["next"], **kw)
         got |= {"grad_x": gx, "grad_y": gy, "grad_weight": gw, "grad_gate": gg, "grad_next": gn}
     return {k: v for k, v in got.items() if v is not None}
@@ -349,8 +349,8 @@ def work(case):
     b = row * (2 + (K or 1) + c["next"]) + 8 * T * K + G * H * es + H * es * (c["post"] + c["next"])
     f = T * H * (2.0 * K + 12)
     if c["grad"]:
-        # grad_out, grad_n, out and y read, grad_x and grad_y written; the forward pass read y and wrote out, but
-        # a backward pass comes later
+        # grad_out, grad_n, x and y read, grad_x and grad_y written; the forward pass read x and y, but a backward
+        # pass comes later
         b += row * (4 + 2 * c["next"]) + 2 * G * H * es + H * es * (c["post"] + c["next"])
         f += T * H * 30.0
     return {"bytes": b, "flops": f}
