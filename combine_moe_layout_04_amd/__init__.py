@@ -31,6 +31,16 @@ from .api import (  # noqa: F401
     moe_lowrank_bwd_workspace_size,
     moe_few_workspace_size,
     FEW_MAX_PAIRS,
+    moe_balance,
+    moe_balance_bwd,
+    moe_balance_workspace_size,
+    moe_quant_rows,
+    moe_matmul_i8,
+    moe_prenorm,
+    moe_prenorm_bwd,
+    moe_postnorm,
+    moe_postnorm_bwd,
+    moe_norm_bwd_workspace_size,
 )
 from . import autograd  # noqa: F401
 

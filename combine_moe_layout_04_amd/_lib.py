@@ -12,7 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_layout.so")
 
 c_int, c_int64, c_size_t, c_void_p = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
-c_char_p = ctypes.c_char_p
+c_char_p, c_float = ctypes.c_char_p, ctypes.c_float
 
 
 class MoeTuning(ctypes.Structure):
@@ -67,6 +67,24 @@ SIGNATURES = {
     "moe_lowrank_bwd": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                 c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                 c_void_p, c_size_t, c_void_p]),
+    "moe_balance_workspace_size": (c_int, [c_int64, c_int, c_int64, ctypes.POINTER(c_size_t)]),
+    "moe_balance": (c_int, [c_void_p, c_int, c_int64, c_int, c_void_p, c_int, c_int, c_void_p, c_int64, c_void_p, c_int,
+                            c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_balance_bwd": (c_int, [c_void_p, c_int, c_int64, c_int, c_int, c_void_p, c_int64, c_void_p, c_int, c_void_p,
+                                c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_quant_rows": (c_int, [c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "moe_matmul_i8": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int, c_void_p, c_void_p, c_int, c_int,
+                              c_int64, c_int, c_void_p, c_int, c_void_p]),
+    "moe_prenorm": (c_int, [c_void_p, c_int, c_int64, c_int64, c_void_p, c_float, c_float, c_void_p, c_void_p, c_void_p,
+                            c_void_p, c_void_p]),
+    "moe_postnorm": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                             c_int64, c_float, c_void_p, c_float, c_float, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_norm_bwd_workspace_size": (c_int, [c_int, c_int64, c_int64, c_int64, ctypes.POINTER(c_size_t)]),
+    "moe_prenorm_bwd": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_float, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_postnorm_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p,
+                                 c_void_p, c_int64, c_float, c_void_p, c_float, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_handle_field": (c_int, [c_void_p, c_int, ctypes.POINTER(c_void_p), ctypes.POINTER(c_size_t)]),
     "moe_handle_dims": (c_int, [c_void_p, ctypes.POINTER(c_int64), ctypes.POINTER(c_int),
                                 ctypes.POINTER(c_int), ctypes.POINTER(c_int)]),

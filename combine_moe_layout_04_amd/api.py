@@ -696,6 +696,354 @@ def moe_lowrank_bwd(handle: Handle, grad_out: torch.Tensor, x: torch.Tensor, a: 
     return grad_x, grad_a, grad_b, grad_w
 
 
+# ---- balance loss ------------------------------------------------------------------
+
+def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_balance_workspace_size(T, E, S, ctypes.byref(n)), "moe_balance_workspace_size")
+    return n.value
+
+
+def _cached_size(f, *key) -> int:
+    """A workspace size, a pure host function of its arguments."""
+    v = _SIZES.get((f,) + key)
+    if v is None:
+        if len(_SIZES) >= _SIZES_MAX:
+            _SIZES.clear()
+        v = _SIZES[(f,) + key] = f(*key)
+    return v
+
+
+def _score(name: str) -> int:
+    if name not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {name!r}")
+    return SCORES[name]
+
+
+def _sequences(dev, T, seq_offset, token_mask) -> int:
+    """Checks the arguments that say which tokens count; the number of sequences."""
+    if token_mask is not None:
+        if token_mask.dtype != torch.bool and token_mask.dtype != torch.uint8:
+            raise TypeError(f"token_mask must be bool or uint8, got {token_mask.dtype}")
+        _need(token_mask, "token_mask", dev, (T,))
+    if seq_offset is None:
+        return 1
+    _need(seq_offset, "seq_offset", dev, dtype=torch.int32)
+    if seq_offset.dim() != 1 or seq_offset.shape[0] < 2:
+        raise ValueError("seq_offset must be [S + 1]")
+    return seq_offset.shape[0] - 1
+
+
+def moe_balance(logits: torch.Tensor, topk_idx: torch.Tensor, seq_offset: Optional[torch.Tensor] = None,
+                token_mask: Optional[torch.Tensor] = None, score: str = "softmax", loss: Optional[torch.Tensor] = None,
+                counts: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None,
+                tokens: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The router's balance and z losses, and how often each expert was chosen (see moe_layout.h).
+
+    logits [T, E]; topk_idx [T, K]; seq_offset int32 [S + 1] or None (one sequence); token_mask
+    bool [T] or None.  Returns (loss float32 [2], counts int32 [S, E], probs float32 [S, E], tokens
+    int32 [S])."""
+    dev, T, E, dt = _logits(logits)
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx must be [{T}, K]")
+    K = topk_idx.shape[1]
+    _need(topk_idx, "topk_idx", dev, (T, K))
+    S = _sequences(dev, T, seq_offset, token_mask)
+
+    def given(t, name, shape, dtype):
+        if t is None:
+            return logits.new_empty(shape, dtype=dtype)
+        _need(t, name, dev, shape, dtype)
+        return t
+
+    loss = given(loss, "loss", (2,), torch.float32)
+    counts = given(counts, "counts", (S, E), torch.int32)
+    probs = given(probs, "probs", (S, E), torch.float32)
+    tokens = given(tokens, "tokens", (S,), torch.int32)
+    if workspace is None:
+        workspace = logits.new_empty(_cached_size(moe_balance_workspace_size, T, E, S), dtype=torch.uint8)
+    else:
+        _need(workspace, "workspace", dev)
+    _run(dev, "moe_balance", logits.data_ptr(), dt, T, E, topk_idx.data_ptr(), _itype(topk_idx), K, _ptr(seq_offset), S,
+         _ptr(token_mask), _score(score), loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return loss, counts, probs, tokens
+
+
+def moe_balance_bwd(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, grad_loss: torch.Tensor, k: int,
+                    seq_offset: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                    score: str = "softmax", grad_base: Optional[torch.Tensor] = None,
+                    grad_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The logits' gradient [T, E] from grad_loss [2], for the forward's counts, tokens and k.
+
+    grad_base [T, E], the gradient through the router's weights, is added."""
+    dev, T, E, dt = _logits(logits)
+    S = _sequences(dev, T, seq_offset, token_mask)
+    _need(counts, "counts", dev, (S, E), torch.int32)
+    _need(tokens, "tokens", dev, (S,), torch.int32)
+    _need(grad_loss, "grad_loss", dev, (2,), torch.float32)
+    if grad_base is not None:
+        _need(grad_base, "grad_base", dev, (T, E), logits.dtype)
+    if grad_logits is None:
+        grad_logits = torch.empty_like(logits)
+    else:
+        _need(grad_logits, "grad_logits", dev, (T, E), logits.dtype)
+    _run(dev, "moe_balance_bwd", logits.data_ptr(), dt, T, E, k, _ptr(seq_offset), S, _ptr(token_mask), _score(score),
+         counts.data_ptr(), tokens.data_ptr(), grad_loss.data_ptr(), _ptr(grad_base), grad_logits.data_ptr())
+    return grad_logits
+
+
+# ---- products in 8-bit integers ----------------------------------------------------
+
+def moe_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+    """Rows [.., width] as 8-bit integers and a float32 scale for each row (see moe_layout.h).
+
+    Also lays out a bank of weights [E, N, width].  Returns (q int8, shaped like x, and scale,
+    shaped like x without its last dimension)."""
+    dev = _on_gpu(x, "x")
+    dt = _dtype_code(x)
+    if x.dim() < 1:
+        raise ValueError("x must be [.., width]")
+    shape, width = x.shape, x.shape[-1]
+    _need(x, "x", dev)
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8)
+    else:
+        _need(q, "q", dev, shape, torch.int8)
+    if scale is None:
+        scale = x.new_empty(shape[:-1], dtype=torch.float32)
+    else:
+        _need(scale, "scale", dev, shape[:-1], torch.float32)
+    _run(dev, "moe_quant_rows", x.data_ptr(), dt, scale.numel(), width, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def moe_matmul_i8(q: torch.Tensor, scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                  handle: Optional[Handle] = None, tokens: bool = False, activation: Optional[str] = None,
+                  first_expert: int = 0, dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products of 8-bit rows with the 8-bit weights of each row's expert (see moe_layout.h).
+
+    w int8 [E, N, width], w_scale float32 [E, N]: the weights of E of the layout's experts from
+    first_expert on.  q int8, scale float32: token rows [T, width] (tokens=True) or receive rows
+    [R, width].  Without a handle q is any [M, width] and w [N, width].  activation "silu" or
+    "gelu_tanh": out = f(gate) * up of the first and last N/2 channels.  Returns out [R or M, N or
+    N/2] in dtype; rows of other experts are not written."""
+    dev = _on_gpu(q, "q")
+    if q.dim() != 2:
+        raise ValueError("q must be [rows, width]")
+    rows, width = q.shape
+    if handle is None:
+        if w.dim() != 2:
+            raise ValueError("w must be [N, width] without a handle")
+        E, N = 1, w.shape[0]
+        _need(w, "w", dev, (N, width), torch.int8)
+        _need(w_scale, "w_scale", dev, (N,), torch.float32)
+        R, ptr = rows, None
+    else:
+        if handle.device is None:
+            raise RuntimeError("the handle has no layout yet")
+        if handle.device.index != dev.index:
+            raise ValueError(f"q must be on {handle.device}")
+        if w.dim() != 3:
+            raise ValueError("w must be [E, N, width]")
+        E, N = w.shape[0], w.shape[1]
+        _need(w, "w", dev, (E, N, width), torch.int8)
+        _need(w_scale, "w_scale", dev, (E, N), torch.float32)
+        R, ptr = handle.R, handle.ptr
+    _need(q, "q", dev, dtype=torch.int8)
+    _need(scale, "scale", dev, (rows,), torch.float32)
+    act = -1 if activation is None else _activation(activation)
+    cols = N if activation is None else N // 2
+    if out is None:
+        out = q.new_empty((R, cols), dtype=dtype)
+    else:
+        _need(out, "out", dev, (R, cols))
+    _run(dev, "moe_matmul_i8", ptr, q.data_ptr(), scale.data_ptr(), rows, width, int(bool(tokens)), w.data_ptr(),
+         w_scale.data_ptr(), E, int(first_expert), N, act, out.data_ptr(), _dtype_code(out))
+    return out
+
+
+# ---- norms before and after a block -------------------------------------------------
+
+def _norm_rows(x: torch.Tensor):
+    dev = _on_gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    _need(x, "x", dev)
+    return dev, x.shape[0], x.shape[1], _dtype_code(x)
+
+
+def moe_prenorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0, quantize: bool = False,
+                out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                rstd: Optional[torch.Tensor] = None):
+    """The norm before a block: x [T, H] over its root mean square, times weight + offset (see moe_layout.h).
+
+    Returns (n [T, H], rstd float32 [T] for the backward pass), or with quantize (q int8 [T, H],
+    scale float32 [T]) for moe_matmul_i8."""
+    dev, T, H, dt = _norm_rows(x)
+    _need(weight, "weight", dev, (H,), x.dtype)
+    if out is None:
+        out = torch.empty_like(x, dtype=torch.int8 if quantize else x.dtype)
+    else:
+        _need(out, "out", dev, (T, H), torch.int8 if quantize else x.dtype)
+    if quantize:
+        if scale is None:
+            scale = x.new_empty(T, dtype=torch.float32)
+        else:
+            _need(scale, "scale", dev, (T,), torch.float32)
+    elif scale is not None:
+        raise ValueError("scale belongs to quantize")
+    elif rstd is None:
+        rstd = x.new_empty(T, dtype=torch.float32)
+    if rstd is not None:
+        _need(rstd, "rstd", dev, (T,), torch.float32)
+    _run(dev, "moe_prenorm", x.data_ptr(), dt, T, H, weight.data_ptr(), offset, eps,
+         None if quantize else out.data_ptr(), out.data_ptr() if quantize else None, _ptr(scale), _ptr(rstd))
+    return (out, scale) if quantize else (out, rstd)
+
+
+def _around(dev, T, H, dtype, weight, gate, next_weight) -> int:
+    """Checks the weights and the gate; the number of gates."""
+    if weight is not None:
+        _need(weight, "weight", dev, (H,), dtype)
+    if next_weight is not None:
+        _need(next_weight, "next_weight", dev, (H,), dtype)
+    if gate is None:
+        return 0
+    if gate.dim() != 2 or gate.shape[0] < 1:
+        raise ValueError(f"gate must be [G, {H}]")
+    _need(gate, "gate", dev, (gate.shape[0], H), dtype)
+    return gate.shape[0]
+
+
+def moe_postnorm(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                 gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                 next_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, offset: float = 0.0,
+                 handle: Optional[Handle] = None, topk_weights: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None,
+                 rstd: Optional[torch.Tensor] = None):
+    """The end of a block: residual_scale x + gate * norm(y), and the next block's norm of it (see moe_layout.h).
+
+    x [T, H]; y [T, H], or with a handle the receive rows [R, H], combined on the way with
+    topk_weights (None: plain sum); weight [H] or None (no norm of y); gate [G, H] (G divides T) or
+    None; next_weight [H] or None.  Returns (out [T, H], n [T, H] or None, rstd float32 [T, 2])."""
+    dev, T, H, dt = _norm_rows(x)
+    gates = _around(dev, T, H, x.dtype, weight, gate, next_weight)
+    if handle is None:
+        _need(y, "y", dev, (T, H), x.dtype)
+    else:
+        if handle.device is None:
+            raise RuntimeError("the handle has no layout yet")
+        if handle.device.index != dev.index:
+            raise ValueError(f"x must be on {handle.device}")
+        _need(y, "y", dev, (handle.R, H), x.dtype)
+        if topk_weights is not None:
+            _need(topk_weights, "topk_weights", dev, (handle.T, handle.K), torch.float32)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", dev, (T, H), x.dtype)
+    if next_weight is not None:
+        if n is None:
+            n = torch.empty_like(x)
+        else:
+            _need(n, "n", dev, (T, H), x.dtype)
+    elif n is not None:
+        raise ValueError("n needs next_weight")
+    if rstd is None:
+        rstd = x.new_empty((T, 2), dtype=torch.float32)
+    else:
+        _need(rstd, "rstd", dev, (T, 2), torch.float32)
+    _run(dev, "moe_postnorm", None if handle is None else handle.ptr, x.data_ptr(), y.data_ptr(), dt, T, H,
+         _ptr(topk_weights), _ptr(weight), _ptr(gate), gates, residual_scale, _ptr(next_weight), offset, eps,
+         out.data_ptr(), _ptr(n), rstd.data_ptr())
+    return out, n, rstd
+
+
+def moe_norm_bwd_workspace_size(dtype: torch.dtype, T: int, H: int, gates: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    code = MOE_F32 if dtype == torch.float32 else MOE_BF16 if dtype == torch.bfloat16 else -1
+    _check(lib().moe_norm_bwd_workspace_size(code, T, H, gates, ctypes.byref(n)), "moe_norm_bwd_workspace_size")
+    return n.value
+
+
+def _norm_workspace(workspace, like, T, H, gates, wanted):
+    if workspace is not None:
+        _need(workspace, "workspace", like.device)
+        return workspace
+    if not wanted:
+        return None
+    return like.new_empty(_cached_size(moe_norm_bwd_workspace_size, like.dtype, T, H, gates), dtype=torch.uint8)
+
+
+def _gradient(t, name, like, dev, possible=True):
+    """None or True: allocated (where there is anything to differentiate), False: not produced, or a tensor."""
+    if t is False or (t is None and not possible):
+        return None
+    if not possible:
+        raise ValueError(f"{name} has nothing it could be the gradient of")
+    if t is None or t is True:
+        return torch.empty_like(like)
+    _need(t, name, dev, tuple(like.shape), like.dtype)
+    return t
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def moe_prenorm_bwd(grad_n: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                    offset: float = 0.0, grad_base: Optional[torch.Tensor] = None, grad_x=None, grad_weight=None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Gradients of moe_prenorm; grad_base [T, H], the gradient that reaches x past the block, is added.
+
+    grad_x, grad_weight: None or True (allocate), False (not produced) or a tensor.
+    Returns (grad_x [T, H], grad_weight [H]), None for those not produced."""
+    dev, T, H, dt = _norm_rows(x)
+    _need(grad_n, "grad_n", dev, (T, H), x.dtype)
+    _need(rstd, "rstd", dev, (T,), torch.float32)
+    _need(weight, "weight", dev, (H,), x.dtype)
+    if grad_base is not None:
+        _need(grad_base, "grad_base", dev, (T, H), x.dtype)
+    grad_x = _gradient(grad_x, "grad_x", x, dev)
+    grad_weight = _gradient(grad_weight, "grad_weight", weight, dev)
+    workspace = _norm_workspace(workspace, x, T, H, 0, grad_weight is not None)
+    _run(dev, "moe_prenorm_bwd", grad_n.data_ptr(), x.data_ptr(), dt, T, H, weight.data_ptr(), offset, rstd.data_ptr(),
+         _ptr(grad_base), _ptr(grad_x), _ptr(grad_weight), _ptr(workspace), _bytes(workspace))
+    return grad_x, grad_weight
+
+
+def moe_postnorm_bwd(grad_out: Optional[torch.Tensor], grad_n: Optional[torch.Tensor], x: torch.Tensor,
+                     y: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                     next_weight: Optional[torch.Tensor] = None, offset: float = 0.0, grad_x=None, grad_y=None,
+                     grad_weight=None, grad_gate=None, grad_next_weight=None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Gradients of moe_postnorm from those of out and n (either may be None: zero), with the
+    forward's x, y and rstd; y is the rows of tokens (after a combine where there is a layout).
+
+    grad_x, grad_y, grad_weight, grad_gate, grad_next_weight: None (allocate where the forward had
+    it), False (not produced) or a tensor.  Returns the five in this order."""
+    dev, T, H, dt = _norm_rows(x)
+    gates = _around(dev, T, H, x.dtype, weight, gate, next_weight)
+    for t, name in ((grad_out, "grad_out"), (grad_n, "grad_n"), (y, "y")):
+        if t is not None:
+            _need(t, name, dev, (T, H), x.dtype)
+    _need(rstd, "rstd", dev, (T, 2), torch.float32)
+    grad_x = _gradient(grad_x, "grad_x", x, dev)
+    grad_y = _gradient(grad_y, "grad_y", x, dev)
+    grad_weight = _gradient(grad_weight, "grad_weight", weight, dev, weight is not None)
+    grad_gate = _gradient(grad_gate, "grad_gate", gate, dev, gate is not None)
+    grad_next_weight = _gradient(grad_next_weight, "grad_next_weight", next_weight, dev, next_weight is not None)
+    sums = grad_weight is not None or grad_gate is not None or grad_next_weight is not None
+    workspace = _norm_workspace(workspace, x, T, H, gates, sums)
+    _run(dev, "moe_postnorm_bwd", _ptr(grad_out), _ptr(grad_n), x.data_ptr(), _ptr(y), dt, T, H, rstd.data_ptr(),
+         _ptr(weight), _ptr(gate), gates, residual_scale, _ptr(next_weight), offset, _ptr(grad_x), _ptr(grad_y),
+         _ptr(grad_weight), _ptr(grad_gate), _ptr(grad_next_weight), _ptr(workspace), _bytes(workspace))
+    return grad_x, grad_y, grad_weight, grad_gate, grad_next_weight
+
+
 class CuBudgetStream:
     """A HIP stream restricted to compute units [cu_first, cu_first + cu_count)
     (moe_stream_create_cu_budget), usable as a torch stream (`.stream`)."""

@@ -12,7 +12,7 @@ The C handle keeps only its latest layout.  A backward pass whose handle was
 laid out again after its forward (for example a per-layer handle reused by a
 later forward pass) raises instead of using the newer routing.
 
-The router and the adapters have a first derivative only; a second raises.  To
+The router, its balance loss, the adapters and the norms have a first derivative only; a second raises.  To
 capture a backward pass into a HIP graph, run its forward inside the capture and
 let no earlier eager graph of the same leaves live: torch accumulates into a leaf
 on the stream of the first graph that used it, which a capture must not wait for.
@@ -108,6 +108,85 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, sco
     """Differentiable router; returns (topk_idx, topk_weights).  The choice has
     no gradient, and the bias, which only moves the choice, none either."""
     return _Route.apply(logits, k, bias, score, renormalize, num_groups, topk_groups, scale)
+
+
+class _Balance(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_idx, seq_offset, token_mask, score):
+        loss, counts, probs, tokens = api.moe_balance(logits, topk_idx, seq_offset, token_mask, score)
+        ctx.save_for_backward(logits, counts, tokens, seq_offset, token_mask)
+        ctx.options = (topk_idx.shape[1], score)
+        ctx.mark_non_differentiable(counts, probs, tokens)
+        return loss, counts, probs, tokens
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss, *_):
+        logits, counts, tokens, seq_offset, token_mask = ctx.saved_tensors
+        k, score = ctx.options
+        grad = api.moe_balance_bwd(logits, counts, tokens, grad_loss.contiguous(), k, seq_offset, token_mask, score)
+        return grad, None, None, None, None
+
+
+def balance(logits: torch.Tensor, topk_idx: torch.Tensor, seq_offset: Optional[torch.Tensor] = None,
+            token_mask: Optional[torch.Tensor] = None, score: str = "softmax"):
+    """Differentiable balance and z losses of a router; returns (loss [2], counts,
+    probs, tokens), of which the loss has a gradient."""
+    return _Balance.apply(logits, topk_idx, seq_offset, token_mask, score)
+
+
+class _Prenorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, eps, offset):
+        n, rstd = api.moe_prenorm(x, weight, eps, offset)
+        ctx.save_for_backward(x, weight, rstd)
+        ctx.offset = offset
+        return n
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_n):
+        x, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        gx, gw = api.moe_prenorm_bwd(grad_n.contiguous(), x, rstd, weight, ctx.offset, grad_x=need[0], grad_weight=need[1])
+        return gx, gw, None, None
+
+
+def prenorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0) -> torch.Tensor:
+    """Differentiable norm before a block."""
+    return _Prenorm.apply(x, weight, eps, offset)
+
+
+class _Postnorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, weight, gate, next_weight, residual_scale, eps, offset):
+        out, n, rstd = api.moe_postnorm(x, y, weight, gate, residual_scale, next_weight, eps, offset)
+        ctx.save_for_backward(x, y, weight, gate, next_weight, rstd)
+        ctx.options = (residual_scale, offset)
+        ctx.set_materialize_grads(False)
+        return (out, n) if next_weight is not None else out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_n=None):
+        x, y, weight, gate, next_weight, rstd = ctx.saved_tensors
+        scale, offset = ctx.options
+        need = ctx.needs_input_grad
+        if grad_out is None and grad_n is None:
+            return (None,) * 8
+        got = api.moe_postnorm_bwd(
+            None if grad_out is None else grad_out.contiguous(), None if grad_n is None else grad_n.contiguous(),
+            x, y, rstd, weight, gate, scale, next_weight, offset, grad_x=need[0], grad_y=need[1],
+            grad_weight=need[2], grad_gate=need[3], grad_next_weight=need[4])
+        return got + (None,) * 3
+
+
+def postnorm(x: torch.Tensor, y: torch.Tensor, weight: Optional[torch.Tensor] = None,
+             gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+             next_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, offset: float = 0.0):
+    """Differentiable end of a block on rows of tokens (after autograd.combine);
+    returns out, or (out, n) with next_weight."""
+    return _Postnorm.apply(x, y, weight, gate, next_weight, residual_scale, eps, offset)
 
 
 class _Lowrank(torch.autograd.Function):

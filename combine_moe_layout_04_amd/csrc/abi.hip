@@ -686,9 +686,11 @@ const char* moe_strerror(int status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size, option or missing companion argument)";
     case MOE_ERR_SHAPE: return "invalid shape (K<1, K>E, E%P!=0, H<1, a row that is not whole 16-byte chunks, router groups that "
-                               "do not divide E or hold too few experts, or adapters without a layout of K=1 and enough experts)";
+                               "do not divide E or hold too few experts, adapters without a layout of K=1 and enough experts, "
+                               "gates that do not divide the tokens, or rows or experts that are not the layout's)";
     case MOE_ERR_UNSUPPORTED: return "unsupported (dtype/itype, P or groups>64, E>1024, K>32, T*K>=2^31, more than "
-                                     "MOE_FEW_MAX_PAIRS pairs in moe_few, rank>MOE_MAX_RANK or rows too wide)";
+                                     "MOE_FEW_MAX_PAIRS pairs in moe_few, rank>MOE_MAX_RANK, too many rows or sequences, "
+                                     "or rows or weights too large)";
     case MOE_ERR_ALIGNMENT: return "misaligned pointer (rows need 16 bytes, workspace 256)";
     case MOE_ERR_WORKSPACE: return "workspace smaller than the call needs (moe_workspace_size() and its like)";
     case MOE_ERR_HANDLE: return "bad handle, or a row call before moe_layout";

@@ -105,6 +105,47 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v;
 }
 
+// Largest value and sum over the wave, in every lane (the total arrives in lane 63).
+// All overloads stand here: one in an unnamed namespace would hide these there.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp0<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8: rows of 16 lanes
+  v = max(v, dpp0<0x112, 0xF>(v));
+  v = max(v, dpp0<0x114, 0xF>(v));
+  v = max(v, dpp0<0x118, 0xF>(v));
+  v = max(v, dpp0<0x142, 0xA>(v));  // last lane of a row to the next row
+  v = max(v, dpp0<0x143, 0xC>(v));  // lane 31 to the upper half
+  return (uint32_t)read_lane_i((int)v, 63);
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_float(float v) {
+  return __uint_as_float(dpp0<CTRL, ROWS>(__float_as_uint(v)));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_float<0x111, 0xF>(v);
+  v += dpp_float<0x112, 0xF>(v);
+  v += dpp_float<0x114, 0xF>(v);
+  v += dpp_float<0x118, 0xF>(v);
+  v += dpp_float<0x142, 0xA>(v);
+  v += dpp_float<0x143, 0xC>(v);
+  return read_lane_f(v, 63);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+  return v;
+}
+
 // Fold the 64 lane partials: for s = 32, 16, ..., 1 every lane adds the
 // partial of lane (l xor s).  float32 addition is commutative, so every lane
 // ends with the same value, the one partial 0 holds.

@@ -177,6 +177,81 @@ struct RouteBwdArgs {
   float scale;
 };
 
+// The balance loss of a router over sequences of tokens, and its gradient.
+struct BalanceArgs {
+  const void* z;          // [T, E] logits
+  const void* idx;        // [T, K] int32 or int64
+  const int* seq;         // [S+1] first token of each sequence, or null: one of all T
+  const uint8_t* mask;    // [T] 0: not counted; or null
+  float* loss;            // [2]
+  int* counts;            // [S, E]
+  float* probs;           // [S, E]
+  int* tokens;            // [S]
+  int T, E, K, S, dtype, itype, score;
+  int tile;               // tokens of a workgroup (backward: of a wave; set by the launcher)
+  float *part_p, *part_z;  // partials by slot (run + sequence): [slots, E], [slots]
+  int *part_c, *part_n;
+  unsigned* ticket;       // workgroups of the second kernel that are done
+  double *seq_sum, *seq_z;  // [S, columns], [S]
+  const float* grad_loss;   // backward: [2]
+  const void* grad_base;    // [T, E] or null
+  void* grad_z;             // [T, E]
+};
+
+// The norms before and after a block (norm_kernel), and rows to 8 bits.
+struct NormArgs {
+  const void* x;          // [T, nch] chunks: the residual stream (quant: the rows)
+  const void* y;          // [T, nch], or [R, nch] with recv_pos; null before a block
+  const void* w1;         // [nch] post-norm, or null
+  const void* gate;       // [T / group, nch] or null
+  const void* w2;         // [nch] the norm of the (next) block, or null
+  const int* recv_pos;    // [T, K] or null
+  const float* w;         // [T, K] or null (plain sum)
+  void* out;              // [T, nch]
+  void* n;                // [T, nch]
+  int8_t* q;              // [T, H] in the place of n, or null
+  float* scale;           // [T]
+  float* rstd;            // [T] before a block, [T, 2] after it; or null
+  int* status;
+  float residual, eps, offset;
+  int T, nch, K, R;
+  int group;              // tokens of a gate
+  int dtype;
+};
+
+struct NormBwdArgs {
+  const void* g;          // [T, nch] gradient of out (before a block: added to grad_x), or null
+  const void* gn;         // [T, nch] gradient of n, or null
+  const void* x;          // [T, nch]
+  const void* y;          // [T, nch]
+  const void *w1, *gate, *w2;
+  const float* rstd;
+  void *gx, *gy, *gw1, *gg, *gw2;  // each may be null
+  float *part1, *part2, *partg;    // [runs, H]; null where not wanted
+  float residual, offset;
+  int T, nch, group, gates;
+  int rows, parts, runs;  // rows of a run, runs that share a gate (1: a run holds whole gates), runs
+  int dtype;
+  bool block;             // after a block
+};
+
+void norm_bwd_plan(int64_t T, int64_t group, int* rows, int* parts, int* runs);
+
+// Grouped product of 8-bit rows and weights.
+struct I8Args {
+  const int8_t* q;        // [M, K]
+  const float* qs;        // [M]
+  const int8_t* w;        // [E, N, K]
+  const float* ws;        // [E, N]
+  const int* offset;      // [E+1] first receive row of each expert, or null: one expert, rows 0..M-1
+  const int* recv_token;  // [R] or null: row p of q belongs to receive row p
+  void* out;              // [R or M, N or N/2]
+  int M, R, E, N;
+  int kch;                // 16-byte chunks of a row of q and w
+  int act;                // MOE_ACT_* or MOE_ACT_NONE
+  int dtype;              // of out
+};
+
 // A whole expert layer for a few tokens (at most kFewMaxPairs pairs).
 constexpr int kFewMaxPairs = 512;  // MOE_FEW_MAX_PAIRS
 
@@ -259,6 +334,14 @@ hipError_t launch_reduce_partitions(const StagedArgs& a, const Tuning& t, hipStr
 hipError_t launch_combine_partitions(const StagedArgs& a, const Tuning& t, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s);
+hipError_t launch_balance(BalanceArgs a, hipStream_t s);
+hipError_t launch_balance_bwd(BalanceArgs a, hipStream_t s);
+int balance_runs(int64_t T);
+int balance_columns(int E);
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t s);
+hipError_t launch_quant(const NormArgs& a, hipStream_t s);
+hipError_t launch_i8(const I8Args& a, hipStream_t s);
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
 hipError_t launch_lowrank_shrink(const LowrankArgs& a, hipStream_t s);
 hipError_t launch_lowrank_expand(const LowrankArgs& a, hipStream_t s);

@@ -35,43 +35,6 @@
 namespace moe {
 namespace {
 
-// ---- wave-wide reductions (DPP; the total arrives in lane 63) -----------------
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp0<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8: rows of 16 lanes
-  v = max(v, dpp0<0x112, 0xF>(v));
-  v = max(v, dpp0<0x114, 0xF>(v));
-  v = max(v, dpp0<0x118, 0xF>(v));
-  v = max(v, dpp0<0x142, 0xA>(v));  // last lane of a row to the next row
-  v = max(v, dpp0<0x143, 0xC>(v));  // lane 31 to the upper half
-  return (uint32_t)read_lane_i((int)v, 63);
-}
-
-__device__ __forceinline__ uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_float(float v) {
-  return __uint_as_float(dpp0<CTRL, ROWS>(__float_as_uint(v)));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_float<0x111, 0xF>(v);
-  v += dpp_float<0x112, 0xF>(v);
-  v += dpp_float<0x114, 0xF>(v);
-  v += dpp_float<0x118, 0xF>(v);
-  v += dpp_float<0x142, 0xA>(v);
-  v += dpp_float<0x143, 0xC>(v);
-  return read_lane_f(v, 63);
-}
-
-__device__ __forceinline__ double shfl_xor_d(double v, int s) { return __shfl_xor(v, s, kWave); }
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v += shfl_xor_d(v, s);
-  return v;
-}
-
 // ---- keys: unsigned integers in the order of the numbers ----------------------
 // Every number's key is above 0, which marks "nothing to choose".
 
@@ -89,12 +52,6 @@ __device__ __forceinline__ uint64_t key_of(double f) {
   if (f != f) f = -INFINITY;
   const uint64_t b = (uint64_t)__double_as_longlong(f + 0.0);
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
-}
-
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  const uint32_t hi = wave_max((uint32_t)(v >> 32));
-  const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-  return ((uint64_t)hi << 32) | lo;
 }
 
 template <typename R>

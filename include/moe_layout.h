@@ -396,6 +396,48 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
                   const int32_t* topk_idx, const float* grad_weights, void* grad_logits,
                   hipStream_t stream);
 
+/* ---- balance loss ---------------------------------------------------------------
+ * What a router is trained by beside its weights, and how often each expert was
+ * chosen.  Tokens form S sequences: q holds tokens seq_offset[q] to
+ * seq_offset[q+1] - 1 (ascending; NULL with S = 1: one sequence of all tokens).  A
+ * token counts if it lies in a sequence and its token_mask is not 0 (NULL: all do);
+ * logits and ids of the others are not read into any result.  With s the token's
+ * softmax, or its sigmoids divided by their sum, n_q the counted tokens of q, n all
+ * of them and S' the sequences with at least one:
+ *   counts[q,e] = pairs (t,k) of q's counted tokens with topk_idx[t,k] = e
+ *   probs[q,e]  = sum of s[t,e] over them,   tokens[q] = n_q
+ *   loss[0] = 1/S' sum_q E / (K n_q^2) sum_e counts[q,e] probs[q,e]
+ *   loss[1] = 1/n sum_t lse(z_t)^2       (the z loss, of the logits for both scores)
+ * loss[0] is 1 where experts are chosen evenly.  Scores and lse in 32 bits, sums over
+ * tokens in a fixed order (bitwise reproducible), the last of them in 64.  A sequence
+ * without counted tokens has no part; with none at all both losses are 0.  Ids
+ * outside [0,E) are not counted.  A token whose scores are all zero (its logits all
+ * -inf, or for sigmoids below -708) has s = 0 and, if all are -inf, no part in
+ * loss[1]; NaN or +inf logits spread as the formulas say.
+ *   logits [T,E] dtype (any E from 1 to 1024), topk_idx [T,K] int32 or int64,
+ *   seq_offset [S+1] int32 on the device, token_mask [T] bytes; loss [2], counts
+ *   [S,E], probs [S,E], tokens [S] are written; workspace 256-byte aligned,
+ *   moe_balance_workspace_size bytes (one per call in flight).
+ * T = 0 is valid: zeros.  MOE_ERR_UNSUPPORTED for more than 2^26 - 4 tokens or
+ * MOE_MAX_SEQUENCES sequences.                                               */
+#define MOE_MAX_SEQUENCES 65535
+int moe_balance_workspace_size(int64_t T, int E, int64_t S, size_t* bytes);
+int moe_balance(const void* logits, int dtype, int64_t T, int E, const void* topk_idx, int itype, int K,
+                const int32_t* seq_offset, int64_t S, const uint8_t* token_mask, int score, float* loss,
+                int32_t* counts, float* probs, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                hipStream_t stream);
+
+/* Gradient of moe_balance: grad_logits[t,:] from grad_loss [2] (device), for the
+ * counts and tokens that the forward call wrote.  Counts have no gradient.  With
+ * a_e = grad_loss[0] E / (S' K n_q^2) counts[q,e]:
+ *   softmax: dz_j = s_j (a_j - sum_m s_m a_m),   sigmoid: the same times 1 - sigmoid(z_j),
+ * plus grad_loss[1] 2/n lse softmax(z)_j.  Tokens that do not count get zero.
+ * grad_base [T,E] dtype or NULL is added (the gradient through the router's weights,
+ * moe_route_bwd; grad_logits may be grad_base).  float32, rounded once.       */
+int moe_balance_bwd(const void* logits, int dtype, int64_t T, int E, int K, const int32_t* seq_offset, int64_t S,
+                    const uint8_t* token_mask, int score, const int32_t* counts, const int32_t* tokens,
+                    const float* grad_loss, const void* grad_base, void* grad_logits, hipStream_t stream);
+
 /* ---- expert layer for a few tokens ---------------------------------------------
  * The whole layer of a decode step, without a layout, a dispatch or a combine:
  *   act[t,k] = f(Wg_e x[t]) * (Wu_e x[t]),   e = topk_idx[t,k]
@@ -479,6 +521,95 @@ int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, 
                     const void* b, int num_adapters, int rank, int64_t N, const float* topk_weights,
                     const float* u, const void* grad_base, void* grad_x, void* grad_a, void* grad_b,
                     float* grad_w, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- products in 8-bit integers -----------------------------------------------------
+ * The experts' products for more than a few tokens, between the layout and the
+ * combine, in 8-bit integers with a scale for each row and each channel.
+ *
+ * moe_quant_rows: scale[m] = max(amax |x[m,:]| / 127, 2^-126) in float32, q[m,k] =
+ * the integer nearest to x[m,k] / scale[m], ties to even, within [-127, 127].  A row
+ * with an infinity or NaN gets that as its scale and zeros in q, so that products
+ * with it are NaN.  x [rows,width] dtype, q [rows,width] int8, 16-byte aligned;
+ * scale [rows] float32.  Weights are laid out the same way: a bank [E,N,width] is
+ * E*N rows.  MOE_ERR_SHAPE unless width is a multiple of 16, MOE_ERR_UNSUPPORTED
+ * above MOE_MAX_I8_WIDTH (where 32-bit sums could overflow) and above 2^26 rows.
+ *
+ * moe_matmul_i8: with acc the exact integer sum, for the receive rows p of the
+ * experts first_expert .. first_expert + num_experts - 1 of the layout,
+ *   y[p,n] = float(acc) * scale[r] * w_scale[e,n],   acc = sum_k q[r,k] w[e,n,k]
+ *   out[p] = round(y[p])                             (MOE_ACT_NONE: N columns)
+ *   out[p] = round(f(y[p,:N/2]) * y[p,N/2:])         (MOE_ACT_SILU, MOE_ACT_GELU_TANH)
+ * in float32.  tokens 1: q and scale hold token rows [T,width], and r is the token
+ * of p (no dispatch is needed; a row of a padded layout without a token gives
+ * zeros).  tokens 0: they hold receive rows [R,width], r = p.  Rows of other experts
+ * and past the layout's last are not written; out has R rows.  h NULL: one expert
+ * on all `rows` rows, q [rows,width], out [rows, ..] (a shared expert).
+ *   q [rows,width], w [num_experts,N,width] int8 (any values), out 16-byte aligned;
+ *   scale [rows], w_scale [num_experts,N] float32; out_dtype MOE_F32 or MOE_BF16.
+ * rows must be T or R of the layout; T = 0 is valid.  MOE_ERR_SHAPE for a width that
+ * is not a multiple of 16 or rows of out that are not whole 16-byte chunks;
+ * MOE_ERR_UNSUPPORTED above MOE_MAX_I8_WIDTH, for N above 2^20, an expert's weights
+ * of 2 GiB, token rows of nearly 4 GiB and more than 2^26 receive rows.  Results
+ * are bitwise reproducible.  Neither call has a gradient.                       */
+#define MOE_MAX_I8_WIDTH 131056
+#define MOE_ACT_NONE (-1)
+int moe_quant_rows(const void* x, int dtype, int64_t rows, int64_t width, int8_t* q, float* scale, hipStream_t stream);
+int moe_matmul_i8(moe_handle_t h, const int8_t* q, const float* scale, int64_t rows, int64_t width, int tokens,
+                  const int8_t* w, const float* w_scale, int num_experts, int first_expert, int64_t N, int activation,
+                  void* out, int out_dtype, hipStream_t stream);
+
+/* ---- norms before and after a block --------------------------------------------------
+ * With rms(v) = v / sqrt(mean(v^2) + eps) over the row and w' = w + offset (offset 1
+ * for weights stored as their distance from 1, else 0):
+ *   moe_prenorm:   n = round(rms(x) w')
+ *   moe_postnorm:  z = residual_scale x + gate * (rms(y) weight'),   out = round(z)
+ *                  n = round(rms(z) next_weight')      (the next block's norm)
+ * weight NULL: no norm after the block (y as it is); next_weight and n NULL: none of
+ * the next block.  gate [gates,H]: gate g belongs to tokens g*T/gates to
+ * (g+1)*T/gates - 1 (gates divides T; one for all, one for each sequence or one for
+ * each token); NULL with gates 0: 1.  float32, each output rounded once; n is formed
+ * from z before its rounding.  moe_prenorm leaves 8-bit rows instead where q is given
+ * (then n is NULL, H a multiple of 16): q and scale as moe_quant_rows makes them of
+ * the rows before rounding.
+ * With a handle moe_postnorm combines on the way: y holds receive rows [R,H], and
+ * sum_k [topk_weights[t,k] *] y[recv_pos[t,k]] takes their place, in float32, in k
+ * order, not rounded.  T must be the layout's.
+ *   x, y, out, n, gate, weights dtype, 16-byte aligned, rows whole 16-byte chunks of
+ *   at most MOE_MAX_NORM_BYTES; out may be x (and y without a handle), n neither;
+ *   rstd float32 or NULL: 1 / sqrt(mean + eps), [T] of x for moe_prenorm, [T,2]
+ *   (8-byte aligned) of y and z for moe_postnorm (1 where there is no norm), what the
+ *   backward passes take.  eps > 0.  T = 0 is valid.                              */
+#define MOE_MAX_NORM_BYTES 65536
+int moe_prenorm(const void* x, int dtype, int64_t T, int64_t H, const void* weight, float offset, float eps, void* n,
+                int8_t* q, float* scale, float* rstd, hipStream_t stream);
+int moe_postnorm(moe_handle_t h, const void* x, const void* y, int dtype, int64_t T, int64_t H,
+                 const float* topk_weights, const void* weight, const void* gate, int64_t gates, float residual_scale,
+                 const void* next_weight, float offset, float eps, void* out, void* n, float* rstd,
+                 hipStream_t stream);
+
+/* Backward of the norms.  With v^ = v * rstd:
+ *   moe_prenorm_bwd:   grad_x = grad_base + rstd (w' grad_n - x^ mean(w' grad_n x^)),
+ *                      grad_weight = sum_t grad_n x^   (grad_base NULL: 0)
+ *   moe_postnorm_bwd:  d = grad_out + rstd_z (next' grad_n - z^ mean(next' grad_n z^)),
+ *     grad_x = residual_scale d,   grad_next_weight = sum_t grad_n z^,   u = gate d,
+ *     grad_gate[g] = sum over its tokens of d rms(y) weight',
+ *     grad_y = rstd_y (weight' u - y^ mean(weight' u y^)),  grad_weight = sum_t u y^
+ * in float32, rounded once, z formed again from x and y; sums over tokens in a fixed
+ * order that depends on the shapes alone.  y is the rows of tokens (after moe_combine
+ * where there is a layout; its own backward pass takes grad_y).  Any output may be
+ * NULL, not all; grad_out or grad_n may be NULL (0), not both; x is read only with
+ * grad_n, y only with grad_n, a norm of it or grad_gate.  grad_x may be grad_out.  workspace (16-byte aligned, moe_norm_bwd_workspace_size bytes; one per
+ * call in flight) is not needed without a sum over tokens.  With T = 0 those sums are
+ * set to zero.                                                                   */
+int moe_norm_bwd_workspace_size(int dtype, int64_t T, int64_t H, int64_t gates, size_t* bytes);
+int moe_prenorm_bwd(const void* grad_n, const void* x, int dtype, int64_t T, int64_t H, const void* weight, float offset,
+                    const float* rstd, const void* grad_base, void* grad_x, void* grad_weight, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+int moe_postnorm_bwd(const void* grad_out, const void* grad_n, const void* x, const void* y, int dtype, int64_t T,
+                     int64_t H, const float* rstd, const void* weight, const void* gate, int64_t gates,
+                     float residual_scale, const void* next_weight, float offset, void* grad_x, void* grad_y,
+                     void* grad_weight, void* grad_gate, void* grad_next_weight, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
 
 /* Device pointer and byte size of one handle field (no synchronisation). */
 int moe_handle_field(moe_handle_t h, int field, void** dev_ptr, size_t* bytes);
