@@ -26,253 +26,439 @@
 #include "mfma.h"
 #include "quant.h"
 #include "../../include/moe_layout.h"
+#include <type_traits>
 
 namespace moe {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256;
+constexpr int kMaxExperts = 1024;           // MOE_MAX_E
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer
 
 struct Tile {
-  int e, row, rows, col;  // expert, first receive row, rows, channel tile
+  int e, row, rows, col;  // expert, first receive row, rows (0: no such tile), channel tile
 };
 
-// Finds tile `id` of a layout; false past the last one.
-__device__ __forceinline__ bool find_tile(const I8Args& a, int bm, int cols, int64_t id, int (&shared)[8], Tile& t) {
-  if (!a.offset) {
-    const int mt = (a.M + bm - 1) / bm;
-    const int64_t total = (int64_t)mt * cols, per = (total + 7) / 8;
-    const int64_t at = (id & 7) * per + (id >> 3);
-    if ((id >> 3) >= per || at >= total) return false;
-    const int m = (int)(at % mt);
-    const int step = ((a.M + mt - 1) / mt + 15) & ~15;
-    t.e = 0;
-    t.col = (int)(at / mt);
-    t.row = m * step;
-    t.rows = min(step, a.M - t.row);
-    return true;
+// The tiles of a call, numbered by expert, channel tile and row tile, the last fastest.
+struct Tiles {
+  const int* before;  // [E+1] in LDS: row tiles of the experts before each
+  const int* first;   // [E+1] in LDS: first receive row of each
+  int E, cols;
+
+  __device__ __forceinline__ uint32_t total() const { return (uint32_t)before[E] * cols; }
+
+  __device__ __forceinline__ Tile at(uint32_t id) const {  // the same in every lane
+    const int key = (int)(id / cols), block = (E + kWave - 1) / kWave;
+    // the expert whose run of row tiles holds number `key`: 64 blocks, then 16 of a block
+    int e = __popcll(__ballot(before[min(E, (lane_id() + 1) * block)] <= key)) * block;
+    e += __popcll(__ballot(lane_id() < block && before[min(E, e + lane_id() + 1)] <= key));
+    e = __builtin_amdgcn_readfirstlane(min(e, E - 1));
+    const int b = __builtin_amdgcn_readfirstlane(before[e]), tiles = __builtin_amdgcn_readfirstlane(before[e + 1]) - b;
+    const int row = __builtin_amdgcn_readfirstlane(first[e]), n = __builtin_amdgcn_readfirstlane(first[e + 1]) - row;
+    const int r = (int)(id - (uint32_t)b * cols), m = r % tiles;
+    const int step = ((n + tiles - 1) / tiles + 15) & ~15;  // rows of a tile
+    return {e, row + m * step, min(step, n - m * step), r / tiles};
   }
-  // each thread has four experts
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
-  const int e0 = 4 * (int)threadIdx.x;
-  int start[5], tiles[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    const int v = a.offset[min(e0 + i, a.E)];
-    start[i] = min(max(v, 0), a.R);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tiles[i] = (max(start[i + 1] - start[i], 0) + bm - 1) / bm;
-    sum += tiles[i];
-  }
-  const int upto = (int)wave_scan((uint32_t)sum);
-  if (lane == 63) shared[wave] = upto;
-  __syncthreads();
-  int before = upto - sum, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / kWave; ++w) {
-    if (w < wave) before += shared[w];
-    all += shared[w];
-  }
-  const int64_t total = (int64_t)all * cols, per = (total + 7) / 8;
-  const int64_t at = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || at >= total) return false;  // uniform
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t first = (int64_t)before * cols;
-    if (tiles[i] > 0 && at >= first && at < first + (int64_t)tiles[i] * cols) {
-      const int r = (int)(at - first), n = start[i + 1] - start[i];
-      const int step = ((n + tiles[i] - 1) / tiles[i] + 15) & ~15;
-      const int m = r % tiles[i];
-      shared[4] = e0 + i;
-      shared[5] = start[i] + m * step;
-      shared[6] = min(step, n - m * step);
-      shared[7] = r / tiles[i];
-    }
-    before += tiles[i];
-  }
-  __syncthreads();
-  t.e = shared[4];
-  t.row = shared[5];
-  t.rows = shared[6];
-  t.col = shared[7];
-  return true;
+};
+
+// f(g) = g sigmoid(x): x = g (silu), or 2 sqrt(2 / pi) (g + 0.044715 g^3), since
+// (1 + tanh(x / 2)) / 2 = sigmoid(x).  The fast exponential is off by (|x| + 2) u of
+// itself (u = 2^-24) and the reciprocal by 2 u, so f by (0.28 + 5) u |g|: s (1 - s) |x|
+// is at most 0.23.
+__device__ __forceinline__ float activate(float g, int act) {
+  const float x = act == MOE_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
+  return g * __builtin_amdgcn_rcpf(1.f + __expf(-x));
 }
 
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act == MOE_ACT_SILU) return g / (1.f + expf(-g));
-  return 0.5f * g * (1.f + tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g)));
-}
+// Which channel of a tile a row of the B stage holds.  A lane has the four channels
+// 4 g .. 4 g + 3 (g = lane / 16) of each 16 x 16 result; the channels are dealt so that
+// what a lane stores together is 16 contiguous bytes and what a wave stores of a row 64:
+// float32 by itself; bfloat16 takes two results, channels 8 g + 4 j + v of 32.  Gated:
+// 16 gate channels (`up` 0) and the up channels (`up` 1) of the same outputs in turn.
+template <int DT, bool GATED, int NB>
+struct Channels {
+  static constexpr bool kPaired = DT == kBF16 && NB % (GATED ? 4 : 2) == 0;
+  static __device__ __forceinline__ int of_row(int r, int& up) {
+    const int m = r % 16, g = m / 4, v = m % 4;
+    int b = r / 16;  // result
+    up = 0;
+    if (GATED) {
+      up = b & 1;
+      b >>= 1;
+    }
+    return kPaired ? b / 2 * 32 + 8 * g + 4 * (b & 1) + v : b * 16 + m;
+  }
+  // the first of the four channels of result b (of the gate and up results: pair b)
+  static __device__ __forceinline__ int of_result(int b, int g) {
+    return kPaired ? b / 2 * 32 + 8 * g + 4 * (b & 1) : b * 16 + 4 * g;
+  }
+};
 
 // MB x NB tiles of 16 x 16 a wave, WM x WN waves.
-template <int DT, bool GATED, int MB, int NB, int WM, int WN, int KC>
-__global__ __launch_bounds__(kThreads) void i8_kernel(I8Args a, int cols) {
-  static_assert(WM * WN * kWave == kThreads);
+template <int DT, bool GATED, int MB, int NB, int WM, int WN, int KC, int STAGES, int EU>
+__global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int cols) {
   constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN, kWaves = WM * WN;
-  constexpr int kRowsPer = kWave / KC;                  // rows of one load instruction
-  constexpr int kLoadsA = BM / kRowsPer / kWaves, kLoadsB = BN / kRowsPer / kWaves;
-  static_assert(kLoadsA >= 1 && kLoadsB >= 1 && BM % (kRowsPer * kWaves) == 0 && BN % (kRowsPer * kWaves) == 0);
-  __shared__ u32x4 a0[BM * KC], b0[BN * KC], a1[BM * KC], b1[BN * KC];
-  __shared__ int found[8];
+  constexpr int kRowsPer = kWave / KC;  // rows of one load instruction
+  constexpr int kLoadsA = (BM + kRowsPer * kWaves - 1) / (kRowsPer * kWaves), kLoadsB = BN / kRowsPer / kWaves;
+  static_assert(kRowsPer * kWaves % 16 == 0);
+  static_assert(kLoadsB >= 1 && BN % (kRowsPer * kWaves) == 0);
+  constexpr int kStageA = kLoadsA * kWaves * kWave, kStageB = BN * KC;
+  __shared__ u32x4 a0[kStageA], b0[kStageB], a1[kStageA], b1[kStageB], a2[STAGES > 2 ? kStageA : 1],
+      b2[STAGES > 2 ? kStageB : 1], a3[STAGES > 3 ? kStageA : 1], b3[STAGES > 3 ? kStageB : 1];
+  auto stage_a = [&](auto I) __attribute__((always_inline)) -> u32x4* {
+    if constexpr (I == 0) return a0;
+    else if constexpr (I == 1) return a1;
+    else if constexpr (I == 2) return a2;
+    else return a3;
+  };
+  auto stage_b = [&](auto I) __attribute__((always_inline)) -> u32x4* {
+    if constexpr (I == 0) return b0;
+    else if constexpr (I == 1) return b1;
+    else if constexpr (I == 2) return b2;
+    else return b3;
+  };
+  __shared__ int sums_of_waves[kWaves];
+  extern __shared__ int tables[];  // before [E+1], first [E+1]
+  int *before = tables, *first = tables + a.E + 1;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave % WM, wn = wave / WM;
   // the bits of a row that its chunks are permuted by: 16 rows over all banks
-  auto key = [](int row) { return KC >= 16 ? row & 15 : (row >> 1) & 7; };
+  auto key = [](int row) { return KC >= 16 ? row & 15 : KC == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
   const int N = GATED ? a.N / 2 : a.N;  // channels of the output
+  const int64_t width = (int64_t)a.kch * 16;
 
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {  // one tile, unless there are more than the largest grid
-    Tile t;
-    if (!find_tile(a, BM, cols, id, found, t)) return;
-    const int64_t width = (int64_t)a.kch * 16;
-    const int n0 = t.col * (GATED ? BN / 2 : BN);
-    // rows of q: the tile's own, or any
-    const int64_t qbase = a.recv_token ? 0 : (int64_t)t.row * width;
-    const int64_t qbytes = min((int64_t)0xFFFFFFE0, (a.recv_token ? (int64_t)a.M : (int64_t)t.rows) * width);
-    const auto rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q) + qbase, 0, (int)(uint32_t)qbytes, 0x00027000);
-    const int64_t wbase = ((int64_t)t.e * a.N + n0) * width;
-    const int64_t wbytes = ((int64_t)a.N - n0) * width;  // below 2 GiB
-    const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.w) + wbase, 0, (int)(uint32_t)wbytes, 0x00027000);
+  // the experts' row tiles
+  {
+    constexpr int kEach = (kMaxExperts + kWaves * kWave - 1) / (kWaves * kWave);  // experts of a thread
+    int start[kEach + 1], tiles[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= kEach; ++i) {
+      const int e = min(kEach * (int)threadIdx.x + i, a.E);
+      start[i] = a.offset ? min(max(a.offset[e], 0), a.R) : e ? a.M : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      tiles[i] = (max(start[i + 1] - start[i], 0) + BM - 1) / BM;
+      sum += tiles[i];
+    }
+    const int upto = (int)wave_scan((uint32_t)sum);
+    if (lane == 63) sums_of_waves[wave] = upto;
+    __syncthreads();
+    int b = upto - sum;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      if (w < wave) b += sums_of_waves[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = kEach * (int)threadIdx.x + i;
+      if (e <= a.E) {
+        before[e] = b;
+        first[e] = start[i];
+      }
+      b += tiles[i];
+    }
+    if (threadIdx.x == kWaves * kWave - 1 && kEach * kWaves * kWave <= a.E) {
+      before[a.E] = b;
+      first[a.E] = start[kEach];
+    }
+    __syncthreads();
+  }
+  const Tiles list = {before, first, a.E, cols};
+  // XCD x (workgroups x, x + 8, ..) takes the x-th eighth of the tiles, its workgroups in turn
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readfirstlane((int)list.total()), per = (total + 7) / 8;
+  const uint32_t from = (blockIdx.x & 7) * per, end = min(total, from + per), stride = gridDim.x / 8;
+  uint32_t id = from + blockIdx.x / 8;
+  auto tile_at = [&](uint32_t i) __attribute__((always_inline)) {
+    Tile none = {0, 0, 0, 0};
+    return i < end ? list.at(i) : none;
+  };
 
-    uint32_t offa[kLoadsA], offb[kLoadsB];
-    int chunka[kLoadsA], chunkb[kLoadsB];
-  #pragma unroll
+  const int mine = wave * kRowsPer + lane / KC;  // this lane's row of a wave's first load
+  const int chunk = lane % KC ^ key(mine);       // the same in all of them
+  const int steps = (a.kch + KC - 1) / KC;
+  Tile t = tile_at(id);
+  if (t.rows == 0) return;  // uniform over the workgroup
+
+  // tokens of the tile's rows that this lane loads (-1: none)
+  auto tokens_of = [&](const Tile& x, int(&token)[kLoadsA]) __attribute__((always_inline)) {
+#pragma unroll
     for (int i = 0; i < kLoadsA; ++i) {
-      const int r = (i * kWaves + wave) * kRowsPer + lane / KC;
-      chunka[i] = lane % KC ^ key(r);
-      offa[i] = kNowhere;
-      if (r < t.rows) {
-        int row = r;
-        if (a.recv_token) row = a.recv_token[t.row + r];
-        if (!a.recv_token || (unsigned)row < (unsigned)a.M) offa[i] = (uint32_t)(row * width) + chunka[i] * 16;
-      }
+      const int r = i * kWaves * kRowsPer + mine;
+      token[i] = -1;
+      if (r < x.rows) token[i] = a.recv_token ? a.recv_token[x.row + r] : r;
     }
-  #pragma unroll
+  };
+  uint32_t offa[kLoadsA], offb[kLoadsB];
+  __amdgpu_buffer_rsrc_t rq, rw;
+  int begin = 0;
+  auto aim = [&](const Tile& x, const int(&token)[kLoadsA]) __attribute__((always_inline)) {
+    // rows of q: the tile's own, or any
+    const int64_t qrows = a.recv_token ? a.M : x.rows;
+    const int64_t qbase = a.recv_token ? 0 : (int64_t)x.row * width;
+    rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q) + qbase, 0, (int)(uint32_t)(qrows * width), 0x00027000);
+    const int n0 = x.col * (GATED ? BN / 2 : BN);
+    const int64_t wbase = ((int64_t)x.e * a.N + n0) * width;
+    rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.w) + wbase, 0, (int)(uint32_t)((a.N - n0) * width),
+                                           0x00027000);
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i)
+      offa[i] = (uint32_t)token[i] < (uint32_t)qrows ? (uint32_t)(token[i] * width) + chunk * 16 : kNowhere;
+#pragma unroll
     for (int i = 0; i < kLoadsB; ++i) {
-      const int r = (i * kWaves + wave) * kRowsPer + lane / KC;
-      chunkb[i] = lane % KC ^ key(r);
-      // gated: 16 gate channels, then their 16 up channels
-      const int n = GATED ? r / 32 * 16 + r % 16 : r;
-      const int row = GATED && (r & 16) ? n + N : n;
-      offb[i] = n0 + n < N ? (uint32_t)(row * width) + chunkb[i] * 16 : kNowhere;
+      const int r = i * kWaves * kRowsPer + mine;
+      int up;
+      const int n = Channels<DT, GATED, NB>::of_row(r, up);
+      offb[i] = n0 + n < N ? (uint32_t)((n + (up ? N : 0)) * width) + chunk * 16 : kNowhere;
     }
-    auto load = [&](u32x4* la, u32x4* lb, int step) {
-      const int left = a.kch - step * KC;  // chunks from here on
-      const int at = step * KC * 16;
-  #pragma unroll
-      for (int i = 0; i < kLoadsA; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rq, (__attribute__((address_space(3))) void*)(la + (i * kWaves + wave) * kWave), 16,
-            (int)(left >= KC || chunka[i] < left ? offa[i] : kNowhere), at, 0, 0);
-  #pragma unroll
-      for (int i = 0; i < kLoadsB; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rw, (__attribute__((address_space(3))) void*)(lb + (i * kWaves + wave) * kWave), 16,
-            (int)(left >= KC || chunkb[i] < left ? offb[i] : kNowhere), at, 0, 0);
-    };
-    i32x4 acc[MB][NB];
-  #pragma unroll
-    for (int i = 0; i < MB; ++i)
-  #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    auto multiply = [&](const u32x4* la, const u32x4* lb) {
-      const int r = lane & 15, c = lane >> 4;
-  #pragma unroll
-      for (int k = 0; k < KC / 4; ++k) {
-        const int slot = (4 * k + c) ^ key(r);  // 16 more rows have the same key
-        i32x4 fa[MB], fb[NB];
-  #pragma unroll
-        for (int i = 0; i < MB; ++i) fa[i] = __builtin_bit_cast(i32x4, la[((i * WM + wm) * 16 + r) * KC + slot]);
-  #pragma unroll
-        for (int j = 0; j < NB; ++j) fb[j] = __builtin_bit_cast(i32x4, lb[((wn * NB + j) * 16 + r) * KC + slot]);
-  #pragma unroll
-        for (int i = 0; i < MB; ++i)
-  #pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    begin = (int)((uint32_t)(x.e * cols + x.col) % (uint32_t)steps);
+  };
+  // Load n of a step: those of q first.  Every load of a step is issued, past the rows'
+  // end too, so that their number is known.
+  auto load = [&](auto STAGE, int s, auto n) __attribute__((always_inline)) {
+    int step = s + begin;
+    if (step >= steps) step -= steps;
+    const bool in = s < steps && chunk < a.kch - step * KC;  // a step there is, not past the row's end
+    const int at = step * KC * 16;
+    if constexpr (n < kLoadsA) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rq, (__attribute__((address_space(3))) void*)(stage_a(STAGE) + (n * kWaves + wave) * kWave), 16,
+          (int)(in ? offa[n] : kNowhere), at, 0, 0);
+    } else {
+      constexpr int m = n - kLoadsA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (__attribute__((address_space(3))) void*)(stage_b(STAGE) + (m * kWaves + wave) * kWave), 16,
+          (int)(in ? offb[m] : kNowhere), at, 0, 0);
+    }
+  };
+  // loads FROM to TO - 1 of a step
+  auto loads = [&](auto STAGE, int s, auto FROM, auto TO) __attribute__((always_inline)) {
+    auto each = [&](auto self, auto n) __attribute__((always_inline)) {
+      if constexpr (n < TO) {
+        load(STAGE, s, n);
+        self(self, std::integral_constant<int, n + 1>{});
       }
     };
-    const int steps = (a.kch + KC - 1) / KC;
-    load(a0, b0, 0);
-    for (int s = 0; s < steps; s += 2) {
-      __syncthreads();  // stage 0 has landed, stage 1 has been read
-      if (s + 1 < steps) load(a1, b1, s + 1);
-      multiply(a0, b0);
-      __syncthreads();
-      if (s + 1 >= steps) break;
-      if (s + 2 < steps) load(a0, b0, s + 2);
-      multiply(a1, b1);
+    each(each, FROM);
+  };
+  constexpr std::integral_constant<int, 0> s0;
+  constexpr std::integral_constant<int, 1> s1;
+  constexpr std::integral_constant<int, 2> s2;
+  constexpr std::integral_constant<int, 3> s3;
+  constexpr std::integral_constant<int, kLoadsA + kLoadsB> every;
+  auto start = [&]() __attribute__((always_inline)) {  // the steps before the first
+    loads(s0, 0, s0, every);
+    if constexpr (STAGES > 2) loads(s1, 1, s0, every);
+    if constexpr (STAGES > 3) loads(s2, 2, s0, every);
+  };
+  i32x4 acc[MB][NB];
+  // the sums, of the first B row tiles of each wave
+  auto sums = [&](auto B) __attribute__((always_inline)) {
+    // step s in stage I: wait for its loads, let the stage before it be filled again, multiply
+    auto work = [&](auto I, int s) __attribute__((always_inline)) {
+      constexpr int kFlying = (STAGES - 2) * (kLoadsA + kLoadsB);  // loads that may still be on their way
+      __asm__ __volatile__("" ::: "memory");  // the barrier alone does not keep LDS reads on their side of it
+      __builtin_amdgcn_s_waitcnt((kFlying & 15) | (7 << 4) | ((kFlying >> 4) << 14));  // and no LDS read
+      __builtin_amdgcn_s_barrier();
+      __asm__ __volatile__("" ::: "memory");
+      constexpr std::integral_constant<int, (I + STAGES - 1) % STAGES> before_it;
+      const u32x4 *la = stage_a(I), *lb = stage_b(I);
+      const int r = lane & 15, c = lane >> 4;
+      constexpr int kParts = KC / 4;
+      i32x4 fa[kParts][B], fb[kParts][NB];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const int slot = (4 * k + c) ^ key(r);  // 16 more rows have the same key
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[k][j] = __builtin_bit_cast(i32x4, lb[((wn * NB + j) * 16 + r) * KC + slot]);
+#pragma unroll
+        for (int i = 0; i < B; ++i) fa[k][i] = __builtin_bit_cast(i32x4, la[((i * WM + wm) * 16 + r) * KC + slot]);
+      }
+      // a load takes the address unit as long as a product the matrix unit: one by one between them
+      constexpr int kGroups = kParts * B;
+      auto group = [&](auto self, auto g) __attribute__((always_inline)) {
+        if constexpr (g < kGroups) {
+          constexpr int k = g / B, i = g % B;
+          loads(before_it, s + STAGES - 1, std::integral_constant<int, g * every / kGroups>{},
+                std::integral_constant<int, (g + 1) * every / kGroups>{});
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[k][j], fa[k][i], acc[i][j], 0, 0, 0);
+          in_order();
+          self(self, std::integral_constant<int, g + 1>{});
+        }
+      };
+      group(group, s0);
+    };
+    int s = 0;
+    for (; s + STAGES <= steps; s += STAGES) {
+      work(s0, s);
+      work(s1, s + 1);
+      if constexpr (STAGES > 2) work(s2, s + 2);
+      if constexpr (STAGES > 3) work(s3, s + 3);
     }
+    if (s < steps) work(s0, s);
+    if constexpr (STAGES > 2)
+      if (s + 1 < steps) work(s1, s + 1);
+    if constexpr (STAGES > 3)
+      if (s + 2 < steps) work(s2, s + 2);
+  };
 
-    // lane: row l % 16 of a row tile, channels 4 (l / 16) + 0..3 of a channel tile
-    const int quad = 4 * (lane >> 4);
-    float sw[NB][4];
-  #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int b = wn * NB + j;
-      const int n = n0 + (GATED ? b / 2 * 16 : b * 16) + quad;
-      const float* p = a.ws + (int64_t)t.e * a.N + (GATED && (b & 1) ? N : 0) + n;
-  #pragma unroll
-      for (int v = 0; v < 4; ++v) sw[j][v] = n < N ? p[v] : 0.f;
+  // lane: row l % 16 of a row tile
+  using Ch = Channels<DT, GATED, NB>;
+  constexpr int kOuts = GATED ? NB / 2 : NB;  // results of a wave in a row tile
+  const int g = lane >> 4;
+  float sw[NB][4], sq[MB];
+  auto scales_of = [&](const Tile& x) __attribute__((always_inline)) {
+    const int n0 = x.col * (GATED ? BN / 2 : BN);
+#pragma unroll
+    for (int j = 0; j < kOuts; ++j) {
+      const int n = n0 + Ch::of_result(wn * kOuts + j, g);
+      const float* p = a.ws + (int64_t)x.e * a.N + n;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (GATED) {
+          sw[2 * j][v] = n < N ? p[v] : 0.f;
+          sw[2 * j + 1][v] = n < N ? p[N + v] : 0.f;
+        } else {
+          sw[j][v] = n < N ? p[v] : 0.f;
+        }
+      }
     }
-  #pragma unroll
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int r = (i * WM + wm) * 16 + (lane & 15);
+      int source = x.row + r;
+      if (r < x.rows && a.recv_token) source = a.recv_token[source];
+      sq[i] = r < x.rows && (unsigned)source < (unsigned)a.M ? a.qs[source] : 0.f;
+    }
+  };
+  int token[kLoadsA];
+  tokens_of(t, token);
+  aim(t, token);
+  start();
+  scales_of(t);
+  for (;;) {
+    id += stride;
+    const Tile next = tile_at(id);
+    tokens_of(next, token);  // they arrive while this tile is worked on
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int tiles = (t.rows + 16 * WM - 1) / (16 * WM);
+    if constexpr (MB == 1) {
+      sums(std::integral_constant<int, 1>{});
+    } else if constexpr (MB == 2) {
+      if (tiles == 1) sums(std::integral_constant<int, 1>{});
+      else sums(std::integral_constant<int, 2>{});
+    } else if constexpr (MB == 4) {
+      if (tiles == 1) sums(std::integral_constant<int, 1>{});
+      else if (tiles == 2) sums(std::integral_constant<int, 2>{});
+      else if (tiles == 3) sums(std::integral_constant<int, 3>{});
+      else sums(std::integral_constant<int, 4>{});
+    } else {
+      if (tiles <= 2) sums(std::integral_constant<int, 2>{});
+      else if (tiles <= 4) sums(std::integral_constant<int, 4>{});
+      else if (tiles == 5) sums(std::integral_constant<int, 5>{});
+      else if (tiles == 6) sums(std::integral_constant<int, 6>{});
+      else if (tiles == 7) sums(std::integral_constant<int, 7>{});
+      else if (tiles == 8 && MB > 8) sums(std::integral_constant<int, 8>{});
+      else sums(std::integral_constant<int, MB>{});
+    }
+    if (next.rows != 0) {  // its first loads run while this tile is written
+      __asm__ __volatile__("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(7 << 4);  // nothing on its way to a stage, or from one
+      __builtin_amdgcn_s_barrier();
+      __asm__ __volatile__("" ::: "memory");
+      aim(next, token);
+      start();
+    }
+    const int n0 = t.col * (GATED ? BN / 2 : BN);
+#pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int r = (i * WM + wm) * 16 + (lane & 15);
       if (r >= t.rows) continue;
       const int64_t p = (int64_t)t.row + r;
-      int64_t source = p;
-      if (a.recv_token) source = a.recv_token[p];
-      const float s = source >= 0 && source < a.M ? a.qs[source] : 0.f;
-      constexpr int kStep = GATED ? 2 : 1;
-  #pragma unroll
-      for (int j = 0; j < NB; j += kStep) {
-        const int n = n0 + (wn * NB + j) / kStep * 16 + quad;
-        float y[4];
-  #pragma unroll
+      float y[kOuts][4];
+#pragma unroll
+      for (int j = 0; j < kOuts; ++j)
+#pragma unroll
         for (int v = 0; v < 4; ++v) {
-          y[v] = (float)acc[i][j][v] * s * sw[j][v];
-          if constexpr (GATED) y[v] = activate(y[v], a.act) * ((float)acc[i][j + 1][v] * s * sw[j + 1][v]);
+          if constexpr (GATED)
+            y[j][v] = activate((float)acc[i][2 * j][v] * sq[i] * sw[2 * j][v], a.act) *
+                      ((float)acc[i][2 * j + 1][v] * sq[i] * sw[2 * j + 1][v]);
+          else
+            y[j][v] = (float)acc[i][j][v] * sq[i] * sw[j][v];
         }
-        if (n >= N) continue;
-        if constexpr (DT == kF32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + p * N + n) = make_float4(y[0], y[1], y[2], y[3]);
+      if constexpr (DT == kF32) {
+        float* out = static_cast<float*>(a.out) + p * N;
+#pragma unroll
+        for (int j = 0; j < kOuts; ++j) {
+          const int n = n0 + Ch::of_result(wn * kOuts + j, g);
+          if (n < N) *reinterpret_cast<float4*>(out + n) = make_float4(y[j][0], y[j][1], y[j][2], y[j][3]);
+        }
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + p * N;
+        if constexpr (Ch::kPaired) {
+#pragma unroll
+          for (int j = 0; j < kOuts; j += 2) {  // N is whole 16-byte chunks: all 8 channels there, or none
+            const int n = n0 + Ch::of_result(wn * kOuts + j, g);
+            if (n < N)
+              *reinterpret_cast<u32x4*>(out + n) = u32x4{round_bf16x2(y[j][0], y[j][1]), round_bf16x2(y[j][2], y[j][3]),
+                                                         round_bf16x2(y[j + 1][0], y[j + 1][1]),
+                                                         round_bf16x2(y[j + 1][2], y[j + 1][3])};
+          }
         } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + p * N + n) =
-              make_uint2(round_bf16x2(y[0], y[1]), round_bf16x2(y[2], y[3]));
+#pragma unroll
+          for (int j = 0; j < kOuts; ++j) {
+            const int n = n0 + Ch::of_result(wn * kOuts + j, g);
+            if (n < N)
+              *reinterpret_cast<uint2*>(out + n) = make_uint2(round_bf16x2(y[j][0], y[j][1]), round_bf16x2(y[j][2], y[j][3]));
+          }
         }
       }
     }
-    __syncthreads();  // the stages and `found` are free again
+    if (next.rows == 0) return;
+    t = next;
+    scales_of(t);
   }
 }
 
-template <int MB, int NB, int WM, int WN, int KC>
+// Tiles of rows there can be at most (whole ones, and one of each expert that is not
+// whole) times tiles of channels: the host does not know the experts' rows.
+int64_t most_tiles(const I8Args& a, int bm, int bn) {
+  const int64_t rows = a.offset ? a.R : a.M, partial = a.offset ? (rows < a.E ? rows : a.E) : 1;
+  return (rows / bm + partial) * ((a.N + bn - 1) / bn);
+}
+
+template <int MB, int NB, int WM, int WN, int KC, int STAGES, int EU>
 hipError_t launch_tile(const I8Args& a, hipStream_t s) {
   constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN;
   const bool gated = a.act != MOE_ACT_NONE;
-  const int bn = gated ? BN / 2 : BN, N = gated ? a.N / 2 : a.N;
-  const int cols = (N + bn - 1) / bn;
-  // tiles of rows there can be at most: whole ones, and one of each expert that is not whole
-  const int64_t rows = a.offset ? a.R : a.M, partial = a.offset ? (rows < a.E ? rows : a.E) : 1;
-  int64_t grid = ((rows / BM + partial) * cols + 7) / 8 * 8;
-  if (grid > (1 << 22)) grid = 1 << 22;
+  const int cols = (a.N + BN - 1) / BN;  // gated: BN / 2 of N / 2 outputs each
+  const int64_t most = (most_tiles(a, BM, BN) + 7) / 8 * 8, fit = 256 * (4 * EU / (WM * WN));  // what the GPU holds at once
+  const unsigned grid = (unsigned)(most < fit ? most : fit);
+  const uint32_t lds = 2 * (a.E + 1) * sizeof(int);
   if (a.dtype == kF32) {
-    if (gated) i8_kernel<kF32, true, MB, NB, WM, WN, KC><<<(unsigned)grid, kThreads, 0, s>>>(a, cols);
-    else i8_kernel<kF32, false, MB, NB, WM, WN, KC><<<(unsigned)grid, kThreads, 0, s>>>(a, cols);
+    if (gated) i8_kernel<kF32, true, MB, NB, WM, WN, KC, STAGES, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    else i8_kernel<kF32, false, MB, NB, WM, WN, KC, STAGES, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
   } else {
-    if (gated) i8_kernel<kBF16, true, MB, NB, WM, WN, KC><<<(unsigned)grid, kThreads, 0, s>>>(a, cols);
-    else i8_kernel<kBF16, false, MB, NB, WM, WN, KC><<<(unsigned)grid, kThreads, 0, s>>>(a, cols);
+    if (gated) i8_kernel<kBF16, true, MB, NB, WM, WN, KC, STAGES, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    else i8_kernel<kBF16, false, MB, NB, WM, WN, KC, STAGES, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Tiles of 128 x 256, one workgroup a CU, where there are enough of them (rows of 2 KiB
+// and wider hide a tile's beginning and end better, so fewer will do); else of 64 x 128,
+// two workgroups a CU; else of 64 x 64.
 hipError_t launch_i8(const I8Args& a, hipStream_t s) {
-  const int64_t rows = a.offset ? a.R : a.M, per = (rows + a.E - 1) / a.E;  // of an expert, on average
-  if (per <= 16) return launch_tile<1, 2, 1, 4, 16>(a, s);
-  return launch_tile<4, 4, 2, 2, 8>(a, s);
+  if (most_tiles(a, 128, 256) >= (a.kch >= 128 ? 192 : 400)) return launch_tile<4, 4, 2, 4, 8, 3, 2>(a, s);
+  if (most_tiles(a, 64, 128) >= 256) return launch_tile<2, 4, 2, 2, 8, 3, 2>(a, s);
+  return launch_tile<1, 2, 4, 2, 8, 3, 4>(a, s);
 }
 
 }  // namespace moe
