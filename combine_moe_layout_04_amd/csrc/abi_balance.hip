@@ -25,7 +25,6 @@ size_t place(moe::BalanceArgs* a, char* ws, int64_t T, int E, int64_t S) {
     at += up256(bytes);
     return p;
   };
-  char* ticket = take(sizeof(unsigned));
   char* seq_sum = take((size_t)S * moe::balance_columns(E) * sizeof(double));
   char* seq_z = take((size_t)S * sizeof(double));
   char* part_z = take(slots * sizeof(float));
@@ -33,7 +32,6 @@ size_t place(moe::BalanceArgs* a, char* ws, int64_t T, int E, int64_t S) {
   char* part_p = take(slots * E * sizeof(float));
   char* part_c = take(slots * E * sizeof(int));
   if (a) {
-    a->ticket = reinterpret_cast<unsigned*>(ticket);
     a->seq_sum = reinterpret_cast<double*>(seq_sum);
     a->seq_z = reinterpret_cast<double*>(seq_z);
     a->part_z = reinterpret_cast<float*>(part_z);

@@ -16,8 +16,10 @@
 // meeting to the next w or q grows, so no two share a slot and W + S slots are
 // enough, without knowing on the host how long the sequences are.  The second
 // kernel adds a sequence's slots in the order of the runs, so results do not
-// depend on timing; whole numbers are counted with LDS atomics.  Its last
-// workgroup to finish forms the losses.
+// depend on timing (whole numbers are counted with LDS atomics), and a third the
+// sequences' losses; where there is one sequence of few partials the second does
+// that too.  (The last workgroup of the second kernel forming them, by a counter,
+// took 18 us against 4: its fences write back and drop the L2s.)
 //
 // Sigmoid scores are formed relative to the largest one where all lie below
 // 0.5: their share of the sum is right however small they are.  As in the router
@@ -30,9 +32,13 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;          // of a workgroup of the first kernel and of the backward
-constexpr int kCols = 32;          // experts of a workgroup of the second kernel
-constexpr int kGroups = 32;        // slots it adds at once
+constexpr int kWaves = 4;     // of a workgroup of the backward
+constexpr int kRuns = 256;    // workgroups of the first kernel: one a CU
+constexpr int kCols = 32;     // experts of a workgroup of the second kernel, if there is more than one
+constexpr int kDirect = 1 << 15;  // values of a kind that one workgroup adds by itself
+
+// Waves of a workgroup of the first kernel: its sums of all of them lie in LDS.
+constexpr int run_waves(int vpl) { return vpl <= 4 ? 16 : 4; }
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* z, size_t i) {
@@ -63,25 +69,21 @@ __device__ __forceinline__ int sequences_before(const BalanceArgs& a, int t) {
   return lo;
 }
 
-__device__ __forceinline__ float wave_maxf(float v) {  // a NaN among others is passed over
-  v = fmaxf(v, __shfl_xor(v, 32, kWave));
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, kWave));
-  return v;
-}
-
-// One token's softmax, its lse, and its scores (p is soft itself for softmax).
+// One token's softmax, its lse, its scores (p is soft itself for softmax) and, for
+// sigmoids, 1 - sigmoid in rest.  The fast exponential is off by (|x| + 2) u of itself
+// (u = 2^-24), which the terms of far smaller logits alone have much of.
 template <int VPL, bool SIG>
-__device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL], float (&p)[VPL], float& lse) {
+__device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL], float (&p)[VPL], float (&rest)[VPL],
+                                       float& lse) {
   float m = z[0];
 #pragma unroll
   for (int v = 1; v < VPL; ++v) m = fmaxf(m, z[v]);
-  m = wave_maxf(m);
+  m = wave_max(m);
   if (m == -INFINITY) m = 0.f;
   float sum = 0.f;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    soft[v] = expf(z[v] - m);
+    soft[v] = __expf(z[v] - m);
     sum += soft[v];
   }
   sum = wave_sum(sum);
@@ -91,10 +93,12 @@ __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL]
     float all = 0.f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      // m > 0: the sigmoid itself; else relative to the largest logit
-      const float top = m > 0.f ? expf(-fabsf(z[v])) : soft[v];
-      const float bottom = m > 0.f ? top : expf(z[v]);
-      p[v] = z[v] < -708.f ? 0.f : (m > 0.f && z[v] > 0.f ? 1.f : top) / (1.f + bottom);
+      // above 0 the sigmoid itself; where all lie below, relative to the largest logit
+      const float e = __expf(-fabsf(z[v])), q = __builtin_amdgcn_rcpf(1.f + e);
+      const bool positive = z[v] > 0.f;
+      const float top = m > 0.f ? (positive ? 1.f : e) : soft[v];
+      p[v] = z[v] < -708.f ? 0.f : top * q;
+      rest[v] = (positive ? e : 1.f) * q;
       all += p[v];
     }
     all = wave_sum(all);
@@ -105,7 +109,10 @@ __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL]
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     soft[v] *= inv;
-    if constexpr (!SIG) p[v] = soft[v];
+    if constexpr (!SIG) {
+      p[v] = soft[v];
+      rest[v] = 1.f;
+    }
   }
 }
 
@@ -121,13 +128,13 @@ __device__ __forceinline__ void load_token(const BalanceArgs& a, int t, float (&
 __device__ __forceinline__ bool counted(const BalanceArgs& a, int t) { return !a.mask || a.mask[t] != 0; }
 
 template <int DT, int VPL, bool SIG>
-__global__ __launch_bounds__(kWaves * kWave) void balance_kernel(BalanceArgs a) {
+__global__ __launch_bounds__(run_waves(VPL) * kWave) void balance_kernel(BalanceArgs a) {
+  constexpr int kWaves = run_waves(VPL);
   __shared__ int hist[kWave * VPL];
   __shared__ float psum[kWaves][kWave * VPL];
   __shared__ float zsum[kWaves];
   __shared__ int nsum[kWaves];
   const int lane = lane_id(), wave = (int)(threadIdx.x / kWave);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   const int t0 = blockIdx.x * a.tile, t1 = (int)min((int64_t)a.T, (int64_t)t0 + a.tile);
   for (int q = sequences_before(a, t0); q < a.S; ++q) {  // uniform over the workgroup
     const int begin = seq_begin(a, q);
@@ -147,8 +154,8 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_kernel(BalanceArgs a) 
       for (int v = 0; v < VPL; ++v) z[v] = next[v];
       if (t + kWaves < hi) load_token<DT, VPL>(a, t + kWaves, next);
       if (!counted(a, t)) continue;
-      float soft[VPL], s[VPL], lse;
-      scores<VPL, SIG>(z, soft, s, lse);
+      float soft[VPL], s[VPL], rest[VPL], lse;
+      scores<VPL, SIG>(z, soft, s, rest, lse);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) p[v] += s[v];
       zz += lse * lse;
@@ -193,93 +200,96 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_kernel(BalanceArgs a) 
   }
 }
 
-// Sum over the workgroup of 1024 threads, in a fixed order, in every thread.
-__device__ __forceinline__ double block_sum(double v, double* shared) {
+// Three sums over the workgroup of 1024 threads, in a fixed order, in every thread.
+__device__ __forceinline__ void block_sums(double (&v)[3], double (&shared)[3][16]) {
 #pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
-  __syncthreads();
-  if (lane_id() == 0) shared[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = 0.0;
+  for (int i = 0; i < 3; ++i) v[i] = wave_sum(v[i]);
+  if (lane_id() == 0)
 #pragma unroll
-  for (int w = 0; w < 16; ++w) v += shared[w];
-  return v;
+    for (int i = 0; i < 3; ++i) shared[i][threadIdx.x / kWave] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    v[i] = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v[i] += shared[i][w];
+  }
 }
 
-// Sequence blockIdx.y, experts from blockIdx.x * kCols on.
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, double sum, double z, double all, double some) {
+  a.loss[0] = some > 0 ? (float)(sum * a.E / (a.K * some)) : 0.f;
+  a.loss[1] = all > 0 ? (float)(z / all) : 0.f;
+}
+
+// Sequence blockIdx.y, a.cols experts from blockIdx.x * a.cols on.
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
-  __shared__ double sp[kGroups][kCols];
-  __shared__ int sc[kGroups][kCols];
-  __shared__ double sums[16];
-  __shared__ bool last;
-  const int q = blockIdx.y, col = threadIdx.x % kCols, g = threadIdx.x / kCols;
-  const int e = blockIdx.x * kCols + col;
+  __shared__ double sp[1024];
+  __shared__ int sc[1024];
+  __shared__ double sums[3][16];
+  const int q = blockIdx.y, wide = (a.cols + kCols - 1) / kCols * kCols, groups = 1024 / wide;
+  const int col = threadIdx.x % wide, g = threadIdx.x / wide;
+  const int e = blockIdx.x * a.cols + col;
+  const bool mine = g < groups && col < a.cols && e < a.E;
   const int lo = seq_begin(a, q), hi = seq_end(a, q);
   const int w0 = lo < hi ? lo / a.tile : 0, w1 = lo < hi ? (hi - 1) / a.tile : -1;
+  double v[3] = {0.0, 0.0, 0.0};  // counts times probabilities, z, tokens
+  if (blockIdx.x == 0)
+    for (int w = w0 + (int)threadIdx.x; w <= w1; w += 1024) {
+      v[1] += a.part_z[w + q];
+      v[2] += a.part_n[w + q];
+    }
   double p = 0.0;
   int c = 0;
-  if (e < a.E)
-    for (int w = w0 + g; w <= w1; w += kGroups) {
-      const size_t at = (size_t)(w + q) * a.E + e;
-      p += a.part_p[at];
-      c += a.part_c[at];
+  if (mine) {
+    const float* pp = a.part_p + e;
+    const int* pc = a.part_c + e;
+#pragma unroll 8
+    for (int w = w0 + g; w <= w1; w += groups) {
+      p += pp[(size_t)(w + q) * a.E];
+      c += pc[(size_t)(w + q) * a.E];
     }
-  sp[g][col] = p;
-  sc[g][col] = c;
+  }
+  sp[threadIdx.x] = p;
+  sc[threadIdx.x] = c;
   __syncthreads();
-  double product = 0.0;
-  if (g == 0) {
-    for (int k = 1; k < kGroups; ++k) {
-      p += sp[k][col];
-      c += sc[k][col];
+  if (mine && g == 0) {
+    for (int k = 1; k < groups; ++k) {
+      p += sp[k * wide + col];
+      c += sc[k * wide + col];
     }
-    if (e < a.E) {
-      a.probs[(size_t)q * a.E + e] = (float)p;
-      a.counts[(size_t)q * a.E + e] = c;
-      product = p * c;
-    }
+    a.probs[(size_t)q * a.E + e] = (float)p;
+    a.counts[(size_t)q * a.E + e] = c;
+    v[0] = p * c;
   }
-  product = block_sum(product, sums);
-  double z = 0.0, n = 0.0;
-  if (blockIdx.x == 0) {  // uniform
-    for (int w = w0 + (int)threadIdx.x; w <= w1; w += 1024) {
-      z += a.part_z[w + q];
-      n += a.part_n[w + q];
-    }
-    z = block_sum(z, sums);
-    n = block_sum(n, sums);  // whole numbers: exact
+  block_sums(v, sums);
+  if (threadIdx.x != 0) return;
+  const double n = v[2];
+  if (blockIdx.x == 0) a.tokens[q] = (int)n;  // whole numbers: exact
+  if (gridDim.x * gridDim.y == 1) {
+    write_loss(a, n > 0 ? v[0] / (n * n) : 0.0, v[1], n, n > 0 ? 1.0 : 0.0);
+  } else {
+    a.seq_sum[(size_t)q * gridDim.x + blockIdx.x] = v[0];
+    if (blockIdx.x == 0) a.seq_z[q] = v[1];
   }
-  if (threadIdx.x == 0) {
-    a.seq_sum[(size_t)q * gridDim.x + blockIdx.x] = product;
-    if (blockIdx.x == 0) {
-      a.seq_z[q] = z;
-      a.tokens[q] = (int)n;
-    }
-    __threadfence();
-    last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double sum = 0.0, all = 0.0, some = 0.0, zz = 0.0;
-  for (int r = threadIdx.x; r < a.S; r += 1024) {
-    const double nq = a.tokens[r];
-    if (nq <= 0) continue;
+}
+
+// The losses from the sums of the sequences' columns.
+__global__ __launch_bounds__(1024) void balance_loss_kernel(BalanceArgs a, int columns) {
+  __shared__ double sums[3][16], more[3][16];
+  double v[3] = {0.0, 0.0, 0.0}, some[3] = {0.0, 0.0, 0.0};
+  for (int q = threadIdx.x; q < a.S; q += 1024) {
+    const double n = a.tokens[q];
+    if (n <= 0) continue;
     double s = 0.0;
-    for (unsigned b = 0; b < gridDim.x; ++b) s += a.seq_sum[(size_t)r * gridDim.x + b];
-    sum += s / (nq * nq);
-    zz += a.seq_z[r];
-    all += nq;
-    some += 1.0;
+    for (int b = 0; b < columns; ++b) s += a.seq_sum[(size_t)q * columns + b];
+    v[0] += s / (n * n);
+    v[1] += a.seq_z[q];
+    v[2] += n;
+    some[0] += 1.0;
   }
-  sum = block_sum(sum, sums);
-  zz = block_sum(zz, sums);
-  all = block_sum(all, sums);
-  some = block_sum(some, sums);
-  if (threadIdx.x == 0) {
-    a.loss[0] = some > 0 ? (float)(sum * a.E / (a.K * some)) : 0.f;
-    a.loss[1] = all > 0 ? (float)(zz / all) : 0.f;
-  }
+  block_sums(v, sums);
+  block_sums(some, more);
+  if (threadIdx.x == 0) write_loss(a, v[0], v[1], v[2], some[0]);
 }
 
 template <int DT, int VPL, bool SIG>
@@ -325,20 +335,13 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
           c[v] = e < a.E ? g0 * (f * (float)a.counts[(size_t)q * a.E + e]) : 0.f;
         }
       }
-      float soft[VPL], p[VPL], lse, dot = 0.f;
-      scores<VPL, SIG>(z, soft, p, lse);
+      float soft[VPL], p[VPL], rest[VPL], lse, dot = 0.f;
+      scores<VPL, SIG>(z, soft, p, rest, lse);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) dot += p[v] * c[v];
       dot = wave_sum(dot);
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        float s = p[v];
-        if constexpr (SIG) {  // 1 - sigmoid(z)
-          const float e = expf(-fabsf(z[v]));
-          s *= (z[v] > 0.f ? e : 1.f) / (1.f + e);
-        }
-        d[v] = s * (c[v] - dot) + g1 * lse * soft[v];
-      }
+      for (int v = 0; v < VPL; ++v) d[v] = p[v] * rest[v] * (c[v] - dot) + g1 * lse * soft[v];
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -356,7 +359,7 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
 template <int DT, int VPL, bool SIG>
 hipError_t launch_one(const BalanceArgs& a, bool backward, dim3 grid, hipStream_t s) {
   if (backward) balance_bwd_kernel<DT, VPL, SIG><<<grid, kWaves * kWave, 0, s>>>(a);
-  else balance_kernel<DT, VPL, SIG><<<grid, kWaves * kWave, 0, s>>>(a);
+  else balance_kernel<DT, VPL, SIG><<<grid, run_waves(VPL) * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -377,18 +380,27 @@ hipError_t launch_typed(const BalanceArgs& a, bool backward, dim3 grid, hipStrea
 
 }  // namespace
 
+// Tokens of a run: enough runs for the CUs, a token or more for each wave.
 int balance_tile(int64_t T) {
-  const int64_t t = (T + 511) / 512;
-  return (int)(t < 4 ? 4 : t);
+  const int64_t t = (T + kRuns - 1) / kRuns;
+  return (int)(t < 16 ? 16 : t);
 }
 int balance_runs(int64_t T) { return T > 0 ? (int)((T + balance_tile(T) - 1) / balance_tile(T)) : 1; }
 int balance_columns(int E) { return (E + kCols - 1) / kCols; }
 
 hipError_t launch_balance(BalanceArgs a, hipStream_t s) {
   a.tile = balance_tile(a.T);
-  const hipError_t e = launch_typed(a, false, dim3(balance_runs(a.T)), s);
+  const int runs = balance_runs(a.T);
+  hipError_t e = launch_typed(a, false, dim3(runs), s);
   if (e != hipSuccess) return e;
-  balance_finish_kernel<<<dim3(balance_columns(a.E), a.S), 1024, 0, s>>>(a);
+  // one sequence of few partials is one workgroup's work, losses included
+  const bool direct = a.S == 1 && (int64_t)runs * a.E <= kDirect;
+  a.cols = direct ? a.E : kCols;
+  const int columns = direct ? 1 : balance_columns(a.E);
+  balance_finish_kernel<<<dim3(columns, a.S), 1024, 0, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (columns * a.S == 1) return hipSuccess;
+  balance_loss_kernel<<<1, 1024, 0, s>>>(a, columns);
   return hipGetLastError();
 }
 

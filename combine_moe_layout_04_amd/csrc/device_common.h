@@ -140,6 +140,24 @@ __device__ __forceinline__ float wave_sum(float v) {
   return read_lane_f(v, 63);
 }
 
+// As dpp_float, but lanes without a source keep their own value.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_own(float v) {
+  const int b = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, ROWS, 0xF, false));
+}
+
+// The largest of the numbers (NaN only where there is nothing else).
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp_or_own<0x111, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x112, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x114, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x118, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x142, 0xA>(v));
+  v = fmaxf(v, dpp_or_own<0x143, 0xC>(v));
+  return read_lane_f(v, 63);
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);

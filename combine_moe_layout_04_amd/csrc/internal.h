@@ -189,9 +189,9 @@ struct BalanceArgs {
   int* tokens;            // [S]
   int T, E, K, S, dtype, itype, score;
   int tile;               // tokens of a workgroup (backward: of a wave; set by the launcher)
+  int cols;               // second kernel: experts of a workgroup (set by the launcher)
   float *part_p, *part_z;  // partials by slot (run + sequence): [slots, E], [slots]
   int *part_c, *part_n;
-  unsigned* ticket;       // workgroups of the second kernel that are done
   double *seq_sum, *seq_z;  // [S, columns], [S]
   const float* grad_loss;   // backward: [2]
   const void* grad_base;    // [T, E] or null

@@ -82,8 +82,6 @@ __device__ float block_rstd(const float (&f)[N], int H, float eps, float* red, f
 
 enum : int { kBefore = 0, kRows = 1, kGather = 2 };  // where y comes from
 
-constexpr int kGatherRows = 4;  // receive rows in flight
-
 template <int DT, int CPL, int SRC>
 __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
   constexpr int V = Elems<DT>::kPerChunk;
@@ -121,6 +119,7 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < CPL * V; ++i) f[i] = 0.f;
+      constexpr int kGatherRows = CPL == 1 ? 8 : 4;  // receive rows in flight
       for (int k0 = 0; k0 < a.K; k0 += kGatherRows) {  // sums in k order from +0
         u32x4 g[kGatherRows][CPL];
         float w[kGatherRows];
@@ -132,7 +131,12 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
           w[k] = there && a.w ? a.w[(size_t)t * a.K + k0 + k] : 1.f;
           good[k] = (unsigned)p < (unsigned)a.R;
           if (there && !good[k] && tid == 0) atomicOr(a.status, MOE_STATUS_BAD_POSITION);
-          if (good[k]) load(a.y, (size_t)p * a.nch, g[k]);
+          if (good[k])
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) {  // read once
+              const int j = tid + i * blockDim.x;
+              g[k][i] = j < a.nch ? __builtin_nontemporal_load(static_cast<const u32x4*>(a.y) + (size_t)p * a.nch + j) : zero;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kGatherRows; ++k) {
@@ -250,7 +254,7 @@ __global__ __launch_bounds__(1024) void quant_block_kernel(NormArgs a) {
 template <int DT, int CPL, bool BLOCK>
 __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int V = Elems<DT>::kPerChunk, N = CPL * V;
-  __shared__ float red[2][kMaxWaves];
+  __shared__ float red[4][kMaxWaves];
   const int tid = threadIdx.x, run = blockIdx.x, H = a.nch * V;
   // the run's rows: a part of one gate's tokens, or whole gates
   int64_t t0, t1;
@@ -263,18 +267,22 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
     t1 = min(t0 + a.rows, (int64_t)a.T);
   }
   const u32x4 zero = {0, 0, 0, 0};
-  auto load = [&](const void* p, size_t at, float(&to)[N]) {
+  auto chunks = [&](const void* p, size_t row, u32x4(&to)[CPL]) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int j = tid + i * blockDim.x;
-      unpack<DT>(j < a.nch ? static_cast<const u32x4*>(p)[at + j] : zero, to + i * V);
+      to[i] = p && j < a.nch ? static_cast<const u32x4*>(p)[row * a.nch + j] : zero;
     }
   };
-  auto store = [&](void* p, size_t at, const float(&from)[N]) {
+  auto floats = [&](const u32x4(&from)[CPL], float(&to)[N]) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) unpack<DT>(from[i], to + i * V);
+  };
+  auto store = [&](void* p, size_t row, const float(&from)[N]) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int j = tid + i * blockDim.x;
-      if (j < a.nch) static_cast<u32x4*>(p)[at + j] = pack<DT>(from + i * V);
+      if (j < a.nch) static_cast<u32x4*>(p)[row * a.nch + j] = pack<DT>(from + i * V);
     }
   };
   auto partial = [&](float* p, size_t at, const float(&from)[N]) {
@@ -283,74 +291,94 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
       const int j = tid + i * blockDim.x;
       if (j < a.nch)
 #pragma unroll
-        for (int v = 0; v < V; ++v) p[at * H + (size_t)j * V + v] = from[i * V + v];
+        for (int v = 0; v < V; v += 4)
+          *reinterpret_cast<float4*>(p + at * H + (size_t)j * V + v) =
+              make_float4(from[i * V + v], from[i * V + v + 1], from[i * V + v + 2], from[i * V + v + 3]);
+    }
+  };
+  // What a row reads: asked for a row ahead, so that it arrives during the sums of the
+  // row before it.
+  struct Row {
+    u32x4 g[CPL], gn[CPL], x[CPL], y[CPL], gate[CPL];
+    float r1, r2;
+  };
+  auto fetch = [&](int64_t t, Row& r) {
+    chunks(a.g, t, r.g);
+    chunks(a.gn, t, r.gn);
+    chunks(a.gn ? a.x : nullptr, t, r.x);
+    r.r1 = 1.f;
+    if constexpr (BLOCK) {
+      chunks(a.y, t, r.y);
+      chunks(a.gate, t / a.group, r.gate);
+      r.r1 = a.rstd[2 * t];
+      r.r2 = a.rstd[2 * t + 1];
+    } else {
+      r.r2 = a.rstd[t];
     }
   };
   float s1[N], s2[N], sg[N];  // sums over the run
 #pragma unroll
   for (int i = 0; i < N; ++i) s1[i] = s2[i] = sg[i] = 0.f;
   float w1[N], w2[N];
-  if (BLOCK && a.w1) load(a.w1, 0, w1);
-  if (a.w2) load(a.w2, 0, w2);
+  u32x4 c[CPL];
+  chunks(BLOCK ? a.w1 : nullptr, 0, c);
+  floats(c, w1);
+  chunks(a.w2, 0, c);
+  floats(c, w2);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w1[i] += a.offset;
+    w2[i] += a.offset;
+  }
+  Row next;
+  if (t0 < t1) fetch(t0, next);
   for (int64_t t = t0; t < t1; ++t) {
-    const size_t row = (size_t)t * a.nch;
-    float d[N], y[N], o[N];
-    float r1 = 1.f, r2;
+    const Row r = next;
+    if (t + 1 < t1) fetch(t + 1, next);
+    const int odd = (int)(t - t0) & 1;  // two rows' sums lie apart: one barrier a sum
+    float d[N], y[N], o[N], g[N];
+    floats(r.g, d);
     if constexpr (BLOCK) {
-      r1 = a.rstd[2 * t];
-      r2 = a.rstd[2 * t + 1];
-    } else {
-      r2 = a.rstd[t];
-    }
-    if (a.g) {
-      load(a.g, row, d);
-    } else {
+      floats(r.y, y);
+      floats(r.gate, g);
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = 0.f;
-    }
-    float g[N];
-    if (BLOCK && a.gate) load(a.gate, (size_t)(t / a.group) * a.nch, g);
-    if (BLOCK && a.y) {
-      load(a.y, row, y);
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] *= r1;
+      for (int i = 0; i < N; ++i) y[i] *= r.r1;
     }
     if (a.gn) {
       float gn[N];
-      load(a.gn, row, gn);
-      load(a.x, row, o);
+      floats(r.gn, gn);
+      floats(r.x, o);
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if constexpr (BLOCK) {  // z again, as the forward pass had it
-          float f = a.w1 ? y[i] * (w1[i] + a.offset) : y[i];
+          float f = a.w1 ? y[i] * w1[i] : y[i];
           if (a.gate) f *= g[i];
           o[i] = a.residual * o[i] + f;
         }
-        o[i] *= r2;
+        o[i] *= r.r2;
         s2[i] += gn[i] * o[i];
-        gn[i] *= w2[i] + a.offset;
+        gn[i] *= w2[i];
         dot += gn[i] * o[i];
       }
-      dot = block_sum(dot, red[0]) / (float)H;
+      dot = block_sum(dot, red[odd]) / (float)H;
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] += r2 * (gn[i] - o[i] * dot);
+      for (int i = 0; i < N; ++i) d[i] += r.r2 * (gn[i] - o[i] * dot);
     }
     if constexpr (!BLOCK) {
-      if (a.gx) store(a.gx, row, d);
-      if (a.gn) __syncthreads();  // red[0] is free again
+      if (a.gx) store(a.gx, t, d);
       continue;
     }
     if (a.gx) {
       float gx[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) gx[i] = a.residual * d[i];
-      store(a.gx, row, gx);
+      store(a.gx, t, gx);
     }
     if (a.gate) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (a.gg) sg[i] += d[i] * (a.w1 ? y[i] * (w1[i] + a.offset) : y[i]);
+        if (a.gg) sg[i] += d[i] * (a.w1 ? y[i] * w1[i] : y[i]);
         d[i] *= g[i];
       }
     }
@@ -359,20 +387,19 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         s1[i] += d[i] * y[i];
-        d[i] *= w1[i] + a.offset;
+        d[i] *= w1[i];
         dot += d[i] * y[i];
       }
-      dot = block_sum(dot, red[1]) / (float)H;
+      dot = block_sum(dot, red[2 + odd]) / (float)H;
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = r1 * (d[i] - y[i] * dot);
+      for (int i = 0; i < N; ++i) d[i] = r.r1 * (d[i] - y[i] * dot);
     }
-    if (a.gy) store(a.gy, row, d);
+    if (a.gy) store(a.gy, t, d);
     if (a.gg && a.parts == 1 && (t + 1) % a.group == 0) {  // the gate's last token
-      store(a.gg, (size_t)(t / a.group) * a.nch, sg);
+      store(a.gg, t / a.group, sg);
 #pragma unroll
       for (int i = 0; i < N; ++i) sg[i] = 0.f;
     }
-    __syncthreads();  // red is free again
   }
   if (a.part1) partial(a.part1, run, s1);
   if (a.part2) partial(a.part2, run, s2);
@@ -380,11 +407,12 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
 }
 
 // Adds partials: blockIdx.y 0 the next norm's weight, 1 the post-norm's, 2.. the gates.
+// 64 columns a workgroup, four a thread; a sixteenth of the partials each.
 template <int DT>
-__global__ __launch_bounds__(1024) void norm_join_kernel(NormBwdArgs a) {
-  __shared__ float sum[16][64];
+__global__ __launch_bounds__(256) void norm_join_kernel(NormBwdArgs a) {
+  __shared__ float4 sum[16][16];
   const int H = a.nch * Elems<DT>::kPerChunk;
-  const int col = blockIdx.x * 64 + threadIdx.x % 64, k = threadIdx.x / 64;
+  const int q = threadIdx.x % 16, k = threadIdx.x / 16, col = blockIdx.x * 64 + 4 * q;
   const float* from;
   void* to;
   int n = a.runs;
@@ -402,15 +430,31 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormBwdArgs a) {
     n = a.parts;
   }
   if (!to) return;  // uniform
-  float s = 0.f;
-  if (col < H)
-    for (int i = k; i < n; i += 16) s += from[(size_t)i * H + col];
-  sum[k][threadIdx.x % 64] = s;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < H) {
+#pragma unroll 8
+    for (int i = k; i < n; i += 16) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (size_t)i * H + col);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  sum[k][q] = s;
   __syncthreads();
   if (k != 0 || col >= H) return;
-  for (int i = 1; i < 16; ++i) s += sum[i][threadIdx.x];
-  if constexpr (DT == kF32) static_cast<float*>(to)[row * H + col] = s;
-  else static_cast<uint16_t*>(to)[row * H + col] = (uint16_t)f32_to_bf16(s);
+  for (int i = 1; i < 16; ++i) {
+    const float4 v = sum[i][q];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  if constexpr (DT == kF32)
+    *reinterpret_cast<float4*>(static_cast<float*>(to) + row * H + col) = s;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(to) + row * H + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
 int chunks_per_lane(int nch) { return nch <= 512 ? 1 : nch <= 1024 ? 2 : 4; }
@@ -438,7 +482,7 @@ hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
   const bool gates = a.gg && a.parts != 1;  // no part (an empty batch): zeros
   if (!a.gw1 && !a.gw2 && !gates) return hipSuccess;
   const int H = a.nch * Elems<DT>::kPerChunk;
-  norm_join_kernel<DT><<<dim3((H + 63) / 64, gates ? 2 + a.gates : 2), 1024, 0, s>>>(a);
+  norm_join_kernel<DT><<<dim3((H + 63) / 64, gates ? 2 + a.gates : 2), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -20,26 +20,40 @@ __device__ __forceinline__ float quant_scale(uint32_t amax_bits) {
   return s < 0x1p-126f ? 0x1p-126f : s;  // a NaN stays
 }
 
-// A row with an infinity or NaN has that as its scale, and zeros: what is made of it is NaN.
-__device__ __forceinline__ int quant_one(float x, float s, float inv) {
-  if (!(s < INFINITY)) return 0;
+// The integer (as a float) nearest to x / s: exact, for a finite row.
+__device__ __forceinline__ float quant_exact(float x, float s, float inv) {
   float q = rintf(x * inv);
   const float r = __builtin_fmaf(-q, s, x), h = 0.5f * s;
   const bool odd = (static_cast<int>(q) & 1) != 0;
   if (r > h || (r == h && odd)) q += 1.f;
   else if (-r > h || (-r == h && odd)) q -= 1.f;
-  return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
+  return q;
 }
 
 // Values of one 16-byte chunk of a row (4 float32, 8 bfloat16) as its 4 or 8 bytes.
+// |x / s| is at most 127 (1 + 2^-23), so x * inv is within 2^-15 of it: only where that
+// lies nearer than 2^-14 to a half can its rounding be another than the quotient's.  A
+// row with an infinity or NaN has that as its scale, and zeros: what is made of it is
+// NaN.
 template <int V>
 __device__ __forceinline__ void store_quant(int8_t* row, int chunk, const float* f, float s, float inv) {
+  float q[V], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float t = f[i] * inv;
+    q[i] = rintf(t);
+    far = fmaxf(far, fabsf(t - q[i]));
+  }
+  if (far > 0.5f - 0x1p-14f)
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = quant_exact(f[i], s, inv);
+  const uint32_t keep = s < INFINITY ? 0xFFFFFFFFu : 0u;
   uint32_t w[V / 4];
 #pragma unroll
   for (int d = 0; d < V / 4; ++d) {
-    w[d] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[d] |= ((uint32_t)quant_one(f[4 * d + i], s, inv) & 0xFFu) << (8 * i);
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)q[4 * d + 1], (uint32_t)(int)q[4 * d], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)q[4 * d + 3], (uint32_t)(int)q[4 * d + 2], 0x04000C0Cu);
+    w[d] = (lo | hi) & keep;
   }
   uint32_t* p = reinterpret_cast<uint32_t*>(row) + (size_t)chunk * (V / 4);
   if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
