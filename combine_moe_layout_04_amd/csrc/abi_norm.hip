@@ -37,7 +37,7 @@ moe::NormBwdArgs bwd_args(int dtype, int64_t T, int64_t H, int64_t gates) {
   a.gates = (int)gates;
   a.group = (int)(T > 0 ? T / gates : 1);
   a.dtype = dtype;
-  moe::norm_bwd_plan(T, a.group, &a.rows, &a.parts, &a.runs);
+  moe::norm_bwd_plan(T, a.group, a.nch, &a.rows, &a.parts, &a.runs);
   return a;
 }
 

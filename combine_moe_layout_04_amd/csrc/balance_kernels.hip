@@ -148,12 +148,20 @@ __global__ __launch_bounds__(run_waves(VPL) * kWave) void balance_kernel(Balance
 #pragma unroll
     for (int v = 0; v < VPL; ++v) p[v] = 0.f;
     float z[VPL], next[VPL];
-    if (lo + wave < hi) load_token<DT, VPL>(a, lo + wave, next);
+    bool there = false, there_next = false;
+    if (lo + wave < hi) {
+      load_token<DT, VPL>(a, lo + wave, next);
+      there_next = counted(a, lo + wave);
+    }
     for (int t = lo + wave; t < hi; t += kWaves) {  // wave-uniform
 #pragma unroll
       for (int v = 0; v < VPL; ++v) z[v] = next[v];
-      if (t + kWaves < hi) load_token<DT, VPL>(a, t + kWaves, next);
-      if (!counted(a, t)) continue;
+      there = there_next;
+      if (t + kWaves < hi) {
+        load_token<DT, VPL>(a, t + kWaves, next);
+        there_next = counted(a, t + kWaves);
+      }
+      if (!there) continue;
       float soft[VPL], s[VPL], rest[VPL], lse;
       scores<VPL, SIG>(z, soft, s, rest, lse);
 #pragma unroll
@@ -312,10 +320,15 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
   float c[VPL];  // the gradient of P of the sequence `at`
   float z[VPL], next[VPL];
   load_token<DT, VPL>(a, t0, next);
+  bool there, there_next = counted(a, t0);
   for (int t = t0; t < t1; ++t) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) z[v] = next[v];
-    if (t + 1 < t1) load_token<DT, VPL>(a, t + 1, next);
+    there = there_next;
+    if (t + 1 < t1) {
+      load_token<DT, VPL>(a, t + 1, next);
+      there_next = counted(a, t + 1);
+    }
     while (q < a.S && end <= t) {
       ++q;
       begin = q < a.S ? seq_begin(a, q) : a.T;
@@ -324,7 +337,7 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
     float d[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) d[v] = 0.f;
-    if (q < a.S && begin <= t && counted(a, t)) {  // wave-uniform
+    if (q < a.S && begin <= t && there) {  // wave-uniform
       if (q != at) {
         at = q;
         const double n = a.tokens[q];
@@ -380,10 +393,10 @@ hipError_t launch_typed(const BalanceArgs& a, bool backward, dim3 grid, hipStrea
 
 }  // namespace
 
-// Tokens of a run: enough runs for the CUs, a token or more for each wave.
+// Tokens of a run: enough runs for the CUs, two tokens or more for each wave.
 int balance_tile(int64_t T) {
   const int64_t t = (T + kRuns - 1) / kRuns;
-  return (int)(t < 16 ? 16 : t);
+  return (int)(t < 32 ? 32 : t);
 }
 int balance_runs(int64_t T) { return T > 0 ? (int)((T + balance_tile(T) - 1) / balance_tile(T)) : 1; }
 int balance_columns(int E) { return (E + kCols - 1) / kCols; }

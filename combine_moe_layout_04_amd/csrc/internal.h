@@ -235,7 +235,7 @@ struct NormBwdArgs {
   bool block;             // after a block
 };
 
-void norm_bwd_plan(int64_t T, int64_t group, int* rows, int* parts, int* runs);
+void norm_bwd_plan(int64_t T, int64_t group, int nch, int* rows, int* parts, int* runs);
 
 // Grouped product of 8-bit rows and weights.
 struct I8Args {

@@ -63,7 +63,7 @@ template <int N>
 __device__ float block_rstd(const float (&f)[N], int H, float eps, float* red, float* red2, float* red3) {
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) ss += f[i] * f[i];
+  for (int i = 0; i < N; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
   ss = block_sum(ss, red);
   if (ss < 3e38f && (ss > 0x1p-100f || eps > 0x1p-70f)) return 1.f / sqrtf(ss / (float)H + eps);  // uniform
   uint32_t top = 0;
@@ -198,33 +198,41 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
 
 // ---- rows to 8 bits -----------------------------------------------------------------
 
-// A wave per row where a row has at most 256 chunks (4 a lane), else a workgroup.
-template <int DT>
+// A wave takes 4 / CPL rows of at most 64 CPL chunks, four chunks a lane in all; wider
+// rows a workgroup each.
+template <int DT, int CPL>
 __global__ __launch_bounds__(256) void quant_wave_kernel(NormArgs a) {
-  constexpr int V = Elems<DT>::kPerChunk, CPL = 4;
-  const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (t >= a.T) return;  // wave-uniform
+  constexpr int V = Elems<DT>::kPerChunk, kRows = 4 / CPL;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + threadIdx.x / kWave) * kRows;
   const int lane = lane_id();
-  const u32x4* p = static_cast<const u32x4*>(a.x) + (size_t)t * a.nch;
-  u32x4 c[CPL];
+  u32x4 c[kRows][CPL];
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    const int j = lane + i * kWave;
-    c[i] = j < a.nch ? p[j] : u32x4{0, 0, 0, 0};
+  for (int r = 0; r < kRows; ++r) {
+    const u32x4* p = static_cast<const u32x4*>(a.x) + (size_t)(t0 + r) * a.nch;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int j = lane + i * kWave;
+      c[r][i] = t0 + r < a.T && j < a.nch ? p[j] : u32x4{0, 0, 0, 0};
+    }
   }
-  float f[CPL * V];
-  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) unpack<DT>(c[i], f + i * V);
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t t = t0 + r;
+    if (t >= a.T) return;  // wave-uniform
+    float f[CPL * V];
+    uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < CPL * V; ++i) top = max(top, abs_bits(f[i]));
-  const float s = quant_scale(wave_max(top)), inv = 1.f / s;
+    for (int i = 0; i < CPL; ++i) unpack<DT>(c[r][i], f + i * V);
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    const int j = lane + i * kWave;
-    if (j < a.nch) store_quant<V>(a.q + (size_t)t * a.nch * V, j, f + i * V, s, inv);
+    for (int i = 0; i < CPL * V; ++i) top = max(top, abs_bits(f[i]));
+    const float s = quant_scale(wave_max(top)), inv = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int j = lane + i * kWave;
+      if (j < a.nch) store_quant<V>(a.q + (size_t)t * a.nch * V, j, f + i * V, s, inv);
+    }
+    if (lane == 0) a.scale[t] = s;
   }
-  if (lane == 0) a.scale[t] = s;
 }
 
 template <int DT>
@@ -251,58 +259,54 @@ __global__ __launch_bounds__(1024) void quant_block_kernel(NormArgs a) {
 
 // ---- backward ---------------------------------------------------------------------
 
-template <int DT, int CPL, bool BLOCK>
-__global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs a) {
+// Rows of up to 512 chunks are asked for a row ahead; wider ones have no registers for
+// that (7168 bfloat16, 4096 rows: 110 us without, 118 with; rows past 16 KiB keep part of
+// it in memory: 16384 bfloat16 take 1.2 ms, eight times their floor).  The chunks stay as they were read, and each of the three passes over them (the
+// first sum, the second, the end) makes its numbers again, a chunk at a time: what lives
+// over a pass is the sums over the run and v.
+template <int DT, int CPL, bool BLOCK, bool kAhead, int MOST>
+__global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int V = Elems<DT>::kPerChunk, N = CPL * V;
   __shared__ float red[4][kMaxWaves];
   const int tid = threadIdx.x, run = blockIdx.x, H = a.nch * V;
   // the run's rows: a part of one gate's tokens, or whole gates
-  int64_t t0, t1;
+  int t0, t1;
   if (a.parts > 1) {
-    const int64_t group = run / a.parts, part = run % a.parts;
+    const int group = run / a.parts, part = run % a.parts;
     t0 = group * a.group + part * a.rows;
     t1 = min(t0 + a.rows, (group + 1) * a.group);
   } else {
-    t0 = (int64_t)run * a.rows;
-    t1 = min(t0 + a.rows, (int64_t)a.T);
+    t0 = (int)min((int64_t)run * a.rows, (int64_t)a.T);
+    t1 = (int)min((int64_t)t0 + a.rows, (int64_t)a.T);
   }
   const u32x4 zero = {0, 0, 0, 0};
-  auto chunks = [&](const void* p, size_t row, u32x4(&to)[CPL]) {
+  auto chunks = [&](const void* p, int row, u32x4(&to)[CPL]) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int j = tid + i * blockDim.x;
-      to[i] = p && j < a.nch ? static_cast<const u32x4*>(p)[row * a.nch + j] : zero;
+      to[i] = p && j < a.nch ? static_cast<const u32x4*>(p)[(size_t)row * a.nch + j] : zero;
     }
   };
-  auto floats = [&](const u32x4(&from)[CPL], float(&to)[N]) {
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) unpack<DT>(from[i], to + i * V);
+  auto store = [&](void* p, int row, int i, const float* from) {
+    const int j = tid + i * blockDim.x;
+    if (j < a.nch) static_cast<u32x4*>(p)[(size_t)row * a.nch + j] = pack<DT>(from);
   };
-  auto store = [&](void* p, size_t row, const float(&from)[N]) {
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      const int j = tid + i * blockDim.x;
-      if (j < a.nch) static_cast<u32x4*>(p)[row * a.nch + j] = pack<DT>(from + i * V);
-    }
-  };
-  auto partial = [&](float* p, size_t at, const float(&from)[N]) {
+  auto partial = [&](float* p, const float(&from)[N]) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int j = tid + i * blockDim.x;
       if (j < a.nch)
 #pragma unroll
         for (int v = 0; v < V; v += 4)
-          *reinterpret_cast<float4*>(p + at * H + (size_t)j * V + v) =
+          *reinterpret_cast<float4*>(p + (size_t)run * H + (size_t)j * V + v) =
               make_float4(from[i * V + v], from[i * V + v + 1], from[i * V + v + 2], from[i * V + v + 3]);
     }
   };
-  // What a row reads: asked for a row ahead, so that it arrives during the sums of the
-  // row before it.
   struct Row {
     u32x4 g[CPL], gn[CPL], x[CPL], y[CPL], gate[CPL];
     float r1, r2;
   };
-  auto fetch = [&](int64_t t, Row& r) {
+  auto fetch = [&](int t, Row& r) {
     chunks(a.g, t, r.g);
     chunks(a.gn, t, r.gn);
     chunks(a.gn ? a.x : nullptr, t, r.x);
@@ -310,8 +314,8 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
     if constexpr (BLOCK) {
       chunks(a.y, t, r.y);
       chunks(a.gate, t / a.group, r.gate);
-      r.r1 = a.rstd[2 * t];
-      r.r2 = a.rstd[2 * t + 1];
+      r.r1 = a.rstd[2 * (size_t)t];
+      r.r2 = a.rstd[2 * (size_t)t + 1];
     } else {
       r.r2 = a.rstd[t];
     }
@@ -319,91 +323,124 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_bwd_kernel(NormBwdArgs 
   float s1[N], s2[N], sg[N];  // sums over the run
 #pragma unroll
   for (int i = 0; i < N; ++i) s1[i] = s2[i] = sg[i] = 0.f;
-  float w1[N], w2[N];
-  u32x4 c[CPL];
-  chunks(BLOCK ? a.w1 : nullptr, 0, c);
-  floats(c, w1);
-  chunks(a.w2, 0, c);
-  floats(c, w2);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w1[i] += a.offset;
-    w2[i] += a.offset;
-  }
-  Row next;
-  if (t0 < t1) fetch(t0, next);
-  for (int64_t t = t0; t < t1; ++t) {
-    const Row r = next;
-    if (t + 1 < t1) fetch(t + 1, next);
-    const int odd = (int)(t - t0) & 1;  // two rows' sums lie apart: one barrier a sum
-    float d[N], y[N], o[N], g[N];
-    floats(r.g, d);
-    if constexpr (BLOCK) {
-      floats(r.y, y);
-      floats(r.gate, g);
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] *= r.r1;
+  u32x4 w1[CPL], w2[CPL];
+  chunks(BLOCK ? a.w1 : nullptr, 0, w1);
+  chunks(a.w2, 0, w2);
+  Row row;
+  if (t0 < t1) fetch(t0, row);
+  for (int t = t0; t < t1; ++t) {
+    Row r = row;
+    if constexpr (kAhead) {
+      if (t + 1 < t1) fetch(t + 1, row);
     }
+    const int odd = (t - t0) & 1;  // two rows' sums lie apart: one barrier a sum
+    // chunk i: y^ and the rows y^ weight' (y^ without a norm), gate
+    auto block_values = [&](int i, float(&y)[V], float(&yn)[V], float(&gate)[V]) {
+      float w[V];
+      unpack<DT>(r.y[i], y);
+      unpack<DT>(w1[i], w);
+      unpack<DT>(r.gate[i], gate);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        y[v] *= r.r1;
+        yn[v] = a.w1 ? y[v] * (w[v] + a.offset) : y[v];
+        if (!a.gate) gate[v] = 1.f;
+      }
+    };
+    // chunk i: z^ (out as the forward pass had it, or x) and grad_n next'
+    auto next_values = [&](int i, const float(&yn)[V], const float(&gate)[V], float(&z)[V], float(&gn)[V], float(&gw)[V]) {
+      float w[V];
+      unpack<DT>(r.x[i], z);
+      unpack<DT>(r.gn[i], gn);
+      unpack<DT>(w2[i], w);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (BLOCK) z[v] = a.residual * z[v] + gate[v] * yn[v];
+        z[v] *= r.r2;
+        gw[v] = gn[v] * (w[v] + a.offset);
+      }
+    };
+    float m2 = 0.f;
     if (a.gn) {
-      float gn[N];
-      floats(r.gn, gn);
-      floats(r.x, o);
-      float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (BLOCK) {  // z again, as the forward pass had it
-          float f = a.w1 ? y[i] * w1[i] : y[i];
-          if (a.gate) f *= g[i];
-          o[i] = a.residual * o[i] + f;
+      for (int i = 0; i < CPL; ++i) {
+        float y[V], yn[V], gate[V], z[V], gn[V], gw[V];
+        if constexpr (BLOCK) block_values(i, y, yn, gate);
+        next_values(i, yn, gate, z, gn, gw);
+#pragma unroll
+        for (int v = 0; v < V; ++v) m2 = __builtin_fmaf(gw[v], z[v], m2);
+      }
+      m2 = block_sum(m2, red[odd]) / (float)H;
+    }
+    float d[N], m1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      if constexpr (CPL > 1) __asm__ __volatile__("" ::: "memory");  // a chunk at a time
+      float y[V], yn[V], gate[V];
+      float* di = d + i * V;
+      if constexpr (BLOCK) block_values(i, y, yn, gate);
+      unpack<DT>(r.g[i], di);
+      if (a.gn) {
+        float z[V], gn[V], gw[V];
+        next_values(i, yn, gate, z, gn, gw);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          s2[i * V + v] += gn[v] * z[v];
+          di[v] += r.r2 * (gw[v] - z[v] * m2);
         }
-        o[i] *= r.r2;
-        s2[i] += gn[i] * o[i];
-        gn[i] *= w2[i];
-        dot += gn[i] * o[i];
       }
-      dot = block_sum(dot, red[odd]) / (float)H;
+      if constexpr (!BLOCK) {
+        if (a.gx) store(a.gx, t, i, di);
+      } else {
+        if (a.gx) {
+          float gx[V];
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] += r.r2 * (gn[i] - o[i] * dot);
-    }
-    if constexpr (!BLOCK) {
-      if (a.gx) store(a.gx, t, d);
-      continue;
-    }
-    if (a.gx) {
-      float gx[N];
+          for (int v = 0; v < V; ++v) gx[v] = a.residual * di[v];
+          store(a.gx, t, i, gx);
+        }
+        float w[V];
+        unpack<DT>(w1[i], w);
 #pragma unroll
-      for (int i = 0; i < N; ++i) gx[i] = a.residual * d[i];
-      store(a.gx, t, gx);
-    }
-    if (a.gate) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (a.gg) sg[i] += d[i] * (a.w1 ? y[i] * w1[i] : y[i]);
-        d[i] *= g[i];
+        for (int v = 0; v < V; ++v) {
+          if (a.gg) sg[i * V + v] += di[v] * yn[v];
+          if (a.gate) di[v] *= gate[v];
+          if (a.w1) {
+            s1[i * V + v] += di[v] * y[v];
+            di[v] *= w[v] + a.offset;
+            m1 = __builtin_fmaf(di[v], y[v], m1);
+          }
+        }
       }
     }
-    if (a.w1) {
-      float dot = 0.f;
+    if constexpr (BLOCK) {
+      if (a.w1) m1 = block_sum(m1, red[2 + odd]) / (float)H;
+      if (a.gy) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        s1[i] += d[i] * y[i];
-        d[i] *= w1[i];
-        dot += d[i] * y[i];
+        for (int i = 0; i < CPL; ++i) {
+          float* di = d + i * V;
+          if (a.w1) {
+            float y[V];
+            unpack<DT>(r.y[i], y);
+#pragma unroll
+            for (int v = 0; v < V; ++v) di[v] = r.r1 * (di[v] - y[v] * r.r1 * m1);
+          }
+          store(a.gy, t, i, di);
+        }
       }
-      dot = block_sum(dot, red[2 + odd]) / (float)H;
+      if (a.gg && a.parts == 1 && (t + 1) % a.group == 0) {  // the gate's last token
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = r.r1 * (d[i] - y[i] * dot);
+        for (int i = 0; i < CPL; ++i) store(a.gg, t / a.group, i, sg + i * V);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sg[i] = 0.f;
+      }
     }
-    if (a.gy) store(a.gy, t, d);
-    if (a.gg && a.parts == 1 && (t + 1) % a.group == 0) {  // the gate's last token
-      store(a.gg, t / a.group, sg);
-#pragma unroll
-      for (int i = 0; i < N; ++i) sg[i] = 0.f;
+    if constexpr (!kAhead) {
+      if (t + 1 < t1) fetch(t + 1, row);
     }
   }
-  if (a.part1) partial(a.part1, run, s1);
-  if (a.part2) partial(a.part2, run, s2);
-  if (a.gg && a.parts > 1) partial(a.partg, run, sg);
+  if (a.part1) partial(a.part1, s1);
+  if (a.part2) partial(a.part2, s2);
+  if (a.gg && a.parts > 1) partial(a.partg, sg);
 }
 
 // Adds partials: blockIdx.y 0 the next norm's weight, 1 the post-norm's, 2.. the gates.
@@ -457,12 +494,13 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormBwdArgs a) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(to) + row * H + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
-int chunks_per_lane(int nch) { return nch <= 512 ? 1 : nch <= 1024 ? 2 : 4; }
 int threads(int nch, int cpl) { return ((nch + cpl - 1) / cpl + kWave - 1) / kWave * kWave; }
 
 template <int DT, int SRC>
 hipError_t launch_norm_typed(const NormArgs& a, hipStream_t s) {
-  const int cpl = chunks_per_lane(a.nch), n = threads(a.nch, cpl);
+  // two chunks a lane: fewer waves meet at a row's sums (4096 x 2048 bfloat16: 16.5 us, one
+  // a lane 18.9, four 16.9; 8192 x 2816 with its combine: 100, 125, 201)
+  const int cpl = a.nch <= kWave ? 1 : a.nch <= 1024 ? 2 : 4, n = threads(a.nch, cpl);
   if (cpl == 1) norm_kernel<DT, 1, SRC><<<a.T, n, 0, s>>>(a);
   else if (cpl == 2) norm_kernel<DT, 2, SRC><<<a.T, n, 0, s>>>(a);
   else norm_kernel<DT, 4, SRC><<<a.T, n, 0, s>>>(a);
@@ -471,11 +509,11 @@ hipError_t launch_norm_typed(const NormArgs& a, hipStream_t s) {
 
 template <int DT, bool BLOCK>
 hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
-  const int cpl = chunks_per_lane(a.nch), n = threads(a.nch, cpl);
   if (a.runs > 0) {
-    if (cpl == 1) norm_bwd_kernel<DT, 1, BLOCK><<<a.runs, n, 0, s>>>(a);
-    else if (cpl == 2) norm_bwd_kernel<DT, 2, BLOCK><<<a.runs, n, 0, s>>>(a);
-    else norm_bwd_kernel<DT, 4, BLOCK><<<a.runs, n, 0, s>>>(a);
+    if (a.nch <= 512) norm_bwd_kernel<DT, 1, BLOCK, true, 512><<<a.runs, threads(a.nch, 1), 0, s>>>(a);
+    else if (a.nch <= 1024) norm_bwd_kernel<DT, 2, BLOCK, false, 512><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
+    else if (a.nch <= 2048) norm_bwd_kernel<DT, 2, BLOCK, false, 1024><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
+    else norm_bwd_kernel<DT, 4, BLOCK, false, 1024><<<a.runs, threads(a.nch, 4), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -497,26 +535,32 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
          : src == kRows ? launch_norm_typed<kBF16, kRows>(a, s) : launch_norm_typed<kBF16, kGather>(a, s);
 }
 
-hipError_t launch_quant(const NormArgs& a, hipStream_t s) {
-  if (a.nch <= 4 * kWave) {
-    const unsigned grid = (unsigned)(((int64_t)a.T + 3) / 4);
-    if (a.dtype == kF32) quant_wave_kernel<kF32><<<grid, 256, 0, s>>>(a);
-    else quant_wave_kernel<kBF16><<<grid, 256, 0, s>>>(a);
-  } else {
-    const int n = a.nch >= 1024 ? 1024 : 512;
-    if (a.dtype == kF32) quant_block_kernel<kF32><<<a.T, n, 0, s>>>(a);
-    else quant_block_kernel<kBF16><<<a.T, n, 0, s>>>(a);
-  }
+template <int DT>
+hipError_t launch_quant_typed(const NormArgs& a, hipStream_t s) {
+  const int cpl = a.nch <= kWave ? 1 : a.nch <= 2 * kWave ? 2 : 4;
+  const int64_t rows = 4 * (4 / cpl);  // of a workgroup
+  const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
+  if (a.nch > 4 * kWave) quant_block_kernel<DT><<<a.T, a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
+  else if (cpl == 1) quant_wave_kernel<DT, 1><<<grid, 256, 0, s>>>(a);
+  else if (cpl == 2) quant_wave_kernel<DT, 2><<<grid, 256, 0, s>>>(a);
+  else quant_wave_kernel<DT, 4><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Rows of a run, runs that share a gate, and runs in all.
-void norm_bwd_plan(int64_t T, int64_t group, int* rows, int* parts, int* runs) {
+hipError_t launch_quant(const NormArgs& a, hipStream_t s) {
+  return a.dtype == kF32 ? launch_quant_typed<kF32>(a, s) : launch_quant_typed<kBF16>(a, s);
+}
+
+// Rows of a run, runs that share a gate, and runs in all: about 2048 waves (4096 x 2048
+// bfloat16, four waves a row: 34 us with 512 runs, 44 with 256, 36 with 1024; 7168, eight
+// waves: 110 with 256, 116 with 512).
+void norm_bwd_plan(int64_t T, int64_t group, int nch, int* rows, int* parts, int* runs) {
   if (T == 0) {
     *rows = *parts = *runs = 0;
     return;
   }
-  int64_t r = (T + 511) / 512;
+  const int waves = (nch + kWave - 1) / kWave, most = waves <= 2 ? 1024 : waves <= 4 ? 512 : 256;
+  int64_t r = (T + most - 1) / most;
   if (group >= r) {
     *parts = (int)((group + r - 1) / r);
     if (*parts == 1) r = group;
