@@ -5,22 +5,33 @@
 //   gated:     f(y[p,i]) * y[p,I+i]         formed before that rounding
 //
 // A workgroup's tile is BM rows of one expert by BN channels; both operands run
-// through LDS in steps of KC 16-byte chunks a row, loaded there directly (no
-// registers on the way) while the matrix cores work on the step before: two stages,
-// one barrier a step.  The stages are separate arrays, so that the compiler sees
-// that a stage's reads need not wait for the other's loads.  The weights are the
-// first operand of the matrix instruction: a lane then holds four neighbouring
-// channels of one row.  Chunks of a row are stored permuted (by the row's bits), so
-// that the 16 rows of an operand lie in different banks.
+// through LDS in steps of 128 bytes of each row, loaded there directly (no registers
+// on the way) into one of three stages: two steps are on their way while the matrix
+// cores work on a third, with one barrier a step.  Rows of 128 bytes, whole lines: with
+// steps of 64 bytes the address units give half the rate (17 to 22 TB/s from L2, 33 to 35
+// with 128).  The stages are separate arrays, so that the compiler sees that reads of one
+// need not wait for loads into another.  The weights are the first operand of the matrix
+// instruction: a lane then holds four neighbouring channels of one row.  A row's chunks
+// are stored permuted (by the row's bits), so that the 16 rows of an operand lie in
+// different banks: no bank conflict is counted.
+//
+// Workgroups stay and take tile after tile: a tile's first loads are asked for before the
+// tile before it is scaled and written, and its rows' tokens while that one is summed.
+// An expert of n rows has ceil(n / BM) tiles of equal size; a tile leaves out the
+// products of 16-row parts that it has no rows for.  The tiles are found from the experts'
+// offsets on the device: the host knows only how many there can be.
 //
 // Rows past an expert's last and chunks past a row's end have an offset outside the
-// buffer: the hardware reads nothing and puts zeros into LDS.
+// buffer: the hardware reads nothing and puts zeros into LDS.  A tile starts its sum at a
+// step of its own, so that workgroups do not all ask for the same part of their rows at
+// the same time.
 //
-// Tiles: an expert of n rows has ceil(n / BM), of equal size; the tile of a
-// workgroup is found from the experts' offsets on the device (the host knows only
-// how many there can be).  Each XCD takes a run of tiles, the rows' tiles of the
-// same channels one after the other, so that weights are read from HBM once and
-// found in that XCD's L2 by the others.
+// Measured (MI355X): one projection of 4096 rows, 7168 x 4096, gated: 107 us, 2.2 POP/s,
+// half of what the matrix cores could do (a library's product of two 8192 x 8192 int8
+// matrices reaches 2.4); the loads alone take 77 us, the products alone 57.  4096 tokens of
+// 8 of 128 experts, 2048 x 1536, gated: 165 us; loads alone 128 (570 MB pass through the
+// L2s, 403 of them weights), products alone 70.  64 tokens there: 73 us, 5.5 TB/s of
+// weights, which is what memory gives.
 #include "device_common.h"
 #include "internal.h"
 #include "mfma.h"
@@ -40,7 +51,12 @@ struct Tile {
   int e, row, rows, col;  // expert, first receive row, rows (0: no such tile), channel tile
 };
 
-// The tiles of a call, numbered by expert, channel tile and row tile, the last fastest.
+// The tiles of a call, numbered by expert, band of kBand row tiles, channel tile and row
+// tile, the last fastest: what an XCD works on at a time is about as high as wide, and
+// reads fewer rows and weights into its L2 than a column of tiles would (4096 rows of
+// 7168 x 4096: 107 us, in columns 110).
+constexpr int kBand = 8;
+
 struct Tiles {
   const int* before;  // [E+1] in LDS: row tiles of the experts before each
   const int* first;   // [E+1] in LDS: first receive row of each
@@ -56,9 +72,11 @@ struct Tiles {
     e = __builtin_amdgcn_readfirstlane(min(e, E - 1));
     const int b = __builtin_amdgcn_readfirstlane(before[e]), tiles = __builtin_amdgcn_readfirstlane(before[e + 1]) - b;
     const int row = __builtin_amdgcn_readfirstlane(first[e]), n = __builtin_amdgcn_readfirstlane(first[e + 1]) - row;
-    const int r = (int)(id - (uint32_t)b * cols), m = r % tiles;
+    const int r = (int)(id - (uint32_t)b * cols);
     const int step = ((n + tiles - 1) / tiles + 15) & ~15;  // rows of a tile
-    return {e, row + m * step, min(step, n - m * step), r / tiles};
+    const int band = r / (kBand * cols), high = min(kBand, tiles - band * kBand), s = r - band * kBand * cols;
+    const int m = band * kBand + s % high;
+    return {e, row + m * step, min(step, n - m * step), s / high};
   }
 };
 
@@ -452,9 +470,14 @@ hipError_t launch_tile(const I8Args& a, hipStream_t s) {
 
 }  // namespace
 
-// Tiles of 128 x 256, one workgroup a CU, where there are enough of them (rows of 2 KiB
-// and wider hide a tile's beginning and end better, so fewer will do); else of 64 x 128,
-// two workgroups a CU; else of 64 x 64.
+// Tiles of 128 x 256, one workgroup a CU, where there are enough of them; else of 64 x
+// 128, two workgroups a CU; else of 64 x 64.  Rows of 2 KiB and more hide a tile's
+// beginning and end better, so fewer large ones will do.  In us, large / middle / small:
+//   64 tokens of 8 of 128 experts, 2048 x 1536 (792 large tiles at most): 73 / 73 / 77
+//   1500 rows, 7168 x 4096 (192): 51 / 58 / 81;   1024 rows (128): 48 / 38 / 52
+//   2000 tokens of 2 of 8, 1024 x 2048 (312): 27 / 23 / 26
+//   4096 rows, 768 x 1024 (128; 512 of the middle size): 12.5 / 10 / 12.4
+//   64 tokens of 2 of 8, 4096 x 2048 (72; 160): 21 / 18 / 14;   1 token of 8 of 128: 14 / 12 / 9
 hipError_t launch_i8(const I8Args& a, hipStream_t s) {
   if (most_tiles(a, 128, 256) >= (a.kch >= 128 ? 192 : 400)) return launch_tile<4, 4, 2, 4, 8, 3, 2>(a, s);
   if (most_tiles(a, 64, 128) >= 256) return launch_tile<2, 4, 2, 2, 8, 3, 2>(a, s);
