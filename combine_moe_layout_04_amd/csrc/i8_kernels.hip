@@ -44,6 +44,9 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// The wait for all but the last n of a wave's memory operations, and all of its LDS ones.
+constexpr int wait_for(int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); }
+
 constexpr int kMaxExperts = 1024;           // MOE_MAX_E
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer
 
@@ -198,30 +201,38 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
   Tile t = tile_at(id);
   if (t.rows == 0) return;  // uniform over the workgroup
 
-  // tokens of the tile's rows that this lane loads (-1: none)
-  auto tokens_of = [&](const Tile& x, int(&token)[kLoadsA]) __attribute__((always_inline)) {
+  // What a tile's rows are made of: rows of q (-1: none) for this lane's loads, and for its
+  // results' scales.
+  struct Rows {
+    int load[kLoadsA], scale[MB];
+  };
+  auto rows_of = [&](const Tile& x, Rows& to) __attribute__((always_inline)) {
+    auto one = [&](int r) __attribute__((always_inline)) {
+      if (r >= x.rows) return -1;
+      return a.recv_token ? a.recv_token[x.row + r] : x.row + r;
+    };
 #pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-      const int r = i * kWaves * kRowsPer + mine;
-      token[i] = -1;
-      if (r < x.rows) token[i] = a.recv_token ? a.recv_token[x.row + r] : r;
-    }
+    for (int i = 0; i < kLoadsA; ++i) to.load[i] = one(i * kWaves * kRowsPer + mine);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) to.scale[i] = one((i * WM + wm) * 16 + (lane & 15));
   };
   uint32_t offa[kLoadsA], offb[kLoadsB];
   __amdgpu_buffer_rsrc_t rq, rw;
   int begin = 0;
-  auto aim = [&](const Tile& x, const int(&token)[kLoadsA]) __attribute__((always_inline)) {
+  auto aim = [&](const Tile& x, const Rows& rows) __attribute__((always_inline)) {
     // rows of q: the tile's own, or any
-    const int64_t qrows = a.recv_token ? a.M : x.rows;
-    const int64_t qbase = a.recv_token ? 0 : (int64_t)x.row * width;
+    const int first_row = a.recv_token ? 0 : x.row;
+    const int64_t qrows = a.recv_token ? a.M : x.rows, qbase = first_row * width;
     rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q) + qbase, 0, (int)(uint32_t)(qrows * width), 0x00027000);
     const int n0 = x.col * (GATED ? BN / 2 : BN);
     const int64_t wbase = ((int64_t)x.e * a.N + n0) * width;
     rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.w) + wbase, 0, (int)(uint32_t)((a.N - n0) * width),
                                            0x00027000);
 #pragma unroll
-    for (int i = 0; i < kLoadsA; ++i)
-      offa[i] = (uint32_t)token[i] < (uint32_t)qrows ? (uint32_t)(token[i] * width) + chunk * 16 : kNowhere;
+    for (int i = 0; i < kLoadsA; ++i) {
+      const int row = rows.load[i] - first_row;  // negative: none
+      offa[i] = (uint32_t)row < (uint32_t)qrows ? (uint32_t)(row * width) + chunk * 16 : kNowhere;
+    }
 #pragma unroll
     for (int i = 0; i < kLoadsB; ++i) {
       const int r = i * kWaves * kRowsPer + mine;
@@ -269,6 +280,10 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
     if constexpr (STAGES > 2) loads(s1, 1, s0, every);
     if constexpr (STAGES > 3) loads(s2, 2, s0, every);
   };
+  using Ch = Channels<DT, GATED, NB>;
+  constexpr int kOuts = GATED ? NB / 2 : NB;  // results of a wave in a row tile
+  constexpr int kStores = MB * (Ch::kPaired ? kOuts / 2 : kOuts);  // of a wave, for a whole tile
+  int stored = 0;  // stores that the tile before ended with, at least
   i32x4 acc[MB][NB];
   // the sums, of the first B row tiles of each wave
   auto sums = [&](auto B) __attribute__((always_inline)) {
@@ -276,7 +291,11 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
     auto work = [&](auto I, int s) __attribute__((always_inline)) {
       constexpr int kFlying = (STAGES - 2) * (kLoadsA + kLoadsB);  // loads that may still be on their way
       __asm__ __volatile__("" ::: "memory");  // the barrier alone does not keep LDS reads on their side of it
-      __builtin_amdgcn_s_waitcnt((kFlying & 15) | (7 << 4) | ((kFlying >> 4) << 14));  // and no LDS read
+      // memory operations complete in their order: the stores of the tile before came after
+      // this one's first loads, and need not be waited for with them
+      if (s < STAGES - 1 && stored == kStores) __builtin_amdgcn_s_waitcnt(wait_for(kFlying + kStores));
+      else if (s < STAGES - 1 && stored >= kStores / 2) __builtin_amdgcn_s_waitcnt(wait_for(kFlying + kStores / 2));
+      else __builtin_amdgcn_s_waitcnt(wait_for(kFlying));
       __builtin_amdgcn_s_barrier();
       __asm__ __volatile__("" ::: "memory");
       constexpr std::integral_constant<int, (I + STAGES - 1) % STAGES> before_it;
@@ -323,43 +342,33 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
   };
 
   // lane: row l % 16 of a row tile
-  using Ch = Channels<DT, GATED, NB>;
-  constexpr int kOuts = GATED ? NB / 2 : NB;  // results of a wave in a row tile
   const int g = lane >> 4;
-  float sw[NB][4], sq[MB];
-  auto scales_of = [&](const Tile& x) __attribute__((always_inline)) {
+  struct Scales {
+    f32x4 w[NB];
+    float q[MB];
+  };
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  auto scales_of = [&](const Tile& x, const Rows& rows, Scales& to) __attribute__((always_inline)) {
     const int n0 = x.col * (GATED ? BN / 2 : BN);
 #pragma unroll
-    for (int j = 0; j < kOuts; ++j) {
-      const int n = n0 + Ch::of_result(wn * kOuts + j, g);
-      const float* p = a.ws + (int64_t)x.e * a.N + n;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if constexpr (GATED) {
-          sw[2 * j][v] = n < N ? p[v] : 0.f;
-          sw[2 * j + 1][v] = n < N ? p[N + v] : 0.f;
-        } else {
-          sw[j][v] = n < N ? p[v] : 0.f;
-        }
-      }
+    for (int j = 0; j < NB; ++j) {
+      const int n = n0 + Ch::of_result(wn * kOuts + (GATED ? j / 2 : j), g);
+      const float* p = a.ws + (int64_t)x.e * a.N + n + (GATED && (j & 1) ? N : 0);
+      to.w[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (n < N) to.w[j] = *reinterpret_cast<const f32x4_any*>(p);
     }
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int r = (i * WM + wm) * 16 + (lane & 15);
-      int source = x.row + r;
-      if (r < x.rows && a.recv_token) source = a.recv_token[source];
-      sq[i] = r < x.rows && (unsigned)source < (unsigned)a.M ? a.qs[source] : 0.f;
-    }
+    for (int i = 0; i < MB; ++i) to.q[i] = (uint32_t)rows.scale[i] < (uint32_t)a.M ? a.qs[rows.scale[i]] : 0.f;
   };
-  int token[kLoadsA];
-  tokens_of(t, token);
-  aim(t, token);
+  Rows rows;
+  Scales now, then;
+  rows_of(t, rows);
+  aim(t, rows);
+  scales_of(t, rows, now);
+  Tile next = tile_at(id += stride);
+  rows_of(next, rows);
   start();
-  scales_of(t);
   for (;;) {
-    id += stride;
-    const Tile next = tile_at(id);
-    tokens_of(next, token);  // they arrive while this tile is worked on
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -384,13 +393,20 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
       else if (tiles == 8 && MB > 8) sums(std::integral_constant<int, 8>{});
       else sums(std::integral_constant<int, MB>{});
     }
+    __asm__ __volatile__("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_for(0));  // nothing on its way to a stage, or from one
+    Tile after = {0, 0, 0, 0};
     if (next.rows != 0) {  // its first loads run while this tile is written
-      __asm__ __volatile__("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(7 << 4);  // nothing on its way to a stage, or from one
       __builtin_amdgcn_s_barrier();
       __asm__ __volatile__("" ::: "memory");
-      aim(next, token);
+      aim(next, rows);
+      scales_of(next, rows, then);
+      after = tile_at(id += stride);
+      rows_of(after, rows);
+      in_order();
       start();
+      __asm__ __volatile__("" ::: "memory");  // the stores below come after these loads
+      in_order();
     }
     const int n0 = t.col * (GATED ? BN / 2 : BN);
 #pragma unroll
@@ -404,10 +420,10 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           if constexpr (GATED)
-            y[j][v] = activate((float)acc[i][2 * j][v] * sq[i] * sw[2 * j][v], a.act) *
-                      ((float)acc[i][2 * j + 1][v] * sq[i] * sw[2 * j + 1][v]);
+            y[j][v] = activate((float)acc[i][2 * j][v] * now.q[i] * now.w[2 * j][v], a.act) *
+                      ((float)acc[i][2 * j + 1][v] * now.q[i] * now.w[2 * j + 1][v]);
           else
-            y[j][v] = (float)acc[i][j][v] * sq[i] * sw[j][v];
+            y[j][v] = (float)acc[i][j][v] * now.q[i] * now.w[j][v];
         }
       if constexpr (DT == kF32) {
         float* out = static_cast<float*>(a.out) + p * N;
@@ -438,8 +454,12 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
       }
     }
     if (next.rows == 0) return;
+    // row tiles of this wave with a row, where every channel is there
+    const int with_rows = min(MB, max(0, (t.rows - wm * 16 + 16 * WM - 1) / (16 * WM)));
+    stored = n0 + (GATED ? BN / 2 : BN) <= N ? with_rows * (kStores / MB) : 0;
     t = next;
-    scales_of(t);
+    next = after;
+    now = then;
   }
 }
 
