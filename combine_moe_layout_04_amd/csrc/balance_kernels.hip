@@ -71,7 +71,8 @@ __device__ __forceinline__ int sequences_before(const BalanceArgs& a, int t) {
 
 // One token's softmax, its lse, its scores (p is soft itself for softmax) and, for
 // sigmoids, 1 - sigmoid in rest.  The fast exponential is off by (|x| + 2) u of itself
-// (u = 2^-24), which the terms of far smaller logits alone have much of.
+// (u = 2^-24), which the terms of far smaller logits alone have much of, the reciprocal by
+// 2 u and the logarithm of up to 1024 terms by 16 u.
 template <int VPL, bool SIG>
 __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL], float (&p)[VPL], float (&rest)[VPL],
                                        float& lse) {
@@ -87,8 +88,8 @@ __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL]
     sum += soft[v];
   }
   sum = wave_sum(sum);
-  lse = sum == 0.f ? 0.f : m + logf(sum);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  lse = sum == 0.f ? 0.f : m + __logf(sum);
+  const float inv = sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
   if constexpr (SIG) {
     float all = 0.f;
 #pragma unroll
@@ -102,7 +103,7 @@ __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL]
       all += p[v];
     }
     all = wave_sum(all);
-    const float share = all == 0.f ? 0.f : 1.f / all;
+    const float share = all == 0.f ? 0.f : __builtin_amdgcn_rcpf(all);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) p[v] *= share;
   }
@@ -153,6 +154,16 @@ __global__ __launch_bounds__(run_waves(VPL) * kWave) void balance_kernel(Balance
       load_token<DT, VPL>(a, lo + wave, next);
       there_next = counted(a, lo + wave);
     }
+    // this thread's first pair, on its way during the tokens (-1: none)
+    const int pairs = (hi - lo) * a.K;  // at most tile * K
+    auto expert_of = [&](int i) -> int {
+      if (!counted(a, lo + i / a.K)) return -1;
+      const size_t at = (size_t)lo * a.K + i;
+      const int64_t e = a.itype == MOE_I32 ? (int64_t) static_cast<const int32_t*>(a.idx)[at]
+                                           : static_cast<const int64_t*>(a.idx)[at];
+      return e >= 0 && e < a.E ? (int)e : -1;
+    };
+    const int pair = (int)threadIdx.x < pairs ? expert_of(threadIdx.x) : -1;
     for (int t = lo + wave; t < hi; t += kWaves) {  // wave-uniform
 #pragma unroll
       for (int v = 0; v < VPL; ++v) z[v] = next[v];
@@ -169,14 +180,10 @@ __global__ __launch_bounds__(run_waves(VPL) * kWave) void balance_kernel(Balance
       zz += lse * lse;
       ++n;
     }
-    const int pairs = (hi - lo) * a.K;  // at most tile * K
-    for (int i = threadIdx.x; i < pairs; i += kWaves * kWave) {
-      const int t = lo + i / a.K;
-      if (!counted(a, t)) continue;
-      const size_t at = (size_t)lo * a.K + i;
-      const int64_t e = a.itype == MOE_I32 ? (int64_t) static_cast<const int32_t*>(a.idx)[at]
-                                           : static_cast<const int64_t*>(a.idx)[at];
-      if (e >= 0 && e < a.E) atomicAdd(&hist[(int)e], 1);
+    if (pair >= 0) atomicAdd(&hist[pair], 1);
+    for (int i = threadIdx.x + kWaves * kWave; i < pairs; i += kWaves * kWave) {
+      const int e = expert_of(i);
+      if (e >= 0) atomicAdd(&hist[e], 1);
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) psum[wave][lane + kWave * v] = p[v];
@@ -306,21 +313,43 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
   const int64_t first = ((int64_t)blockIdx.x * kWaves + threadIdx.x / kWave) * a.tile;  // tile: tokens of a wave
   const int t0 = (int)min((int64_t)a.T, first), t1 = (int)min((int64_t)a.T, first + a.tile);
   if (t0 >= t1) return;
-  int all = 0, some = 0;
-  for (int q = lane; q < a.S; q += kWave) {
-    const int n = a.tokens[q];
-    all += n;
-    some += n > 0;
-  }
-  all = read_lane_i((int)wave_scan((uint32_t)all), 63);
-  some = read_lane_i((int)wave_scan((uint32_t)some), 63);
-  const float g0 = a.grad_loss[0], g1 = all > 0 ? a.grad_loss[1] * (float)(2.0 / all) : 0.f;
-  int q = sequences_before(a, t0), at = -1;
-  int begin = q < a.S ? seq_begin(a, q) : a.T, end = q < a.S ? seq_end(a, q) : a.T;
-  float c[VPL];  // the gradient of P of the sequence `at`
+  // everything a wave begins with is asked for before any of it is used
   float z[VPL], next[VPL];
   load_token<DT, VPL>(a, t0, next);
   bool there, there_next = counted(a, t0);
+  const float given0 = a.grad_loss[0], given1 = a.grad_loss[1];
+  int q = sequences_before(a, t0);
+  int begin, end, count[VPL];
+  float n;
+  auto enter = [&](int s) {  // sequence s
+    const bool in = s < a.S;
+    begin = in ? seq_begin(a, s) : a.T;
+    end = in ? seq_end(a, s) : a.T;
+    n = in ? (float)a.tokens[s] : 0.f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = lane + kWave * v;
+      count[v] = in && e < a.E ? a.counts[(size_t)s * a.E + e] : 0;
+    }
+  };
+  enter(q);
+  int all = 0, some = 0;
+  for (int s = lane; s < a.S; s += kWave) {
+    const int m = a.tokens[s];
+    all += m;
+    some += m > 0;
+  }
+  all = read_lane_i((int)wave_scan((uint32_t)all), 63);
+  some = read_lane_i((int)wave_scan((uint32_t)some), 63);
+  const float g0 = given0, g1 = all > 0 ? given1 * (2.f / (float)all) : 0.f;
+  const float even = (float)a.E / ((float)a.K * (float)some);
+  float c[VPL];  // the gradient of the sequence's P
+  auto weigh = [&]() {
+    const float f = n > 0.f ? even / n / n : 0.f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) c[v] = g0 * (f * (float)count[v]);
+  };
+  weigh();
   for (int t = t0; t < t1; ++t) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) z[v] = next[v];
@@ -329,25 +358,14 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
       load_token<DT, VPL>(a, t + 1, next);
       there_next = counted(a, t + 1);
     }
-    while (q < a.S && end <= t) {
-      ++q;
-      begin = q < a.S ? seq_begin(a, q) : a.T;
-      end = q < a.S ? seq_end(a, q) : a.T;
+    if (q < a.S && end <= t) {
+      while (q < a.S && end <= t) enter(++q);
+      weigh();
     }
     float d[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) d[v] = 0.f;
     if (q < a.S && begin <= t && there) {  // wave-uniform
-      if (q != at) {
-        at = q;
-        const double n = a.tokens[q];
-        const float f = n > 0 ? (float)((double)a.E / ((double)a.K * some * n * n)) : 0.f;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          const int e = lane + kWave * v;
-          c[v] = e < a.E ? g0 * (f * (float)a.counts[(size_t)q * a.E + e]) : 0.f;
-        }
-      }
       float soft[VPL], p[VPL], rest[VPL], lse, dot = 0.f;
       scores<VPL, SIG>(z, soft, p, rest, lse);
 #pragma unroll

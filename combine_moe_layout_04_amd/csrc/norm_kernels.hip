@@ -179,7 +179,7 @@ __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
       top = max(top, abs_bits(x[i]));
     }
     if (a.q) {
-      const float s = quant_scale(block_max(top, red[6])), inv = 1.f / s;
+      const float s = quant_scale(block_max(top, red[6])), inv = quant_inverse(s);
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         const int j = tid + i * blockDim.x;
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(256) void quant_wave_kernel(NormArgs a) {
     for (int i = 0; i < CPL; ++i) unpack<DT>(c[r][i], f + i * V);
 #pragma unroll
     for (int i = 0; i < CPL * V; ++i) top = max(top, abs_bits(f[i]));
-    const float s = quant_scale(wave_max(top)), inv = 1.f / s;
+    const float s = quant_scale(wave_max(top)), inv = quant_inverse(s);
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int j = lane + i * kWave;
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(1024) void quant_block_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) top = max(top, abs_bits(f[i]));
   }
-  const float s = quant_scale(block_max(top, red)), inv = 1.f / s;
+  const float s = quant_scale(block_max(top, red)), inv = quant_inverse(s);
   for (int j = threadIdx.x; j < a.nch; j += blockDim.x) {  // the row again, from the caches
     float f[V];
     unpack<DT>(p[j], f);

@@ -2,7 +2,7 @@
 //
 //   s = amax / 127 in float32, at least 2^-126;  q = the integer nearest to x / s,
 //   ties to even.
-// The quotient is not formed: x times the rounded 1 / s is within one step of it, and
+// The quotient is not formed: x times about 1 / s is within one step of it, and
 // the remainder x - q s is exact in float32 (it is a multiple of the smaller operand's
 // last place and not larger than s), so comparing it with s / 2 settles the rounding.
 // That makes the result a function of the numbers alone, the same in every kernel.
@@ -15,10 +15,18 @@ namespace moe {
 // bits of the largest |x| (as unsigned integers they are ordered like the values, NaN above all)
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// amax / 127, rounded as a division is: the product with the rounded 1 / 127 is within one
+// place of it, its remainder is exact, and one step from there rounds right (on the CPU
+// equal to the division for every amax of the exponents tried, the ends among them).
 __device__ __forceinline__ float quant_scale(uint32_t amax_bits) {
-  const float s = __uint_as_float(amax_bits) / 127.f;
-  return s < 0x1p-126f ? 0x1p-126f : s;  // a NaN stays
+  const float m = __uint_as_float(amax_bits), q = m * (1.f / 127.f);
+  const float s = __builtin_fmaf(__builtin_fmaf(-127.f, q, m), 1.f / 127.f, q);
+  if (!(m < INFINITY)) return m;  // infinite or NaN, as it is
+  return s < 0x1p-126f ? 0x1p-126f : s;
 }
+
+// About 1 / scale: what is made with it is corrected where that matters.
+__device__ __forceinline__ float quant_inverse(float s) { return __builtin_amdgcn_rcpf(s); }
 
 // The integer (as a float) nearest to x / s: exact, for a finite row.
 __device__ __forceinline__ float quant_exact(float x, float s, float inv) {
@@ -31,7 +39,8 @@ __device__ __forceinline__ float quant_exact(float x, float s, float inv) {
 }
 
 // Values of one 16-byte chunk of a row (4 float32, 8 bfloat16) as its 4 or 8 bytes.
-// |x / s| is at most 127 (1 + 2^-23), so x * inv is within 2^-15 of it: only where that
+// |x / s| is at most 127 (1 + 2^-23) and inv off by 2^-23 of itself, so x * inv is within
+// 2^-15 of it: only where that
 // lies nearer than 2^-14 to a half can its rounding be another than the quotient's.  A
 // row with an infinity or NaN has that as its scale, and zeros: what is made of it is
 // NaN.
