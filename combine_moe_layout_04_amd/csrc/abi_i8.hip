@@ -9,7 +9,7 @@ int moe_quant_rows(const void* x, int dtype, int64_t rows, int64_t width, int8_t
   if (rows < 0) return MOE_ERR_INVALID_ARG;
   if (width < 1 || width % 16 != 0) return MOE_ERR_SHAPE;
   const int eb = moe::elem_bytes(dtype);
-  if (eb == 0 || width > MOE_MAX_I8_WIDTH || rows > (int64_t(1) << 26)) return MOE_ERR_UNSUPPORTED;
+  if (eb == 0 || width > MOE_MAX_I8_WIDTH || rows > (int64_t(1) << 26) - 4) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;  // nothing to read or write; empty arrays may be NULL
   if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned(x, 16) || !moe::aligned(q, 16) || !moe::aligned(scale, 4)) return MOE_ERR_ALIGNMENT;

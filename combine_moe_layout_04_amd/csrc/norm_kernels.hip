@@ -82,11 +82,18 @@ __device__ float block_rstd(const float (&f)[N], int H, float eps, float* red, f
 
 enum : int { kBefore = 0, kRows = 1, kGather = 2 };  // where y comes from
 
+// A workgroup for each of `rows` rows: a dimension of a grid has fewer than 2^32 threads, so
+// from kAcross rows on they go down a second one.
+constexpr int kAcross = 1 << 20;
+dim3 row_grid(int rows) { return dim3(rows < kAcross ? rows : kAcross, (rows + kAcross - 1) / kAcross); }
+__device__ __forceinline__ int row_of_block() { return blockIdx.y * kAcross + blockIdx.x; }
+
 template <int DT, int CPL, int SRC>
 __global__ __launch_bounds__(Block<CPL>::kMax) void norm_kernel(NormArgs a) {
   constexpr int V = Elems<DT>::kPerChunk;
   __shared__ float red[7][kMaxWaves];
-  const int t = blockIdx.x, tid = threadIdx.x, H = a.nch * V;
+  const int t = row_of_block(), tid = threadIdx.x, H = a.nch * V;
+  if (t >= a.T) return;  // uniform
   const size_t row = (size_t)t * a.nch;
   float f[CPL * V], x[CPL * V];
   u32x4 c[CPL];
@@ -239,7 +246,8 @@ template <int DT>
 __global__ __launch_bounds__(1024) void quant_block_kernel(NormArgs a) {
   constexpr int V = Elems<DT>::kPerChunk;
   __shared__ float red[kMaxWaves];
-  const size_t t = blockIdx.x;
+  const size_t t = row_of_block();
+  if (t >= (size_t)a.T) return;  // uniform
   const u32x4* p = static_cast<const u32x4*>(a.x) + t * a.nch;
   uint32_t top = 0;
   for (int j = threadIdx.x; j < a.nch; j += blockDim.x) {
@@ -501,9 +509,9 @@ hipError_t launch_norm_typed(const NormArgs& a, hipStream_t s) {
   // two chunks a lane: fewer waves meet at a row's sums (4096 x 2048 bfloat16: 16.5 us, one
   // a lane 18.9, four 16.9; 8192 x 2816 with its combine: 100, 125, 201)
   const int cpl = a.nch <= kWave ? 1 : a.nch <= 1024 ? 2 : 4, n = threads(a.nch, cpl);
-  if (cpl == 1) norm_kernel<DT, 1, SRC><<<a.T, n, 0, s>>>(a);
-  else if (cpl == 2) norm_kernel<DT, 2, SRC><<<a.T, n, 0, s>>>(a);
-  else norm_kernel<DT, 4, SRC><<<a.T, n, 0, s>>>(a);
+  if (cpl == 1) norm_kernel<DT, 1, SRC><<<row_grid(a.T), n, 0, s>>>(a);
+  else if (cpl == 2) norm_kernel<DT, 2, SRC><<<row_grid(a.T), n, 0, s>>>(a);
+  else norm_kernel<DT, 4, SRC><<<row_grid(a.T), n, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -540,7 +548,7 @@ hipError_t launch_quant_typed(const NormArgs& a, hipStream_t s) {
   const int cpl = a.nch <= kWave ? 1 : a.nch <= 2 * kWave ? 2 : 4;
   const int64_t rows = 4 * (4 / cpl);  // of a workgroup
   const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
-  if (a.nch > 4 * kWave) quant_block_kernel<DT><<<a.T, a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
+  if (a.nch > 4 * kWave) quant_block_kernel<DT><<<row_grid(a.T), a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
   else if (cpl == 1) quant_wave_kernel<DT, 1><<<grid, 256, 0, s>>>(a);
   else if (cpl == 2) quant_wave_kernel<DT, 2><<<grid, 256, 0, s>>>(a);
   else quant_wave_kernel<DT, 4><<<grid, 256, 0, s>>>(a);

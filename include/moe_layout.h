@@ -532,7 +532,8 @@ int moe_lowrank_bwd(moe_handle_t h, const void* grad_out, int dtype, int64_t H, 
  * with it are NaN.  x [rows,width] dtype, q [rows,width] int8, 16-byte aligned;
  * scale [rows] float32.  Weights are laid out the same way: a bank [E,N,width] is
  * E*N rows.  MOE_ERR_SHAPE unless width is a multiple of 16, MOE_ERR_UNSUPPORTED
- * above MOE_MAX_I8_WIDTH (where 32-bit sums could overflow) and above 2^26 rows.
+ * above MOE_MAX_I8_WIDTH (where 32-bit sums could overflow) and for more than
+ * 2^26 - 4 rows.
  *
  * moe_matmul_i8: with acc the exact integer sum, for the receive rows p of the
  * experts first_expert .. first_expert + num_experts - 1 of the layout,
@@ -578,7 +579,7 @@ int moe_matmul_i8(moe_handle_t h, const int8_t* q, const float* scale, int64_t r
  *   at most MOE_MAX_NORM_BYTES; out may be x (and y without a handle), n neither;
  *   rstd float32 or NULL: 1 / sqrt(mean + eps), [T] of x for moe_prenorm, [T,2]
  *   (8-byte aligned) of y and z for moe_postnorm (1 where there is no norm), what the
- *   backward passes take.  eps > 0.  T = 0 is valid.                              */
+ *   backward passes take.  eps > 0.  T = 0 is valid; MOE_ERR_UNSUPPORTED above 2^26. */
 #define MOE_MAX_NORM_BYTES 65536
 int moe_prenorm(const void* x, int dtype, int64_t T, int64_t H, const void* weight, float offset, float eps, void* n,
                 int8_t* q, float* scale, float* rstd, hipStream_t stream);

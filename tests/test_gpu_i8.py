@@ -241,6 +241,27 @@ def test_weights_and_rows_past_32_bit_offsets():
     assert (out[:-4:4001] == 0).all()
 
 
+def test_many_wide_rows():
+    """2^23 rows that take a workgroup of 512 threads each: more than one dimension of a grid holds."""
+    rows, width = (1 << 23) + 5, 1040
+    x = torch.zeros(rows, width, device=DEV)
+    tail = torch.randn(3, width, generator=torch.Generator().manual_seed(1)).to(DEV)
+    at = torch.tensor([0, (1 << 22) + 1, rows - 1], device=DEV)
+    x[at] = tail
+    q, s = M.moe_quant_rows(x)
+    rq, rs = exact_quant(tail)
+    assert torch.equal(q[at].cpu(), rq) and torch.equal(s[at].cpu(), rs)
+    s[at] = 2.0 ** -126
+    assert (s == 2.0 ** -126).all()
+    # the most rows at all, several of them a wave
+    rows = (1 << 26) - 4
+    del x, q, s
+    x = torch.zeros(rows, 16, dtype=BF16, device=DEV)
+    x[-1] = torch.arange(16)
+    q, s = M.moe_quant_rows(x)
+    assert torch.equal(q[-1].cpu(), exact_quant(x[-1:])[0][0]) and (q[:-1:100003] == 0).all() and (s[:-1] == 2.0 ** -126).all()
+
+
 def test_results_repeat_and_an_empty_batch():
     idx, h = routed(500, 4, 16, 1)
     q, s = rows8(500, 304, 1)

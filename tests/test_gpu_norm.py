@@ -338,6 +338,21 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(got[0][-3:], ref[0]) and torch.equal(got[1][-3:], ref[1])
 
 
+def test_the_most_rows():
+    """2^26 rows of one chunk: more workgroups than one dimension of a grid holds threads for."""
+    T = 1 << 26
+    x = torch.zeros(T, 8, dtype=BF16, device=DEV)
+    d = make(3, 8, BF16, 2)
+    at = torch.tensor([0, (1 << 25) + 1, T - 1], device=DEV)
+    x[at] = d["x"]
+    n, rstd = M.moe_prenorm(x, d["next_weight"])
+    one, r1 = M.moe_prenorm(d["x"], d["next_weight"])
+    assert torch.equal(n[at], one) and torch.equal(rstd[at], r1) and int((n != 0).any(1).sum()) == 3
+    gx, gw = M.moe_prenorm_bwd(x, x, rstd, d["next_weight"])
+    g1, w1 = M.moe_prenorm_bwd(d["x"], d["x"], r1, d["next_weight"])
+    assert torch.equal(gx[at], g1) and torch.allclose(gw.float(), w1.float(), rtol=2 ** -7)
+
+
 def test_refusals():
     d = make(12, 64, F32, 1, 3)
     kw = dict(x=d["x"], y=d["y"], weight=d["weight"], gate=d["gate"], next_weight=d["next_weight"])

@@ -16,7 +16,7 @@ GOOD = dict(h=None, q=FAKE, scale=FAKE, rows=3, width=32, tokens=0, w=FAKE, w_sc
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), "MOE_ERR_INVALID_ARG"), (dict(width=0), "MOE_ERR_SHAPE"), (dict(width=24), "MOE_ERR_SHAPE"),
     (dict(dtype=2), "MOE_ERR_UNSUPPORTED"), (dict(width=131072), "MOE_ERR_UNSUPPORTED"),
-    (dict(rows=(1 << 26) + 1), "MOE_ERR_UNSUPPORTED"), (dict(x=None), "MOE_ERR_INVALID_ARG"),
+    (dict(rows=(1 << 26) - 3), "MOE_ERR_UNSUPPORTED"), (dict(x=None), "MOE_ERR_INVALID_ARG"),
     (dict(q=None), "MOE_ERR_INVALID_ARG"), (dict(scale=None), "MOE_ERR_INVALID_ARG"),
     (dict(x=FAKE + 8), "MOE_ERR_ALIGNMENT"), (dict(q=FAKE + 8), "MOE_ERR_ALIGNMENT"),
     (dict(scale=FAKE + 2), "MOE_ERR_ALIGNMENT")])
