@@ -16,6 +16,7 @@ from ._lib import MoeRouteOptions, MoeTuning, lib
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_I32, MOE_I64 = 0, 1
+MOE_NORM_WIDE = 8192
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 FEW_MAX_PAIRS = 512
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -1037,7 +1038,8 @@ def moe_postnorm_bwd(grad_out: Optional[torch.Tensor], grad_n: Optional[torch.Te
     grad_gate = _gradient(grad_gate, "grad_gate", gate, dev, gate is not None)
     grad_next_weight = _gradient(grad_next_weight, "grad_next_weight", next_weight, dev, next_weight is not None)
     sums = grad_weight is not None or grad_gate is not None or grad_next_weight is not None
-    workspace = _norm_workspace(workspace, x, T, H, gates, sums)
+    wide = H > MOE_NORM_WIDE  # in two kernels, which meet in the workspace
+    workspace = _norm_workspace(workspace, x, T, H, gates, sums or wide)
     _run(dev, "moe_postnorm_bwd", _ptr(grad_out), _ptr(grad_n), x.data_ptr(), _ptr(y), dt, T, H, rstd.data_ptr(),
          _ptr(weight), _ptr(gate), gates, residual_scale, _ptr(next_weight), offset, _ptr(grad_x), _ptr(grad_y),
          _ptr(grad_weight), _ptr(grad_gate), _ptr(grad_next_weight), _ptr(workspace), _bytes(workspace))

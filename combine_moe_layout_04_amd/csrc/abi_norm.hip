@@ -7,6 +7,8 @@
 
 namespace {
 
+static_assert(moe::kNormWide == MOE_NORM_WIDE, "one limit");
+
 int check_norm(int dtype, int64_t T, int64_t H) {
   if (T < 0) return MOE_ERR_INVALID_ARG;
   if (H < 1) return MOE_ERR_SHAPE;
@@ -30,19 +32,23 @@ bool all_aligned(size_t n, P... p) {
   return (moe::aligned(p, n) && ...);
 }
 
-moe::NormBwdArgs bwd_args(int dtype, int64_t T, int64_t H, int64_t gates) {
+moe::NormBwdArgs bwd_args(int dtype, int64_t T, int64_t H, int64_t gates, bool block) {
   moe::NormBwdArgs a{};
+  a.block = block;
   a.T = (int)T;
   a.nch = (int)(H * moe::elem_bytes(dtype) / 16);
   a.gates = (int)gates;
   a.group = (int)(T > 0 ? T / gates : 1);
   a.dtype = dtype;
-  moe::norm_bwd_plan(T, a.group, a.nch, &a.rows, &a.parts, &a.runs);
+  moe::norm_bwd_plan(T, a.group, a.nch, block && H > moe::kNormWide, &a.rows, &a.parts, &a.runs);
   return a;
 }
 
 // Partials of one kind of sum over tokens.
 size_t part_bytes(const moe::NormBwdArgs& a, int64_t H) { return (size_t)a.runs * H * sizeof(float); }
+
+// A wide row's means.
+size_t means_bytes(int64_t T, int64_t H) { return H > moe::kNormWide ? (size_t)T * 2 * sizeof(float) : 0; }
 
 }  // namespace
 
@@ -127,7 +133,9 @@ int moe_norm_bwd_workspace_size(int dtype, int64_t T, int64_t H, int64_t gates, 
   if (st != MOE_OK) return st;
   const int gs = check_gates(T, gates);
   if (gs != MOE_OK) return gs;
-  *bytes = 3 * part_bytes(bwd_args(dtype, T, H, gates > 0 ? gates : 1), H);
+  const size_t before = part_bytes(bwd_args(dtype, T, H, 1, false), H);
+  const size_t after = 3 * part_bytes(bwd_args(dtype, T, H, gates > 0 ? gates : 1, true), H) + means_bytes(T, H);
+  *bytes = before > after ? before : after;
   return MOE_OK;
 }
 
@@ -140,7 +148,7 @@ int moe_prenorm_bwd(const void* grad_n, const void* x, int dtype, int64_t T, int
   if (T > 0 && (!grad_n || !x || !weight || !rstd || (grad_weight && !workspace))) return MOE_ERR_INVALID_ARG;
   if (!all_aligned(16, grad_n, x, weight, grad_base, grad_x, grad_weight, workspace) || !all_aligned(4, rstd))
     return MOE_ERR_ALIGNMENT;
-  moe::NormBwdArgs a = bwd_args(dtype, T, H, 1);
+  moe::NormBwdArgs a = bwd_args(dtype, T, H, 1, false);
   if (grad_weight && workspace_bytes < part_bytes(a, H)) return MOE_ERR_WORKSPACE;
   a.g = grad_base;
   a.gn = grad_n;
@@ -173,15 +181,15 @@ int moe_postnorm_bwd(const void* grad_out, const void* grad_n, const void* x, co
     if ((weight || grad_gate) && !y) return MOE_ERR_INVALID_ARG;
     if ((grad_weight && !weight) || (grad_next_weight && !next_weight)) return MOE_ERR_INVALID_ARG;
     if (!grad_x && !grad_y && !sums) return MOE_ERR_INVALID_ARG;
-    if (!rstd || (sums && !workspace)) return MOE_ERR_INVALID_ARG;
+    if (!rstd || ((sums || H > moe::kNormWide) && !workspace)) return MOE_ERR_INVALID_ARG;
   }
   if (!all_aligned(16, grad_out, grad_n, x, y, weight, gate, next_weight, grad_x, grad_y, grad_weight, grad_gate,
                    grad_next_weight, workspace) ||
       !all_aligned(8, rstd))
     return MOE_ERR_ALIGNMENT;
-  moe::NormBwdArgs a = bwd_args(dtype, T, H, gates > 0 ? gates : 1);
-  const size_t part = part_bytes(a, H);
-  if (sums && workspace_bytes < 3 * part) return MOE_ERR_WORKSPACE;
+  moe::NormBwdArgs a = bwd_args(dtype, T, H, gates > 0 ? gates : 1, true);
+  const size_t part = part_bytes(a, H), means = means_bytes(T, H);
+  if ((sums || means) && workspace_bytes < 3 * part + means) return MOE_ERR_WORKSPACE;
   float* ws = static_cast<float*>(workspace);
   a.g = grad_out;
   a.gn = grad_n;
@@ -199,9 +207,9 @@ int moe_postnorm_bwd(const void* grad_out, const void* grad_n, const void* x, co
   a.part1 = grad_weight ? ws : nullptr;
   a.part2 = grad_next_weight ? ws + part / sizeof(float) : nullptr;
   a.partg = grad_gate ? ws + 2 * (part / sizeof(float)) : nullptr;
+  a.means = means && (weight || grad_n) ? ws + 3 * (part / sizeof(float)) : nullptr;
   a.residual = residual_scale;
   a.offset = offset;
-  a.block = true;
   return moe::hip_status(moe::launch_norm_bwd(a, stream));
 }
 

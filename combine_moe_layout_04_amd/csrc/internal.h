@@ -228,6 +228,7 @@ struct NormBwdArgs {
   const float* rstd;
   void *gx, *gy, *gw1, *gg, *gw2;  // each may be null
   float *part1, *part2, *partg;    // [runs, H]; null where not wanted
+  float* means;                    // [T, 2] of a wide row after a block, where it has a norm
   float residual, offset;
   int T, nch, group, gates;
   int rows, parts, runs;  // rows of a run, runs that share a gate (1: a run holds whole gates), runs
@@ -235,7 +236,9 @@ struct NormBwdArgs {
   bool block;             // after a block
 };
 
-void norm_bwd_plan(int64_t T, int64_t group, int nch, int* rows, int* parts, int* runs);
+constexpr int kNormWide = 8192;  // MOE_NORM_WIDE
+
+void norm_bwd_plan(int64_t T, int64_t group, int nch, bool wide, int* rows, int* parts, int* runs);
 
 // Grouped product of 8-bit rows and weights.
 struct I8Args {

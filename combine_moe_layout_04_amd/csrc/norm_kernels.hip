@@ -15,7 +15,7 @@
 //
 // One workgroup per row (forward) or per run of rows (backward), a row's chunks in
 // registers from the first read to the last use, so every row is read and written
-// once.  Sums over a row: each wave's by lane moves, then the waves' in order through
+// once (rows of more than 8192 after a block go backward in two kernels).  Sums over a row: each wave's by lane moves, then the waves' in order through
 // LDS.  Sums over tokens: a workgroup's run in registers, one partial for each run,
 // the partials added in the order of the runs by a second kernel, so that results do
 // not depend on timing.
@@ -267,18 +267,8 @@ __global__ __launch_bounds__(1024) void quant_block_kernel(NormArgs a) {
 
 // ---- backward ---------------------------------------------------------------------
 
-// Rows of up to 512 chunks are asked for a row ahead; wider ones have no registers for
-// that (7168 bfloat16, 4096 rows: 110 us without, 118 with; rows past 16 KiB keep part of
-// it in memory: 16384 bfloat16 take 1.2 ms, eight times their floor).  The chunks stay as they were read, and each of the three passes over them (the
-// first sum, the second, the end) makes its numbers again, a chunk at a time: what lives
-// over a pass is the sums over the run and v.
-template <int DT, int CPL, bool BLOCK, bool kAhead, int MOST>
-__global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
-  constexpr int V = Elems<DT>::kPerChunk, N = CPL * V;
-  __shared__ float red[4][kMaxWaves];
-  const int tid = threadIdx.x, run = blockIdx.x, H = a.nch * V;
-  // the run's rows: a part of one gate's tokens, or whole gates
-  int t0, t1;
+// The tokens of a run: a part of one gate's tokens, or whole gates.
+__device__ __forceinline__ void tokens_of_run(const NormBwdArgs& a, int run, int& t0, int& t1) {
   if (a.parts > 1) {
     const int group = run / a.parts, part = run % a.parts;
     t0 = group * a.group + part * a.rows;
@@ -287,6 +277,53 @@ __global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
     t0 = (int)min((int64_t)run * a.rows, (int64_t)a.T);
     t1 = (int)min((int64_t)t0 + a.rows, (int64_t)a.T);
   }
+}
+
+// A chunk of a row after a block: y^, y^ weight' (y^ without a norm), gate.
+template <int DT, int V>
+__device__ __forceinline__ void block_chunk(const NormBwdArgs& a, u32x4 yc, u32x4 wc, u32x4 gatec, float r1, float (&y)[V],
+                                            float (&yn)[V], float (&gate)[V]) {
+  float w[V];
+  unpack<DT>(yc, y);
+  unpack<DT>(wc, w);
+  unpack<DT>(gatec, gate);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    y[v] *= r1;
+    yn[v] = a.w1 ? y[v] * (w[v] + a.offset) : y[v];
+    if (!a.gate) gate[v] = 1.f;
+  }
+}
+
+// A chunk of the norm before the next block: z^ (from out as the forward pass had it, or
+// x), grad_n, grad_n next'.
+template <int DT, bool BLOCK, int V>
+__device__ __forceinline__ void next_chunk(const NormBwdArgs& a, u32x4 xc, u32x4 gnc, u32x4 wc, float r2, const float (&yn)[V],
+                                           const float (&gate)[V], float (&z)[V], float (&gn)[V], float (&gw)[V]) {
+  float w[V];
+  unpack<DT>(xc, z);
+  unpack<DT>(gnc, gn);
+  unpack<DT>(wc, w);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (BLOCK) z[v] = a.residual * z[v] + gate[v] * yn[v];
+    z[v] *= r2;
+    gw[v] = gn[v] * (w[v] + a.offset);
+  }
+}
+
+// Rows of up to 512 chunks are asked for a row ahead; wider ones have no registers for
+// that (7168 bfloat16, 4096 rows: 110 us without, 118 with).  The chunks stay as they were
+// read, and each of the three passes over them (the first sum, the second, the end) makes
+// its numbers again, a chunk at a time: what lives over a pass is the sums over the run and
+// v.
+template <int DT, int CPL, bool BLOCK, bool kAhead, int MOST>
+__global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int V = Elems<DT>::kPerChunk, N = CPL * V;
+  __shared__ float red[4][kMaxWaves];
+  const int tid = threadIdx.x, run = blockIdx.x, H = a.nch * V;
+  int t0, t1;
+  tokens_of_run(a, run, t0, t1);
   const u32x4 zero = {0, 0, 0, 0};
   auto chunks = [&](const void* p, int row, u32x4(&to)[CPL]) {
 #pragma unroll
@@ -342,31 +379,11 @@ __global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
       if (t + 1 < t1) fetch(t + 1, row);
     }
     const int odd = (t - t0) & 1;  // two rows' sums lie apart: one barrier a sum
-    // chunk i: y^ and the rows y^ weight' (y^ without a norm), gate
     auto block_values = [&](int i, float(&y)[V], float(&yn)[V], float(&gate)[V]) {
-      float w[V];
-      unpack<DT>(r.y[i], y);
-      unpack<DT>(w1[i], w);
-      unpack<DT>(r.gate[i], gate);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        y[v] *= r.r1;
-        yn[v] = a.w1 ? y[v] * (w[v] + a.offset) : y[v];
-        if (!a.gate) gate[v] = 1.f;
-      }
+      block_chunk<DT>(a, r.y[i], w1[i], r.gate[i], r.r1, y, yn, gate);
     };
-    // chunk i: z^ (out as the forward pass had it, or x) and grad_n next'
     auto next_values = [&](int i, const float(&yn)[V], const float(&gate)[V], float(&z)[V], float(&gn)[V], float(&gw)[V]) {
-      float w[V];
-      unpack<DT>(r.x[i], z);
-      unpack<DT>(r.gn[i], gn);
-      unpack<DT>(w2[i], w);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if constexpr (BLOCK) z[v] = a.residual * z[v] + gate[v] * yn[v];
-        z[v] *= r.r2;
-        gw[v] = gn[v] * (w[v] + a.offset);
-      }
+      next_chunk<DT, BLOCK>(a, r.x[i], r.gn[i], w2[i], r.r2, yn, gate, z, gn, gw);
     };
     float m2 = 0.f;
     if (a.gn) {
@@ -451,6 +468,130 @@ __global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
   if (a.gg && a.parts > 1) partial(a.partg, sg);
 }
 
+// Wide rows after a block, in two kernels: the two means of every row first, then, with
+// those known, a wave for 64 chunks of the columns of a run, which needs no other wave.
+// The rows are read twice, but nothing stays in registers but a chunk and its sums (2048
+// rows of 16384 bfloat16: 175 us, 65 are what the bytes of one reading take).
+template <int DT>
+__global__ __launch_bounds__(1024) void norm_means_kernel(NormBwdArgs a) {
+  constexpr int V = Elems<DT>::kPerChunk;
+  __shared__ float red[2][kMaxWaves];
+  const int t = row_of_block(), H = a.nch * V;
+  if (t >= a.T) return;  // uniform
+  const u32x4 zero = {0, 0, 0, 0};
+  auto chunk = [&](const void* p, int row, int j) {
+    return p ? static_cast<const u32x4*>(p)[(size_t)row * a.nch + j] : zero;
+  };
+  const float r1 = a.rstd[2 * (size_t)t], r2 = a.rstd[2 * (size_t)t + 1];
+  const int group = t / a.group;
+  float m2 = 0.f, m1 = 0.f;
+  if (a.gn) {
+    for (int j = threadIdx.x; j < a.nch; j += blockDim.x) {
+      float y[V], yn[V], gate[V], z[V], gn[V], gw[V];
+      block_chunk<DT>(a, chunk(a.y, t, j), chunk(a.w1, 0, j), chunk(a.gate, group, j), r1, y, yn, gate);
+      next_chunk<DT, true>(a, chunk(a.x, t, j), chunk(a.gn, t, j), chunk(a.w2, 0, j), r2, yn, gate, z, gn, gw);
+#pragma unroll
+      for (int v = 0; v < V; ++v) m2 = __builtin_fmaf(gw[v], z[v], m2);
+    }
+    m2 = block_sum(m2, red[0]) / (float)H;
+  }
+  if (a.w1) {
+    for (int j = threadIdx.x; j < a.nch; j += blockDim.x) {  // the row again, from the caches
+      float y[V], yn[V], gate[V], w[V], d[V];
+      const u32x4 wc = chunk(a.w1, 0, j);
+      block_chunk<DT>(a, chunk(a.y, t, j), wc, chunk(a.gate, group, j), r1, y, yn, gate);
+      unpack<DT>(wc, w);
+      unpack<DT>(chunk(a.g, t, j), d);
+      if (a.gn) {
+        float z[V], gn[V], gw[V];
+        next_chunk<DT, true>(a, chunk(a.x, t, j), chunk(a.gn, t, j), chunk(a.w2, 0, j), r2, yn, gate, z, gn, gw);
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] += r2 * (gw[v] - z[v] * m2);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) m1 = __builtin_fmaf(d[v] * gate[v] * (w[v] + a.offset), y[v], m1);
+    }
+    m1 = block_sum(m1, red[1]) / (float)H;
+  }
+  if (threadIdx.x == 0) *reinterpret_cast<float2*>(a.means + 2 * (size_t)t) = make_float2(m1, m2);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormBwdArgs a) {
+  constexpr int V = Elems<DT>::kPerChunk;
+  const int run = blockIdx.y, H = a.nch * V, j = blockIdx.x * blockDim.x + threadIdx.x;
+  if (j >= a.nch) return;
+  int t0, t1;
+  tokens_of_run(a, run, t0, t1);
+  const u32x4 zero = {0, 0, 0, 0};
+  auto chunk = [&](const void* p, int row) { return p ? static_cast<const u32x4*>(p)[(size_t)row * a.nch + j] : zero; };
+  auto store = [&](void* p, int row, const float(&from)[V]) { static_cast<u32x4*>(p)[(size_t)row * a.nch + j] = pack<DT>(from); };
+  struct Row {
+    u32x4 g, gn, x, y;
+    float2 r, m;
+  };
+  auto fetch = [&](int t, Row& r) {
+    r.g = chunk(a.g, t);
+    r.gn = chunk(a.gn, t);
+    r.x = chunk(a.gn ? a.x : nullptr, t);
+    r.y = chunk(a.y, t);
+    r.r = *reinterpret_cast<const float2*>(a.rstd + 2 * (size_t)t);
+    r.m = a.means ? *reinterpret_cast<const float2*>(a.means + 2 * (size_t)t) : make_float2(0.f, 0.f);
+  };
+  float s1[V], s2[V], sg[V];  // sums over the run
+#pragma unroll
+  for (int v = 0; v < V; ++v) s1[v] = s2[v] = sg[v] = 0.f;
+  const u32x4 w1 = chunk(a.w1, 0), w2 = chunk(a.w2, 0);
+  Row row;
+  if (t0 < t1) fetch(t0, row);
+  for (int t = t0; t < t1; ++t) {
+    const Row r = row;
+    if (t + 1 < t1) fetch(t + 1, row);
+    float y[V], yn[V], gate[V], d[V], w[V];
+    block_chunk<DT>(a, r.y, w1, chunk(a.gate, t / a.group), r.r.x, y, yn, gate);
+    unpack<DT>(r.g, d);
+    if (a.gn) {
+      float z[V], gn[V], gw[V];
+      next_chunk<DT, true>(a, r.x, r.gn, w2, r.r.y, yn, gate, z, gn, gw);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s2[v] += gn[v] * z[v];
+        d[v] += r.r.y * (gw[v] - z[v] * r.m.y);
+      }
+    }
+    if (a.gx) {
+      float gx[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) gx[v] = a.residual * d[v];
+      store(a.gx, t, gx);
+    }
+    unpack<DT>(w1, w);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (a.gg) sg[v] += d[v] * yn[v];
+      if (a.gate) d[v] *= gate[v];
+      if (a.w1) {
+        s1[v] += d[v] * y[v];
+        d[v] = r.r.x * (d[v] * (w[v] + a.offset) - y[v] * r.m.x);
+      }
+    }
+    if (a.gy) store(a.gy, t, d);
+    if (a.gg && a.parts == 1 && (t + 1) % a.group == 0) {  // the gate's last token
+      store(a.gg, t / a.group, sg);
+#pragma unroll
+      for (int v = 0; v < V; ++v) sg[v] = 0.f;
+    }
+  }
+  auto partial = [&](float* p, const float(&from)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4)
+      *reinterpret_cast<float4*>(p + (size_t)run * H + (size_t)j * V + v) = make_float4(from[v], from[v + 1], from[v + 2], from[v + 3]);
+  };
+  if (a.part1) partial(a.part1, s1);
+  if (a.part2) partial(a.part2, s2);
+  if (a.gg && a.parts > 1) partial(a.partg, sg);
+}
+
 // Adds partials: blockIdx.y 0 the next norm's weight, 1 the post-norm's, 2.. the gates.
 // 64 columns a workgroup, four a thread; a sixteenth of the partials each.
 template <int DT>
@@ -518,10 +659,18 @@ hipError_t launch_norm_typed(const NormArgs& a, hipStream_t s) {
 template <int DT, bool BLOCK>
 hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
   if (a.runs > 0) {
-    if (a.nch <= 512) norm_bwd_kernel<DT, 1, BLOCK, true, 512><<<a.runs, threads(a.nch, 1), 0, s>>>(a);
+    // a run's sums of two chunks of eight numbers a lane do not fit beside a row: rows of
+    // more than 8192 after a block in two kernels (4096 x 8200 bfloat16: 183 us, in one 817;
+    // 8192: 167 against 122; float32, 8196: 327, 8192: 295 against 254)
+    if (BLOCK && a.nch * Elems<DT>::kPerChunk > kNormWide) {
+      if (a.means) norm_means_kernel<DT><<<row_grid(a.T), a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
+      norm_columns_kernel<DT><<<dim3((a.nch + 255) / 256, a.runs), 256, 0, s>>>(a);
+    } else if (a.nch <= 512) norm_bwd_kernel<DT, 1, BLOCK, true, 512><<<a.runs, threads(a.nch, 1), 0, s>>>(a);
     else if (a.nch <= 1024) norm_bwd_kernel<DT, 2, BLOCK, false, 512><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
-    else if (a.nch <= 2048) norm_bwd_kernel<DT, 2, BLOCK, false, 1024><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
-    else norm_bwd_kernel<DT, 4, BLOCK, false, 1024><<<a.runs, threads(a.nch, 4), 0, s>>>(a);
+    else if constexpr (!BLOCK || DT == kF32) {
+      if (a.nch <= 2048) norm_bwd_kernel<DT, 2, BLOCK, false, 1024><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
+      else if constexpr (!BLOCK) norm_bwd_kernel<DT, 4, BLOCK, false, 1024><<<a.runs, threads(a.nch, 4), 0, s>>>(a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -561,13 +710,15 @@ hipError_t launch_quant(const NormArgs& a, hipStream_t s) {
 
 // Rows of a run, runs that share a gate, and runs in all: about 2048 waves (4096 x 2048
 // bfloat16, four waves a row: 34 us with 512 runs, 44 with 256, 36 with 1024; 7168, eight
-// waves: 110 with 256, 116 with 512).
-void norm_bwd_plan(int64_t T, int64_t group, int nch, int* rows, int* parts, int* runs) {
+// waves: 110 with 256, 116 with 512).  Wide rows in two kernels have a wave for every 64
+// chunks of a run: 128 runs (4096 x 8200: 183 us, 226 with 64, 195 with 512; 2048 x 16384:
+// 175, 163, 189).
+void norm_bwd_plan(int64_t T, int64_t group, int nch, bool wide, int* rows, int* parts, int* runs) {
   if (T == 0) {
     *rows = *parts = *runs = 0;
     return;
   }
-  const int waves = (nch + kWave - 1) / kWave, most = waves <= 2 ? 1024 : waves <= 4 ? 512 : 256;
+  const int waves = (nch + kWave - 1) / kWave, most = wide ? 128 : waves <= 2 ? 1024 : waves <= 4 ? 512 : 256;
   int64_t r = (T + most - 1) / most;
   if (group >= r) {
     *parts = (int)((group + r - 1) / r);

@@ -581,6 +581,7 @@ int moe_matmul_i8(moe_handle_t h, const int8_t* q, const float* scale, int64_t r
  *   (8-byte aligned) of y and z for moe_postnorm (1 where there is no norm), what the
  *   backward passes take.  eps > 0.  T = 0 is valid; MOE_ERR_UNSUPPORTED above 2^26. */
 #define MOE_MAX_NORM_BYTES 65536
+#define MOE_NORM_WIDE 8192 /* moe_postnorm_bwd needs its workspace for every row wider than this */
 int moe_prenorm(const void* x, int dtype, int64_t T, int64_t H, const void* weight, float offset, float eps, void* n,
                 int8_t* q, float* scale, float* rstd, hipStream_t stream);
 int moe_postnorm(moe_handle_t h, const void* x, const void* y, int dtype, int64_t T, int64_t H,
@@ -599,9 +600,10 @@ int moe_postnorm(moe_handle_t h, const void* x, const void* y, int dtype, int64_
  * order that depends on the shapes alone.  y is the rows of tokens (after moe_combine
  * where there is a layout; its own backward pass takes grad_y).  Any output may be
  * NULL, not all; grad_out or grad_n may be NULL (0), not both; x is read only with
- * grad_n, y only with grad_n, a norm of it or grad_gate.  grad_x may be grad_out.  workspace (16-byte aligned, moe_norm_bwd_workspace_size bytes; one per
- * call in flight) is not needed without a sum over tokens.  With T = 0 those sums are
- * set to zero.                                                                   */
+ * grad_n, y only with grad_n, a norm of it or grad_gate.  grad_x may be grad_out.
+ * workspace (16-byte aligned, moe_norm_bwd_workspace_size bytes; one per call in flight)
+ * is not needed without a sum over tokens, of rows after a block of at most MOE_NORM_WIDE
+ * elements.  With T = 0 those sums are set to zero.                               */
 int moe_norm_bwd_workspace_size(int dtype, int64_t T, int64_t H, int64_t gates, size_t* bytes);
 int moe_prenorm_bwd(const void* grad_n, const void* x, int dtype, int64_t T, int64_t H, const void* weight, float offset,
                     const float* rstd, const void* grad_base, void* grad_x, void* grad_weight, void* workspace,

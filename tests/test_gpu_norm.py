@@ -269,6 +269,28 @@ def test_gradients_that_are_asked_for():
         assert all(torch.equal(s, t) for s, t in zip(p, q))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,H,G", [(200, 8200, 2), (200, 8200, 100), (130, 9216, 130), (3, 12288, 1), (65, 16384, 0)])
+def test_wide_rows_backward(dtype, T, H, G):
+    """Past MOE_NORM_WIDE: gates of more and of fewer tokens than a run, in place, each output alone."""
+    d = make(T, H, dtype, T + H, G)
+    _, _, rstd, ref = run_all(d, 0.5)
+    kw = dict(weight=d["weight"], gate=d.get("gate"), residual_scale=0.5, next_weight=d["next_weight"])
+    g = d["grad_out"].clone()
+    size = M.moe_norm_bwd_workspace_size(dtype, T, H, G)
+    ws = torch.full((size + 512,), 171, dtype=torch.uint8, device=DEV)
+    got = names(M.moe_postnorm_bwd(g, d["grad_n"], d["x"], d["y"], rstd, grad_x=g, workspace=ws, **kw))
+    assert all(got[k] is None or torch.equal(got[k], ref[k]) for k in got) and (ws[size:] == 171).all()
+    for name in ref:
+        if ref[name] is None:
+            continue
+        ask = {k: k == name for k in ref}
+        got = names(M.moe_postnorm_bwd(d["grad_out"], d["grad_n"], d["x"], d["y"], rstd, **kw, **ask))
+        assert torch.equal(got[name], ref[name])
+    run_all(make(T, H, dtype, 1, 0, False, False), 0.5)
+    run_all(make(T, H, dtype, 2, G, False, True), 0.5)
+
+
 def test_outputs_in_place_and_what_lies_around():
     d = make(20, 128, BF16, 2, 4)
     ref = run_all(d)

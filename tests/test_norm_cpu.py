@@ -72,6 +72,17 @@ def test_postnorm_bwd_refusals(L, kw, code):  # noqa: F811
     assert L.moe_postnorm_bwd(*dict(POST_BWD, **kw).values(), None) == C[code]
 
 
+def test_wide_rows_need_the_workspace(L):  # noqa: F811
+    """Rows past MOE_NORM_WIDE after a block go backward in two kernels, which meet in the workspace."""
+    one = dict(POST_BWD, H=8200, gw=None, gg=None, gnw=None)
+    assert L.moe_postnorm_bwd(*dict(one, ws=None).values(), None) == C["MOE_ERR_INVALID_ARG"]
+    assert L.moe_postnorm_bwd(*dict(one, ws_bytes=64).values(), None) == C["MOE_ERR_WORKSPACE"]
+    n, m = ctypes.c_size_t(), ctypes.c_size_t()
+    f = L.moe_norm_bwd_workspace_size
+    assert f(1, 4096, 8200, 1, ctypes.byref(n)) == 0 and n.value >= 64 * 8200 * 12 + 4096 * 8
+    assert f(1, 4096, 8192, 1, ctypes.byref(m)) == 0 and m.value == 256 * 8192 * 12
+
+
 def test_handles_empty_calls_and_workspace(L):  # noqa: F811
     h = ctypes.c_void_p()
     assert L.moe_handle_create(ctypes.byref(h), None) == C["MOE_OK"]
