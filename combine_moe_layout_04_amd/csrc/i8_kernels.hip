@@ -26,12 +26,12 @@
 // step of its own, so that workgroups do not all ask for the same part of their rows at
 // the same time.
 //
-// Measured (MI355X): one projection of 4096 rows, 7168 x 4096, gated: 107 us, 2.2 POP/s,
-// half of what the matrix cores could do (a library's product of two 8192 x 8192 int8
-// matrices reaches 2.4); the loads alone take 77 us, the products alone 57.  4096 tokens of
-// 8 of 128 experts, 2048 x 1536, gated: 165 us; loads alone 128 (570 MB pass through the
-// L2s, 403 of them weights), products alone 70.  64 tokens there: 73 us, 5.5 TB/s of
-// weights, which is what memory gives.
+// Measured (MI355X): one projection of 4096 rows, 7168 x 4096, gated: 103 to 113 us, 2.1 to
+// 2.3 POP/s, half of what the matrix cores could do (a library's product of two 8192 x 8192
+// int8 matrices reaches 2.4); the loads alone take 77 us, the products alone 57.  4096 tokens
+// of 8 of 128 experts, 2048 x 1536, gated: 156 us; loads alone 128 (520 to 570 MB are read,
+// 403 of them weights), products alone 70.  64 tokens there: 73 us, 5.5 TB/s of weights,
+// which is what memory gives.
 #include "device_common.h"
 #include "internal.h"
 #include "mfma.h"
@@ -57,7 +57,7 @@ struct Tile {
 // The tiles of a call, numbered by expert, band of kBand row tiles, channel tile and row
 // tile, the last fastest: what an XCD works on at a time is about as high as wide, and
 // reads fewer rows and weights into its L2 than a column of tiles would (4096 rows of
-// 7168 x 4096: 107 us, in columns 110).
+// 7168 x 4096: 107 us when this was tried, in columns 110).
 constexpr int kBand = 8;
 
 struct Tiles {

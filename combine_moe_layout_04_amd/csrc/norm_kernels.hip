@@ -15,10 +15,16 @@
 //
 // One workgroup per row (forward) or per run of rows (backward), a row's chunks in
 // registers from the first read to the last use, so every row is read and written
-// once (rows of more than 8192 after a block go backward in two kernels).  Sums over a row: each wave's by lane moves, then the waves' in order through
-// LDS.  Sums over tokens: a workgroup's run in registers, one partial for each run,
-// the partials added in the order of the runs by a second kernel, so that results do
-// not depend on timing.
+// once (rows of more than 8192 after a block go backward in two kernels).  Sums over
+// a row: each wave's by lane moves, then the waves' in order through LDS.  Sums over
+// tokens: a workgroup's run in registers, one partial for each run, the partials added
+// in the order of the runs by a second kernel, so that results do not depend on
+// timing.
+//
+// Bound by HBM.  Measured (MI355X, kernels): 8192 rows of 2816 with their combine of 8
+// receive rows: 100 us, 510 MB (a combine alone 70, 415 MB); 4096 x 7168 to 8 bits: 24 us,
+// 3.6 TB/s, what the rounding leaves of the bandwidth; 4096 x 2048 after a block: 16.5 us
+// forward (67 MB), 28 + 4 backward (101 MB and 13 MB of partials).
 #include "device_common.h"
 #include "internal.h"
 #include "quant.h"
