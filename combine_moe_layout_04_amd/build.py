@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["abi.hip", "layout_kernels.hip", "row_kernels.hip", "staged_kernels.hip", "copy_kernels.hip",
            "abi_route.hip", "route_kernels.hip", "abi_few.hip", "few_kernels.hip",
            "abi_lowrank.hip", "lowrank_kernels.hip", "abi_balance.hip", "balance_kernels.hip",
-           "abi_i8.hip", "i8_kernels.hip", "abi_norm.hip", "norm_kernels.hip"]
+           "abi_i8.hip", "i8_kernels.hip", "i8_middle.hip", "i8_small.hip", "abi_norm.hip", "norm_kernels.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
