@@ -40,10 +40,9 @@ __device__ __forceinline__ float quant_exact(float x, float s, float inv) {
 
 // Values of one 16-byte chunk of a row (4 float32, 8 bfloat16) as its 4 or 8 bytes.
 // |x / s| is at most 127 (1 + 2^-23) and inv off by 2^-23 of itself, so x * inv is within
-// 2^-15 of it: only where that
-// lies nearer than 2^-14 to a half can its rounding be another than the quotient's.  A
-// row with an infinity or NaN has that as its scale, and zeros: what is made of it is
-// NaN.
+// 2^-15 of it: only where that lies nearer than 2^-14 to a half can its rounding be another
+// than the quotient's.  A row with an infinity or NaN has that as its scale, and zeros:
+// what is made of it is NaN.
 template <int V>
 __device__ __forceinline__ void store_quant(int8_t* row, int chunk, const float* f, float s, float inv) {
   float q[V], far = 0.f;
