@@ -256,7 +256,8 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
   auto load = [&](auto STAGE, int s, auto n) __attribute__((always_inline)) {
     int step = s + begin;
     if (step >= full) step -= full;
-    const bool in = s < full && chunk < a.kch - step * KC;  // a step there is, not past the row's end
+    const int left = s < full ? a.kch - step * KC : 0;  // chunks of the row from there on (a select, no branch)
+    const bool in = chunk < left;
     const int at = step * KC * 16;
     if constexpr (n < kLoadsA) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
