@@ -262,6 +262,25 @@ def test_many_wide_rows():
     assert torch.equal(q[-1].cpu(), exact_quant(x[-1:])[0][0]) and (q[:-1:100003] == 0).all() and (s[:-1] == 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("rows,N", [(6500, 4096), (2700, 1024), (700, 512)])
+@pytest.mark.parametrize("width", [16, 128, 144, 256, 272, 384, 400, 512, 640, 752, 768, 896])
+def test_many_tiles_of_few_steps(rows, N, width):
+    """Every size of tile, one to seven steps each, several tiles a workgroup.
+
+    Sums stay below 2^24 (896 * 127^2 = 14.5e6), so a float32 product has them exactly in any
+    order, and float(acc) * scale * w_scale is formed as the kernel forms it: equal in all bits."""
+    g = torch.Generator(device=DEV).manual_seed(width)
+    q = torch.randint(-127, 128, (rows, width), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, width), generator=g, device=DEV, dtype=torch.int8)
+    s = torch.rand(rows, generator=g, device=DEV) + 0.5
+    ws = torch.rand(N, generator=g, device=DEV) + 0.5
+    want = (q.float() @ w.float().T) * s[:, None] * ws
+    for _ in range(3):
+        out = torch.full((rows, N), math.nan, dtype=torch.float32, device=DEV)
+        assert torch.equal(M.moe_matmul_i8(q, s, w, ws, dtype=torch.float32, out=out), want)
+    assert torch.equal(M.moe_matmul_i8(q, s, w, ws, dtype=torch.bfloat16), want.to(torch.bfloat16))
+
+
 def test_results_repeat_and_an_empty_batch():
     idx, h = routed(500, 4, 16, 1)
     q, s = rows8(500, 304, 1)
