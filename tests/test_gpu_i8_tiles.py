@@ -1,0 +1,121 @@
+"""Products in 8-bit integers in every size of tile: segments of every length around the tiles' edges, several
+column tiles, whole and partial steps, rows gathered by token, every activation and output type.
+
+Sums and scales as in test_gpu_i8: without an activation outputs are equal to float32 arithmetic of known order,
+bit for bit; with one they are off by 24 u |g up| (u = 2^-24), and eps/2 of themselves for the rounding.
+"""
+import math
+
+import pytest
+import torch
+
+import combine_moe_layout_04_amd as M
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+F32, BF16 = torch.float32, torch.bfloat16
+U = 2.0 ** -24
+
+# rows of each expert: none, one, and both sides of 16, 32, 64, 128, 256 and of what three row parts hold
+ROWS = [0, 1, 15, 16, 17, 31, 48, 64, 65, 112, 127, 128, 129, 0, 240, 255, 256, 257, 300, 288, 289, 383, 384, 385, 513]
+E, R = len(ROWS), sum(ROWS)
+
+
+def tiles(rows, N, width, experts):
+    """The rule by which the library takes its tiles (128 x 256, 64 x 128, 64 x 64), in whole numbers."""
+    def most(bm, bn):
+        return (rows // bm + (min(rows, experts) if experts else 1)) * -(-N // bn)
+    if most(128, 256) >= (192 if width >= 2048 else 400):
+        return "large"
+    return "middle" if most(64, 128) >= 256 else "small"
+
+
+def operands(rows, width, banks, N, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = torch.randint(-128, 128, (rows, width), generator=g, dtype=torch.int8, device=DEV)
+    w = torch.randint(-128, 128, (banks, N, width), generator=g, dtype=torch.int8, device=DEV)
+    s = (torch.rand(rows, generator=g, device=DEV) + 0.5) / 64
+    ws = (torch.rand(banks, N, generator=g, device=DEV) + 0.5) * (width ** -0.5 / 64)
+    return q, s, w, ws
+
+
+def expected(q, s, w, ws, act, dtype):
+    """(value, bound) of one expert's rows; sums in float64, exact below 2^53."""
+    acc = torch.mm(q.double(), w.double().t().contiguous())
+    if act is None:
+        return ((acc.float() * s[:, None]) * ws).to(dtype), 0.0
+    y = acc * s.double()[:, None] * ws.double()
+    g, up = y.chunk(2, 1)
+    if act == "silu":
+        f = g / (1 + torch.exp(-g))
+    else:
+        f = 0.5 * g * (1 + torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)))
+    ref, tol = f * up, 24 * U * (g * up).abs()
+    return ref, tol + torch.finfo(dtype).eps / 2 * (ref.abs() + tol) + 1e-37
+
+
+def check(got, ref, tol, what):
+    if isinstance(tol, float):
+        assert torch.equal(got, ref), what
+    else:
+        err = (got.double() - ref).abs()
+        assert bool((err <= tol).all()), (what, float((err - tol).max()))
+
+
+KINDS = [(None, F32), ("silu", BF16), ("gelu_tanh", F32), (None, BF16), ("silu", F32), ("gelu_tanh", BF16)]
+SHAPES = [(16, 2064, "large"), (128, 2064, "large"), (272, 2304, "large"), (1024, 2304, "large"), (1040, 2064, "large"),
+          (1280, 2064, "large"), (2064, 1040, "large"), (144, 1040, "middle"), (1040, 1040, "middle"), (1152, 1040, "middle"),
+          (1280, 1040, "middle"), (2064, 656, "middle"), (144, 144, "small"), (1040, 144, "small"), (2064, 144, "small")]
+
+
+@pytest.mark.parametrize("tokens", [True, False])
+@pytest.mark.parametrize("width,N,size", SHAPES)
+def test_segments_of_every_length(tokens, width, N, size):
+    assert tiles(R, N, width, E) == size
+    g = torch.Generator().manual_seed(width + N)
+    idx = torch.repeat_interleave(torch.arange(E), torch.tensor(ROWS))[torch.randperm(R, generator=g)]
+    h = M.moe_layout(idx.to(torch.int32).view(-1, 1).to(DEV), E, 1)
+    q, s, w, ws = operands(R, width, E, N, width)
+    token, off = h.field("recv_token").long(), h.field("expert_offset").tolist()
+    assert [b - a for a, b in zip(off, off[1:])] == ROWS
+    outs = []
+    for act, dtype in KINDS:
+        out = torch.full((R, N if act is None else N // 2), math.nan, dtype=dtype, device=DEV)
+        outs.append(M.moe_matmul_i8(q, s, w, ws, handle=h, tokens=tokens, activation=act, out=out))
+    for e in range(E):
+        at = slice(off[e], off[e + 1])
+        rows = token[at] if tokens else torch.arange(off[e], off[e + 1], device=DEV)
+        for (act, dtype), out in zip(KINDS, outs):
+            ref, tol = expected(q[rows], s[rows], w[e], ws[e], act, dtype)
+            check(out[at], ref, tol, (e, ROWS[e], act, dtype))
+
+
+@pytest.mark.parametrize("width,N,size", [(400, 2064, "large"), (1040, 2064, "large"), (400, 656, "middle"), (1168, 656, "middle")])
+def test_several_experts_a_token(width, N, size):
+    """Each token's row is read by four experts, of very different numbers of tokens."""
+    T, K, experts = 1000, 4, 16
+    assert tiles(T * K, N, width, experts) == size
+    g = torch.Generator().manual_seed(width)
+    z = torch.randn(T, experts, generator=g) - 0.3 * torch.arange(experts)
+    idx = torch.topk(z, K, 1)[1].to(torch.int32).to(DEV)
+    h = M.moe_layout(idx, experts, 1)
+    q, s, w, ws = operands(T, width, experts, N, width)
+    token, off = h.field("recv_token").long(), h.field("expert_offset").tolist()
+    assert min(b - a for a, b in zip(off, off[1:])) < 64 and max(b - a for a, b in zip(off, off[1:])) > 300
+    for act, dtype in KINDS[:4]:
+        out = M.moe_matmul_i8(q, s, w, ws, handle=h, tokens=True, activation=act, dtype=dtype)
+        for e in range(experts):
+            rows = token[off[e]:off[e + 1]]
+            ref, tol = expected(q[rows], s[rows], w[e], ws[e], act, dtype)
+            check(out[off[e]:off[e + 1]], ref, tol, (e, act, dtype))
+
+
+@pytest.mark.parametrize("rows,width,N,size", [(4099, 400, 3344, "large"), (4099, 1296, 3344, "large"), (4099, 2192, 1552, "large"),
+                                               (1030, 1040, 2064, "middle"), (1030, 2064, 2064, "middle")])
+def test_without_a_layout(rows, width, N, size):
+    assert tiles(rows, N, width, 0) == size
+    q, s, w, ws = operands(rows, width, 1, N, rows)
+    for act, dtype in KINDS:
+        out = M.moe_matmul_i8(q, s, w[0], ws[0], activation=act, dtype=dtype)
+        ref, tol = expected(q, s, w[0], ws[0], act, dtype)
+        check(out, ref, tol, (act, dtype))
