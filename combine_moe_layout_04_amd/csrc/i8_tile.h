@@ -425,8 +425,12 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
       else sums(std::integral_constant<int, 4>{}, FIRST, follow);
     }
     __asm__ __volatile__("" ::: "memory");
+    bool token[MB];  // a row without one is zero, whatever the channels' scales are
 #pragma unroll
-    for (int i = 0; i < MB; ++i) scale_row[i] = rows.scale[i];
+    for (int i = 0; i < MB; ++i) {
+      token[i] = scale_row[i] >= 0;
+      scale_row[i] = rows.scale[i];
+    }
     const Tile after = tile_at(id += stride);
     rows_of(after, rows);
     in_order();
@@ -458,6 +462,7 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
                       ((float)acc[i][2 * j + 1][v] * scale_q[i] * scale_w[2 * j + 1][v]);
           else
             y[j][v] = (float)acc[i][j][v] * scale_q[i] * scale_w[j][v];
+          if (!token[i]) y[j][v] = 0.f;
         }
       if constexpr (DT == kF32) {
 #pragma unroll

@@ -119,3 +119,26 @@ def test_without_a_layout(rows, width, N, size):
         out = M.moe_matmul_i8(q, s, w[0], ws[0], activation=act, dtype=dtype)
         ref, tol = expected(q, s, w[0], ws[0], act, dtype)
         check(out, ref, tol, (act, dtype))
+
+
+@pytest.mark.parametrize("N,size", [(2064, "large"), (1040, "middle"), (144, "small")])
+@pytest.mark.parametrize("act", [None, "silu", "gelu_tanh"])
+def test_padding_rows_are_zero_whatever_the_weights_scales(N, size, act):
+    """Channels whose weights were not finite have an infinity or NaN as their scale: NaN in every token's row,
+    and still zero in a row without a token."""
+    h = M.Handle(pad_multiple=16)
+    idx = torch.repeat_interleave(torch.arange(E), torch.tensor(ROWS)).to(torch.int32).view(-1, 1).to(DEV)
+    M.moe_layout(idx, E, 1, handle=h)
+    assert tiles(h.R, N, 144, E) == size
+    q, s, w, ws = operands(R, 144, E, N, 5)
+    plain = M.moe_matmul_i8(q, s, w, ws, handle=h, tokens=True, activation=act, dtype=F32)
+    w[:, 3], ws[:, 3] = 0, math.inf
+    w[:, N - 1], ws[:, N - 1] = 0, math.nan
+    out = M.moe_matmul_i8(q, s, w, ws, handle=h, tokens=True, activation=act, dtype=F32)
+    there = h.field("expert_offset")[-1]
+    token = h.field("recv_token")[:there]
+    out, plain = out[:there], plain[:there]
+    assert int((token < 0).sum()) > 100 and (out[token < 0] == 0).all()
+    bad = [3, N - 1] if act is None else [3, N // 2 - 1]
+    keep = [n for n in range(out.shape[1]) if n not in bad]
+    assert torch.isnan(out[token >= 0][:, bad]).all() and torch.equal(out[:, keep], plain[:, keep])
