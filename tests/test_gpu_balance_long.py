@@ -34,3 +34,37 @@ def test_tokens_that_do_not_count_change_nothing(score):
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
     assert (got[0][4][~keep] == 0).all() and (got[0][4][keep] != 0).any()
+
+
+@pytest.mark.parametrize("E", [64, 200, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_far_logits_keep_their_digits(score, E):
+    """Scores of logits up to 80 below the largest, each token a sequence of its own, so that probs are the
+    scores.
+
+    Logits are multiples of 2^-10 below 2^7, so z - max is exact.  u = 2^-24: an exponential is off by 3 u, a
+    sum of at most 16 + 6 terms by 22 u more, the quotient by 2 u, so a softmax by 30 u; a sigmoid relative
+    to the largest is an exponential, a sum with another, a quotient and a product, 9 u, so its share is off by
+    9 + 31 + 2 u.  The gradient of loss[1] is 2/n lse softmax: 30 u, 3 u for the products, and lse to
+    4 u (|lse| + max) + 32 u."""
+    T = 48
+    g = torch.Generator().manual_seed(E)
+    z = -torch.floor(torch.rand(T, E, generator=g) * 80 * 1024) / 1024
+    z += torch.floor(torch.rand(T, 1, generator=g) * 40 * 1024 - 20 * 1024) / 1024
+    idx = torch.randint(0, E, (T, 2), generator=g).to(torch.int32).to(DEV)
+    seq = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    loss, counts, probs, tokens = M.moe_balance(z.to(DEV), idx, seq, None, score)
+    grad = M.moe_balance_bwd(z.to(DEV), counts, tokens, torch.tensor([0.0, 1.0], device=DEV), 2, seq, None, score)
+    zd = z.double()
+    soft, lse = torch.softmax(zd, 1), torch.logsumexp(zd, 1, keepdim=True)
+    ref = soft
+    if score == "sigmoid":
+        ref = torch.sigmoid(zd)
+        ref = ref / ref.sum(1, keepdim=True)
+    err = ((probs.cpu().double() - ref).abs() / ref).max()
+    assert err <= (30 if score == "softmax" else 42) * U, float(err / U)
+    want = 2 / T * lse * soft
+    dl = 4 * U * (lse.abs() + zd.amax(1, keepdim=True).abs()) + 32 * U
+    tol = 33 * U * want.abs() + 2 / T * soft * dl + 1e-37
+    bad = (grad.cpu().double() - want).abs() - tol
+    assert bool((bad <= 0).all()), float(bad.max())
