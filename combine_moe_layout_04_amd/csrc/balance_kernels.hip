@@ -105,6 +105,12 @@ __device__ __forceinline__ void scores(const float (&z)[VPL], float (&soft)[VPL]
   }
   sum = wave_sum(sum);
   lse = sum == 0.f ? 0.f : m + logf(sum);
+  if (m == INFINITY) {  // its differences are NaN; the same in every lane
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) nan |= z[v] != z[v];
+    if (!__any(nan)) lse = m;
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if constexpr (SIG) {
     float all = 0.f;

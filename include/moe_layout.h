@@ -413,7 +413,8 @@ int moe_route_bwd(const void* logits, int dtype, int64_t T, int E, int K, const 
  * without counted tokens has no part; with none at all both losses are 0.  Ids
  * outside [0,E) are not counted.  A token whose scores are all zero (its logits all
  * -inf, or for sigmoids below -708) has s = 0 and, if all are -inf, no part in
- * loss[1]; NaN or +inf logits spread as the formulas say.
+ * loss[1]; NaN or +inf logits spread as the formulas say (with +inf the token's softmax
+ * is NaN and its lse +inf).
  *   logits [T,E] dtype (any E from 1 to 1024), topk_idx [T,K] int32 or int64,
  *   seq_offset [S+1] int32 on the device, token_mask [T] bytes; loss [2], counts
  *   [S,E], probs [S,E], tokens [S] are written; workspace 256-byte aligned,

@@ -68,3 +68,18 @@ def test_far_logits_keep_their_digits(score, E):
     tol = 33 * U * want.abs() + 2 / T * soft * dl + 1e-37
     bad = (grad.cpu().double() - want).abs() - tol
     assert bool((bad <= 0).all()), float(bad.max())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_infinite_logit_has_an_infinite_z_loss(score):
+    """lse of a token with +inf is +inf, and so is the mean of lse^2; with NaN beside it it is NaN."""
+    for E in (5, 64, 300):
+        z = torch.randn(40, E, generator=torch.Generator().manual_seed(E)).to(DEV)
+        idx = torch.zeros(40, 1, dtype=torch.int32, device=DEV)
+        z[3, E // 2] = math.inf
+        assert M.moe_balance(z, idx, score=score)[0][1] == math.inf
+        z[3, 0] = math.inf
+        z[3, E - 1] = -math.inf
+        assert M.moe_balance(z, idx, score=score)[0][1] == math.inf
+        z[3, 1] = math.nan
+        assert torch.isnan(M.moe_balance(z, idx, score=score)[0][1])
