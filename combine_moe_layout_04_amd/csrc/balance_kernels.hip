@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kWaves = 4;     // of a workgroup of the backward
 constexpr int kRuns = 256;    // workgroups of the first kernel: one a CU
+constexpr int kAdded = 128;   // tokens that a wave adds in 32 bits at most
 constexpr int kCols = 32;     // experts of a workgroup of the second kernel, if there is more than one
 constexpr int kDirect = 1 << 15;  // values of a kind that one workgroup adds by itself
 
@@ -438,10 +439,13 @@ hipError_t launch_typed(const BalanceArgs& a, bool backward, dim3 grid, hipStrea
 
 }  // namespace
 
-// Tokens of a run: enough runs for the CUs, two tokens or more for each wave.
+// Tokens of a run: enough runs for the CUs, two tokens or more for each wave.  Past 2^19
+// tokens there are more runs instead of longer ones: sums over a run are in 32 bits, those
+// of the runs in 64, so a result is as near with 2^26 tokens as with 2^19 (2^23 tokens of 13
+// experts alike: off by 432 u of itself with 256 runs, u = 2^-24).
 int balance_tile(int64_t T) {
   const int64_t t = (T + kRuns - 1) / kRuns;
-  return (int)(t < 32 ? 32 : t);
+  return (int)(t < 2 * kRunWaves ? 2 * kRunWaves : t > kAdded * kRunWaves ? kAdded * kRunWaves : t);
 }
 int balance_runs(int64_t T) { return T > 0 ? (int)((T + balance_tile(T) - 1) / balance_tile(T)) : 1; }
 int balance_columns(int E) { return (E + kCols - 1) / kCols; }

@@ -83,3 +83,21 @@ def test_an_infinite_logit_has_an_infinite_z_loss(score):
         assert M.moe_balance(z, idx, score=score)[0][1] == math.inf
         z[3, 1] = math.nan
         assert torch.isnan(M.moe_balance(z, idx, score=score)[0][1])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,dtype", [((1 << 23) + 5, 13, F32), ((1 << 21) + 3, 300, BF16)])
+def test_sums_over_many_equal_tokens(score, T, E, dtype):
+    """Equal logits, whose scores 1/E are not dyadic: a long sum in 32 bits rounds to the same side again and again.
+
+    u = 2^-24: a score is off by 4 u, at most 128 of them are added in a wave and 16 waves' sums of them in a run,
+    144 u; the rest is in 64 bits, and rounded once.  lse is off by 4 u, its square by 9 u."""
+    z = torch.full((T, E), 0.5, dtype=dtype, device=DEV)
+    idx = (torch.arange(T, device=DEV) % E).to(torch.int32).view(-1, 1)
+    loss, counts, probs, tokens = M.moe_balance(z, idx, score=score)
+    assert torch.equal(counts[0].long(), torch.bincount(idx.view(-1), minlength=E)) and tokens.tolist() == [T]
+    err = float((probs.double() * (E / T) - 1).abs().max())
+    assert err <= 149 * U, err / U
+    assert abs(float(loss[0]) - 1) <= 150 * U, float(loss[0] - 1) / U
+    lse2 = (0.5 + math.log(E)) ** 2
+    assert abs(float(loss[1]) / lse2 - 1) <= 155 * U, (float(loss[1]) / lse2 - 1) / U
