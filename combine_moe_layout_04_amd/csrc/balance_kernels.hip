@@ -169,7 +169,10 @@ __global__ __launch_bounds__(kRunWaves * kWave) void balance_kernel(BalanceArgs 
     const int begin = seq_begin(a, q);
     if (begin >= t1) break;
     const int lo = max(t0, begin), hi = min(t1, seq_end(a, q));
-    if (lo >= hi) continue;
+    if (lo >= hi) {  // empty, as any number after it may be
+      q = max(q, sequences_before(a, lo) - 1);
+      continue;
+    }
     for (int e = threadIdx.x; e < a.E; e += kWaves * kWave) hist[e] = 0;
     __syncthreads();
     float p[VPL], zz = 0.f;
@@ -243,8 +246,9 @@ __global__ __launch_bounds__(kRunWaves * kWave) void balance_kernel(BalanceArgs 
   }
 }
 
-// Three sums over the workgroup of 1024 threads, in a fixed order, in every thread.
-__device__ __forceinline__ void block_sums(double (&v)[3], double (&shared)[3][16]) {
+// Three sums over the workgroup, in a fixed order, in every thread.
+template <int WAVES>
+__device__ __forceinline__ void block_sums(double (&v)[3], double (&shared)[3][WAVES]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) v[i] = wave_sum(v[i]);
   if (lane_id() == 0)
@@ -255,7 +259,7 @@ __device__ __forceinline__ void block_sums(double (&v)[3], double (&shared)[3][1
   for (int i = 0; i < 3; ++i) {
     v[i] = 0.0;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) v[i] += shared[i][w];
+    for (int w = 0; w < WAVES; ++w) v[i] += shared[i][w];
   }
 }
 
@@ -265,11 +269,12 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, double sum, dou
 }
 
 // Sequence blockIdx.y, a.cols experts from blockIdx.x * a.cols on.
-__global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
-  __shared__ double sp[1024];
-  __shared__ int sc[1024];
-  __shared__ double sums[3][16];
-  const int q = blockIdx.y, wide = (a.cols + kCols - 1) / kCols * kCols, groups = 1024 / wide;
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void balance_finish_kernel(BalanceArgs a) {
+  __shared__ double sp[THREADS];
+  __shared__ int sc[THREADS];
+  __shared__ double sums[3][THREADS / kWave];
+  const int q = blockIdx.y, wide = (a.cols + kCols - 1) / kCols * kCols, groups = THREADS / wide;
   const int col = threadIdx.x % wide, g = threadIdx.x / wide;
   const int e = blockIdx.x * a.cols + col;
   const bool mine = g < groups && col < a.cols && e < a.E;
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
   const int w0 = lo < hi ? lo / a.tile : 0, w1 = lo < hi ? (hi - 1) / a.tile : -1;
   double v[3] = {0.0, 0.0, 0.0};  // counts times probabilities, z, tokens
   if (blockIdx.x == 0)
-    for (int w = w0 + (int)threadIdx.x; w <= w1; w += 1024) {
+    for (int w = w0 + (int)threadIdx.x; w <= w1; w += THREADS) {
       v[1] += a.part_z[w + q];
       v[2] += a.part_n[w + q];
     }
@@ -321,14 +326,13 @@ __global__ __launch_bounds__(1024) void balance_loss_kernel(BalanceArgs a, int c
   __shared__ double sums[3][16], more[3][16];
   double v[3] = {0.0, 0.0, 0.0}, some[3] = {0.0, 0.0, 0.0};
   for (int q = threadIdx.x; q < a.S; q += 1024) {
-    const double n = a.tokens[q];
-    if (n <= 0) continue;
+    const double n = a.tokens[q], z = a.seq_z[q];  // zeros of a sequence without tokens
     double s = 0.0;
     for (int b = 0; b < columns; ++b) s += a.seq_sum[(size_t)q * columns + b];
-    v[0] += s / (n * n);
-    v[1] += a.seq_z[q];
+    v[0] += n > 0 ? s / (n * n) : 0.0;
+    v[1] += z;
     v[2] += n;
-    some[0] += 1.0;
+    some[0] += n > 0 ? 1.0 : 0.0;
   }
   block_sums(v, sums);
   block_sums(some, more);
@@ -337,14 +341,18 @@ __global__ __launch_bounds__(1024) void balance_loss_kernel(BalanceArgs a, int c
 
 template <int DT, int VPL, bool SIG>
 __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs a) {
+  __shared__ int sums[2][kWaves];
   const int lane = lane_id();
   const int64_t first = ((int64_t)blockIdx.x * kWaves + threadIdx.x / kWave) * a.tile;  // tile: tokens of a wave
   const int t0 = (int)min((int64_t)a.T, first), t1 = (int)min((int64_t)a.T, first + a.tile);
-  if (t0 >= t1) return;
+  const bool mine = t0 < t1;  // wave-uniform
   // everything a wave begins with is asked for before any of it is used
   float z[VPL], next[VPL];
-  load_token<DT, VPL>(a, t0, next);
-  bool there, there_next = counted(a, t0);
+  bool there, there_next = false;
+  if (mine) {
+    load_token<DT, VPL>(a, t0, next);
+    there_next = counted(a, t0);
+  }
   const float given0 = a.grad_loss[0], given1 = a.grad_loss[1];
   int q = sequences_before(a, t0);
   int begin, end, count[VPL];
@@ -361,14 +369,33 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
     }
   };
   enter(q);
+  // all sequences' tokens: a wave by itself where it has one each lane, else the workgroup
+  const bool alone = a.S <= kWave;
   int all = 0, some = 0;
-  for (int s = lane; s < a.S; s += kWave) {
+  auto add = [&](int s) {
     const int m = a.tokens[s];
     all += m;
     some += m > 0;
+  };
+  if (alone) {
+    if (lane < a.S) add(lane);
+  } else {
+#pragma unroll 8
+    for (int s = threadIdx.x; s < a.S; s += kWaves * kWave) add(s);
   }
   all = read_lane_i((int)wave_scan((uint32_t)all), 63);
   some = read_lane_i((int)wave_scan((uint32_t)some), 63);
+  if (!alone) {
+    sums[0][threadIdx.x / kWave] = all;
+    sums[1][threadIdx.x / kWave] = some;
+    __syncthreads();
+    all = some = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      all += sums[0][w];
+      some += sums[1][w];
+    }
+  }
   const float g0 = given0, g1 = all > 0 ? given1 * (2.f / (float)all) : 0.f;
   const float even = (float)a.E / ((float)a.K * (float)some);
   float c[VPL];  // the gradient of the sequence's P
@@ -387,7 +414,8 @@ __global__ __launch_bounds__(kWaves * kWave) void balance_bwd_kernel(BalanceArgs
       there_next = counted(a, t + 1);
     }
     if (q < a.S && end <= t) {
-      while (q < a.S && end <= t) enter(++q);
+      enter(++q);
+      if (end <= t && q < a.S) enter(q = max(q, sequences_before(a, t)));  // that one was empty
       weigh();
     }
     float d[VPL];
@@ -457,9 +485,15 @@ hipError_t launch_balance(BalanceArgs a, hipStream_t s) {
   if (e != hipSuccess) return e;
   // one sequence of few partials is one workgroup's work, losses included
   const bool direct = a.S == 1 && (int64_t)runs * a.E <= kDirect;
-  a.cols = direct ? a.E : kCols;
-  const int columns = direct ? 1 : balance_columns(a.E);
-  balance_finish_kernel<<<dim3(columns, a.S), 1024, 0, s>>>(a);
+  // Sequences of a few partials on average: a wave for 64 experts of each, not 1024 threads
+  // for 32.  (Forward kernels of 16384 tokens, 256 runs, 128 experts: 1024 sequences 34 us and
+  // 81, 64 20.2 and 20.4, 24 20.3 and 19.8, 2 27 and 20; 320 experts: 64 29 and 35, 24 28.6
+  // and 27.7.)
+  const bool few = !direct && 4 * (int64_t)a.S >= runs;
+  a.cols = direct ? a.E : few ? kWave : kCols;
+  const int columns = (a.E + a.cols - 1) / a.cols;
+  if (few) balance_finish_kernel<kWave><<<dim3(columns, a.S), kWave, 0, s>>>(a);
+  else balance_finish_kernel<1024><<<dim3(columns, a.S), 1024, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (columns * a.S == 1) return hipSuccess;
   balance_loss_kernel<<<1, 1024, 0, s>>>(a, columns);
