@@ -85,10 +85,9 @@ __device__ __forceinline__ int sequences_before(const BalanceArgs& a, int t) {
 // 13.8.)
 __device__ __forceinline__ float exp_below(float x) {
   x = x < -200.f ? -200.f : x;  // -inf has no second part
-  const float t = x * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596303e-8
-  const float rest = __builtin_fmaf(x, 1.92596303e-8f, __builtin_fmaf(x, 1.44269502f, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, rest * 0.693147182f, e);
+  float t;
+  const float rest = exp_parts(x, t), e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, rest, e);
 }
 
 // One token's softmax, its lse, its scores (p is soft itself for softmax) and, for

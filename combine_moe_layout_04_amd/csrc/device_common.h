@@ -176,4 +176,11 @@ __device__ __forceinline__ float fold64(float v) {
   return v;
 }
 
+// exp(x) = 2^t (1 + rest) for |x| <= 200: t is the product with log2(e) rounded, and what that
+// leaves of it is small.
+__device__ __forceinline__ float exp_parts(float x, float& t) {
+  t = x * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596303e-8
+  return __builtin_fmaf(x, 1.92596303e-8f, __builtin_fmaf(x, 1.44269502f, -t)) * 0.693147182f;
+}
+
 }  // namespace moe

@@ -96,12 +96,17 @@ struct Tiles {
 };
 
 // f(g) = g sigmoid(x): x = g (silu), or 2 sqrt(2 / pi) (g + 0.044715 g^3), since
-// (1 + tanh(x / 2)) / 2 = sigmoid(x).  The fast exponential is off by (|x| + 2) u of
-// itself (u = 2^-24) and the reciprocal by 2 u, so f by (0.28 + 5) u |g|: s (1 - s) |x|
-// is at most 0.23.
+// (1 + tanh(x / 2)) / 2 = sigmoid(x).  The exponential is off by 4 u of itself (u = 2^-24),
+// the sum by u, the reciprocal by 2 u and the product by u: silu by 8 u of itself however far
+// g lies below 0.  (The exponential's first part alone is off by (|x| + 2) u.  4096 tokens of 8
+// of 128 experts, 2048 x 1536: 154 us, with the first part alone 152, with expf and a division
+// 168.)
 __device__ __forceinline__ float activate(float g, int act) {
   const float x = act == MOE_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return g * __builtin_amdgcn_rcpf(1.f + __expf(-x));
+  float t;
+  const float y = __builtin_amdgcn_fmed3f(-x, -200.f, 200.f);  // past it 0 or infinite, as it is
+  const float rest = exp_parts(y, t);
+  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t) * (1.f + rest));
 }
 
 // Which channel of a tile a row of the B stage holds.  A lane has the four channels

@@ -142,3 +142,17 @@ def test_padding_rows_are_zero_whatever_the_weights_scales(N, size, act):
     bad = [3, N - 1] if act is None else [3, N // 2 - 1]
     keep = [n for n in range(out.shape[1]) if n not in bad]
     assert torch.isnan(out[token >= 0][:, bad]).all() and torch.equal(out[:, keep], plain[:, keep])
+
+
+def test_far_gates_keep_their_digits():
+    """silu(g) of whole g down to -80 to 9 u of itself: the exponential is off by 4 u of itself, the sum by u, the
+    reciprocal by 2 u, the products with g and with up = 1 by u each."""
+    q = torch.zeros(1, 16, dtype=torch.int8, device=DEV)
+    q[0, 0] = 1
+    g = torch.arange(-80, 48, device=DEV)
+    w = torch.zeros(256, 16, dtype=torch.int8, device=DEV)
+    w[:128, 0], w[128:, 0] = g.to(torch.int8), 1
+    one = torch.ones(256, device=DEV)
+    out = M.moe_matmul_i8(q, one[:1], w, one, activation="silu", dtype=F32)[0].double()
+    ref = g.double() / (1 + torch.exp(-g.double()))
+    assert bool(((out - ref).abs() <= 9 * U * ref.abs()).all()), float(((out - ref).abs() / ref.abs().clamp(min=1e-300)).max() / U)
