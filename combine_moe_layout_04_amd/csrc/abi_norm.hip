@@ -22,7 +22,7 @@ int check_norm(int dtype, int64_t T, int64_t H) {
 int check_gates(int64_t T, int64_t gates) {
   if (gates < 0) return MOE_ERR_INVALID_ARG;
   if (gates > 0 && T % gates != 0) return MOE_ERR_SHAPE;
-  return T == 0 && gates > 65533 ? MOE_ERR_UNSUPPORTED : MOE_OK;  // zeros for each: a row of the grid
+  return T == 0 && gates > 65533 ? MOE_ERR_UNSUPPORTED : MOE_OK;  // zeros for each, in a grid of so many
 }
 
 bool bad_eps(float eps) { return !(eps > 0.f) || !isfinite(eps); }

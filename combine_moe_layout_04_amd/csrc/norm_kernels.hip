@@ -17,14 +17,16 @@
 // registers from the first read to the last use, so every row is read and written
 // once (rows of more than 8192 after a block go backward in two kernels).  Sums over
 // a row: each wave's by lane moves, then the waves' in order through LDS.  Sums over
-// tokens: a workgroup's run in registers, one partial for each run, the partials added
-// in the order of the runs by a second kernel, so that results do not depend on
-// timing.
+// tokens: a workgroup's run of at most 256 rows in registers, one partial for each run,
+// the partials added in the order of the runs and in 64 bits by a second kernel, so that
+// results do not depend on timing, nor their errors on the number of tokens.
 //
 // Bound by HBM.  Measured (MI355X, kernels): 8192 rows of 2816 with their combine of 8
 // receive rows: 100 us, 510 MB (a combine alone 70, 415 MB); 4096 x 7168 to 8 bits: 24 us,
 // 3.6 TB/s, what the rounding leaves of the bandwidth; 4096 x 2048 after a block: 16.5 us
 // forward (67 MB), 28 + 4 backward (101 MB and 13 MB of partials).
+#include <algorithm>
+
 #include "device_common.h"
 #include "internal.h"
 #include "quant.h"
@@ -536,7 +538,8 @@ __global__ __launch_bounds__(1024) void norm_means_kernel(NormBwdArgs a) {
 template <int DT>
 __global__ __launch_bounds__(256) void norm_columns_kernel(NormBwdArgs a) {
   constexpr int V = Elems<DT>::kPerChunk;
-  const int run = blockIdx.y, H = a.nch * V, j = blockIdx.x * blockDim.x + threadIdx.x;
+  const int columns = (a.nch + blockDim.x - 1) / blockDim.x;  // workgroups of a run
+  const int run = blockIdx.x / columns, H = a.nch * V, j = blockIdx.x % columns * blockDim.x + threadIdx.x;
   if (j >= a.nch) return;
   int t0, t1;
   tokens_of_run(a, run, t0, t1);
@@ -609,55 +612,56 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormBwdArgs a) {
   if (a.gg && a.parts > 1) partial(a.partg, sg);
 }
 
-// Adds partials: blockIdx.y 0 the next norm's weight, 1 the post-norm's, 2.. the gates.
-// 64 columns a workgroup, four a thread; a sixteenth of the partials each.
+// Adds partials: blockIdx.y 0 the next norm's weight, 1 the post-norm's, from 2 on the gates
+// (a grid's second dimension may hold fewer).  64 columns a workgroup, four a thread; a
+// sixteenth of the partials each.
+constexpr int kGateRows = 32768;  // of the grid
+
 template <int DT>
 __global__ __launch_bounds__(256) void norm_join_kernel(NormBwdArgs a) {
-  __shared__ float4 sum[16][16];
+  __shared__ double sum[16][64], four[4][64];
   const int H = a.nch * Elems<DT>::kPerChunk;
-  const int q = threadIdx.x % 16, k = threadIdx.x / 16, col = blockIdx.x * 64 + 4 * q;
-  const float* from;
-  void* to;
-  int n = a.runs;
-  size_t row = 0;
-  if (blockIdx.y == 0) {
-    from = a.part2;
-    to = a.gw2;
-  } else if (blockIdx.y == 1) {
-    from = a.part1;
-    to = a.gw1;
-  } else {
-    row = blockIdx.y - 2;
-    from = a.partg + row * a.parts * H;
-    to = a.gg;
-    n = a.parts;
-  }
+  const int tid = threadIdx.x, q = tid % 16, k = tid / 16, col = blockIdx.x * 64 + 4 * q;
+  const bool gates = blockIdx.y >= 2;
+  void* to = gates ? a.gg : blockIdx.y == 1 ? a.gw1 : a.gw2;
   if (!to) return;  // uniform
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < H) {
-#pragma unroll 8
-    for (int i = k; i < n; i += 16) {
-      const float4 v = *reinterpret_cast<const float4*>(from + (size_t)i * H + col);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+  const int n = gates ? a.parts : a.runs;
+  for (int64_t row = gates ? blockIdx.y - 2 : 0; row < (gates ? a.gates : 1); row += kGateRows) {
+    const float* from = gates ? a.partg + row * n * H : blockIdx.y == 1 ? a.part1 : a.part2;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    if (col < H)
+      for (int i0 = k; i0 < n; i0 += 16 * 8) {
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const float4*>(from + (size_t)min(i0 + 16 * u, n - 1) * H + col);
+        __builtin_amdgcn_sched_barrier(0);  // all on their way before the first is added
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const bool there = i0 + 16 * u < n;
+          s[0] += there ? v[u].x : 0.f;
+          s[1] += there ? v[u].y : 0.f;
+          s[2] += there ? v[u].z : 0.f;
+          s[3] += there ? v[u].w : 0.f;
+        }
+      }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sum[k][4 * q + v] = s[v];
+    __syncthreads();
+    const int c = tid % 64, g = tid / 64 * 4;
+    four[tid / 64][c] = ((sum[g][c] + sum[g + 1][c]) + sum[g + 2][c]) + sum[g + 3][c];
+    __syncthreads();
+    if (k == 0 && col < H) {
+      float f[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        f[v] = (float)(((four[0][4 * q + v] + four[1][4 * q + v]) + four[2][4 * q + v]) + four[3][4 * q + v]);
+      if constexpr (DT == kF32)
+        *reinterpret_cast<float4*>(static_cast<float*>(to) + row * H + col) = make_float4(f[0], f[1], f[2], f[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(to) + row * H + col) =
+            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
     }
   }
-  sum[k][q] = s;
-  __syncthreads();
-  if (k != 0 || col >= H) return;
-  for (int i = 1; i < 16; ++i) {
-    const float4 v = sum[i][q];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
-  }
-  if constexpr (DT == kF32)
-    *reinterpret_cast<float4*>(static_cast<float*>(to) + row * H + col) = s;
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(to) + row * H + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
 int threads(int nch, int cpl) { return ((nch + cpl - 1) / cpl + kWave - 1) / kWave * kWave; }
@@ -681,7 +685,7 @@ hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
     // 8192: 167 against 122; float32, 8196: 327, 8192: 295 against 254)
     if (BLOCK && a.nch * Elems<DT>::kPerChunk > kNormWide) {
       if (a.means) norm_means_kernel<DT><<<row_grid(a.T), a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
-      norm_columns_kernel<DT><<<dim3((a.nch + 255) / 256, a.runs), 256, 0, s>>>(a);
+      norm_columns_kernel<DT><<<(a.nch + 255) / 256 * a.runs, 256, 0, s>>>(a);
     } else if (a.nch <= 512) norm_bwd_kernel<DT, 1, BLOCK, true, 512><<<a.runs, threads(a.nch, 1), 0, s>>>(a);
     else if (a.nch <= 1024) norm_bwd_kernel<DT, 2, BLOCK, false, 512><<<a.runs, threads(a.nch, 2), 0, s>>>(a);
     else if constexpr (!BLOCK || DT == kF32) {
@@ -694,7 +698,8 @@ hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
   const bool gates = a.gg && a.parts != 1;  // no part (an empty batch): zeros
   if (!a.gw1 && !a.gw2 && !gates) return hipSuccess;
   const int H = a.nch * Elems<DT>::kPerChunk;
-  norm_join_kernel<DT><<<dim3((H + 63) / 64, gates ? 2 + a.gates : 2), 256, 0, s>>>(a);
+  const int rows = !gates ? 0 : a.gates < kGateRows ? a.gates : kGateRows;
+  norm_join_kernel<DT><<<dim3((H + 63) / 64, 2 + rows), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -729,14 +734,17 @@ hipError_t launch_quant(const NormArgs& a, hipStream_t s) {
 // bfloat16, four waves a row: 34 us with 512 runs, 44 with 256, 36 with 1024; 7168, eight
 // waves: 110 with 256, 116 with 512).  Wide rows in two kernels have a wave for every 64
 // chunks of a run: 128 runs (4096 x 8200: 183 us, 226 with 64, 195 with 512; 2048 x 16384:
-// 175, 163, 189).
+// 175, 163, 189).  A run has at most 256 rows, more runs instead of longer ones past that,
+// because its sums are in 32 bits (2^21 rows of 4 float32 alike in 1024 runs were off by
+// 518 u of themselves, u = 2^-24; 2^18 x 2048 after a block: 1450 us so, 1310 with 512 runs,
+// 2^19 x 2048 2660 both, 2^20 x 256 1080 and 1650).
 void norm_bwd_plan(int64_t T, int64_t group, int nch, bool wide, int* rows, int* parts, int* runs) {
   if (T == 0) {
     *rows = *parts = *runs = 0;
     return;
   }
   const int waves = (nch + kWave - 1) / kWave, most = wide ? 128 : waves <= 2 ? 1024 : waves <= 4 ? 512 : 256;
-  int64_t r = (T + most - 1) / most;
+  int64_t r = std::min<int64_t>((T + most - 1) / most, 256);
   if (group >= r) {
     *parts = (int)((group + r - 1) / r);
     if (*parts == 1) r = group;
