@@ -17,6 +17,6 @@ hipError_t launch_i8(const I8Args& a, hipStream_t s) {
   return launch_i8_small(a, s);
 }
 
-hipError_t launch_i8_large(const I8Args& a, hipStream_t s) { return launch_tile<4, 4, 2, 4, 8, 2>(a, s); }
+hipError_t launch_i8_large(const I8Args& a, hipStream_t s) { return launch_tile<4, 4, 2, 4, 2>(a, s); }
 
 }  // namespace moe

@@ -3,6 +3,6 @@
 
 namespace moe {
 
-hipError_t launch_i8_middle(const I8Args& a, hipStream_t s) { return launch_tile<2, 4, 2, 2, 8, 2>(a, s); }
+hipError_t launch_i8_middle(const I8Args& a, hipStream_t s) { return launch_tile<2, 4, 2, 2, 2>(a, s); }
 
 }  // namespace moe

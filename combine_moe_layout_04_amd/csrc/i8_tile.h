@@ -36,8 +36,8 @@
 // 2.3 POP/s, half of what the matrix cores could do (a library's product of two 8192 x 8192
 // int8 matrices reaches 2.4); the loads alone take 77 us, the products alone 57.  4096 tokens
 // of 8 of 128 experts, 2048 x 1536, gated: 156 us; loads alone 128 (520 to 570 MB are read,
-// 403 of them weights), products alone 70.  64 tokens there: 73 us, 5.5 TB/s of weights,
-// which is what memory gives.
+// 403 of them weights), products alone 70.  64 tokens there: 73 to 76 us, 5.2 to 5.5 TB/s
+// of weights; a plain read of as much reaches 6.15.
 #pragma once
 
 #include "device_common.h"
@@ -59,8 +59,10 @@ constexpr int wait_for(int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); }
 constexpr int kMaxExperts = 1024;           // MOE_MAX_E
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer
 
+constexpr int kStep = 8;  // 16-byte chunks of a row in a step
+
 // Steps of a tile: two are asked for ahead.
-__host__ __device__ constexpr int steps_of(int kch, int kc) { return kch > kc ? (kch + kc - 1) / kc : 2; }
+__host__ __device__ constexpr int steps_of(int kch) { return kch > kStep ? (kch + kStep - 1) / kStep : 2; }
 
 struct Tile {
   int e, row, rows, col;  // expert, first receive row, rows (0: no such tile), channel tile
@@ -134,14 +136,14 @@ struct Channels {
 };
 
 // MB x NB tiles of 16 x 16 a wave, WM x WN waves.  REST: steps of a tile, modulo 3.
-template <int DT, bool GATED, int MB, int NB, int WM, int WN, int KC, int REST, int EU>
+template <int DT, bool GATED, int MB, int NB, int WM, int WN, int REST, int EU>
 __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int cols) {
   constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN, kWaves = WM * WN;
-  constexpr int kRowsPer = kWave / KC;  // rows of one load instruction
+  constexpr int kRowsPer = kWave / kStep;  // rows of one load instruction
   constexpr int kLoadsA = (BM + kRowsPer * kWaves - 1) / (kRowsPer * kWaves), kLoadsB = BN / kRowsPer / kWaves;
   static_assert(kRowsPer * kWaves % 16 == 0);
   static_assert(kLoadsB >= 1 && BN % (kRowsPer * kWaves) == 0);
-  constexpr int kStageA = kLoadsA * kWaves * kWave, kStageB = BN * KC;
+  constexpr int kStageA = kLoadsA * kWaves * kWave, kStageB = BN * kStep;
   __shared__ u32x4 a0[kStageA], b0[kStageB], a1[kStageA], b1[kStageB], a2[kStageA], b2[kStageB];
   auto stage_a = [&](auto I) __attribute__((always_inline)) -> u32x4* {
     if constexpr (I == 0) return a0;
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave % WM, wn = wave / WM;
   // the bits of a row that its chunks are permuted by: 16 rows over all banks
-  auto key = [](int row) { return KC >= 16 ? row & 15 : KC == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  auto key = [](int row) { return (row >> 1) & 7; };
   const int N = GATED ? a.N / 2 : a.N;  // channels of the output
   const int64_t width = (int64_t)a.kch * 16;
 
@@ -209,9 +211,9 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
     return i < end ? list.at(i) : none;
   };
 
-  const int mine = wave * kRowsPer + lane / KC;  // this lane's row of a wave's first load
-  const int chunk = lane % KC ^ key(mine);       // the same in all of them
-  const int full = (a.kch + KC - 1) / KC, steps = steps_of(a.kch, KC);  // the second may have one without a load
+  const int mine = wave * kRowsPer + lane / kStep;  // this lane's row of a wave's first load
+  const int chunk = lane % kStep ^ key(mine);       // the same in all of them
+  const int full = (a.kch + kStep - 1) / kStep, steps = steps_of(a.kch);  // the second may have one without a load
   Tile t = tile_at(id);
   if (t.rows == 0) return;  // uniform over the workgroup
 
@@ -261,9 +263,9 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
   auto load = [&](auto STAGE, int s, auto n) __attribute__((always_inline)) {
     int step = s + begin;
     if (step >= full) step -= full;
-    const int left = s < full ? a.kch - step * KC : 0;  // chunks of the row from there on (a select, no branch)
+    const int left = s < full ? a.kch - step * kStep : 0;  // chunks of the row from there on (a select, no branch)
     const bool in = chunk < left;
-    const int at = step * KC * 16;
+    const int at = step * kStep * 16;
     if constexpr (n < kLoadsA) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rq, (__attribute__((address_space(3))) void*)(stage_a(STAGE) + (n * kWaves + wave) * kWave), 16,
@@ -311,15 +313,15 @@ __global__ __launch_bounds__(WM* WN* kWave, EU) void i8_kernel(I8Args a, int col
       constexpr std::integral_constant<int, (I + 2) % 3> before_it;
       const u32x4 *la = stage_a(I), *lb = stage_b(I);
       const int r = lane & 15, c = lane >> 4;
-      constexpr int kParts = KC / 4;
+      constexpr int kParts = kStep / 4;
       i32x4 fa[kParts][B], fb[kParts][NB];
 #pragma unroll
       for (int k = 0; k < kParts; ++k) {
         const int slot = (4 * k + c) ^ key(r);  // 16 more rows have the same key
 #pragma unroll
-        for (int j = 0; j < NB; ++j) fb[k][j] = __builtin_bit_cast(i32x4, lb[((wn * NB + j) * 16 + r) * KC + slot]);
+        for (int j = 0; j < NB; ++j) fb[k][j] = __builtin_bit_cast(i32x4, lb[((wn * NB + j) * 16 + r) * kStep + slot]);
 #pragma unroll
-        for (int i = 0; i < B; ++i) fa[k][i] = __builtin_bit_cast(i32x4, la[((i * WM + wm) * 16 + r) * KC + slot]);
+        for (int i = 0; i < B; ++i) fa[k][i] = __builtin_bit_cast(i32x4, la[((i * WM + wm) * 16 + r) * kStep + slot]);
       }
       if constexpr (first) in_order();  // else the compiler waits for more than it has to
       // a load takes the address unit as long as a product the matrix unit: one by one between them
@@ -511,7 +513,7 @@ int64_t most_tiles(const I8Args& a, int bm, int bn) {
   return (rows / bm + partial) * ((a.N + bn - 1) / bn);
 }
 
-template <int MB, int NB, int WM, int WN, int KC, int REST, int EU>
+template <int MB, int NB, int WM, int WN, int REST, int EU>
 hipError_t launch_steps(const I8Args& a, hipStream_t s) {
   constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN;
   const bool gated = a.act != MOE_ACT_NONE;
@@ -520,21 +522,21 @@ hipError_t launch_steps(const I8Args& a, hipStream_t s) {
   const unsigned grid = (unsigned)(most < fit ? most : fit);
   const uint32_t lds = 2 * (a.E + 1) * sizeof(int);
   if (a.dtype == kF32) {
-    if (gated) i8_kernel<kF32, true, MB, NB, WM, WN, KC, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
-    else i8_kernel<kF32, false, MB, NB, WM, WN, KC, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    if (gated) i8_kernel<kF32, true, MB, NB, WM, WN, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    else i8_kernel<kF32, false, MB, NB, WM, WN, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
   } else {
-    if (gated) i8_kernel<kBF16, true, MB, NB, WM, WN, KC, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
-    else i8_kernel<kBF16, false, MB, NB, WM, WN, KC, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    if (gated) i8_kernel<kBF16, true, MB, NB, WM, WN, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
+    else i8_kernel<kBF16, false, MB, NB, WM, WN, REST, EU><<<grid, WM * WN * kWave, lds, s>>>(a, cols);
   }
   return hipGetLastError();
 }
 
-template <int MB, int NB, int WM, int WN, int KC, int EU>
+template <int MB, int NB, int WM, int WN, int EU>
 hipError_t launch_tile(const I8Args& a, hipStream_t s) {
-  switch (steps_of(a.kch, KC) % 3) {
-    case 0: return launch_steps<MB, NB, WM, WN, KC, 0, EU>(a, s);
-    case 1: return launch_steps<MB, NB, WM, WN, KC, 1, EU>(a, s);
-    default: return launch_steps<MB, NB, WM, WN, KC, 2, EU>(a, s);
+  switch (steps_of(a.kch) % 3) {
+    case 0: return launch_steps<MB, NB, WM, WN, 0, EU>(a, s);
+    case 1: return launch_steps<MB, NB, WM, WN, 1, EU>(a, s);
+    default: return launch_steps<MB, NB, WM, WN, 2, EU>(a, s);
   }
 }
 
