@@ -27,9 +27,10 @@
 // zero (every logit -inf) has s = 0, no part in the z loss and no gradient.
 //
 // Bound by latency and instruction issue, not by its bytes.  Measured (MI355X, kernels):
-// 4096 tokens of 128 experts 5.4 + 5.9 us forward, 5.4 backward (1.1 MB read by each);
-// 16384 tokens of 256 experts in 24 sequences, float32: 12.6 + 5.1 + 4.5 forward (17 MB read),
-// 14.4 backward (34 MB).
+// 4096 tokens of 128 experts 5.8 + 6.0 us forward, 5.3 backward (1.1 MB read by each);
+// 16384 tokens of 256 experts in 24 sequences, sigmoid, float32: 14.2 + 5.1 + 4.5 forward
+// (17 MB read), 16.2 backward (34 MB).  A run works through the sequences that it meets one by
+// one, about 2 us each: 65535 tokens, each a sequence, 548 + 64 + 47 and 51.
 #include "device_common.h"
 #include "internal.h"
 #include "../../include/moe_layout.h"

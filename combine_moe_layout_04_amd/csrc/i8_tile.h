@@ -35,7 +35,7 @@
 // Measured (MI355X): one projection of 4096 rows, 7168 x 4096, gated: 102 to 113 us, 2.1 to
 // 2.3 POP/s, half of what the matrix cores could do (a library's product of two 8192 x 8192
 // int8 matrices reaches 2.4); the loads alone take 77 us, the products alone 57.  4096 tokens
-// of 8 of 128 experts, 2048 x 1536, gated: 156 us; loads alone 128 (520 to 570 MB are read,
+// of 8 of 128 experts, 2048 x 1536, gated: 154 to 162 us; loads alone 128 (520 to 570 MB are read,
 // 403 of them weights), products alone 70.  64 tokens there: 73 to 76 us, 5.2 to 5.5 TB/s
 // of weights; a plain read of as much reaches 6.15.
 #pragma once

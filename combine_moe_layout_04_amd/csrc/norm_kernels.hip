@@ -24,7 +24,7 @@
 // Bound by HBM.  Measured (MI355X, kernels): 8192 rows of 2816 with their combine of 8
 // receive rows: 100 us, 510 MB (a combine alone 70, 415 MB); 4096 x 7168 to 8 bits: 24 us,
 // 3.6 TB/s, what the rounding leaves of the bandwidth; 4096 x 2048 after a block: 16.5 us
-// forward (67 MB), 28 + 4 backward (101 MB and 13 MB of partials).
+// forward (67 MB), 29 + 5 backward (101 MB and 13 MB of partials).
 #include <algorithm>
 
 #include "device_common.h"
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(MOST) void norm_bwd_kernel(NormBwdArgs a) {
 // Wide rows after a block, in two kernels: the two means of every row first, then, with
 // those known, a wave for 64 chunks of the columns of a run, which needs no other wave.
 // The rows are read twice, but nothing stays in registers but a chunk and its sums (2048
-// rows of 16384 bfloat16: 175 us, 65 are what the bytes of one reading take).
+// rows of 16384 bfloat16: 79 + 85 us, 65 are what the bytes of one reading take).
 template <int DT>
 __global__ __launch_bounds__(1024) void norm_means_kernel(NormBwdArgs a) {
   constexpr int V = Elems<DT>::kPerChunk;
@@ -681,7 +681,7 @@ template <int DT, bool BLOCK>
 hipError_t launch_norm_bwd_typed(const NormBwdArgs& a, hipStream_t s) {
   if (a.runs > 0) {
     // a run's sums of two chunks of eight numbers a lane do not fit beside a row: rows of
-    // more than 8192 after a block in two kernels (4096 x 8200 bfloat16: 183 us, in one 817;
+    // more than 8192 after a block in two kernels (4096 x 8200 bfloat16: 178 us, in one 817;
     // 8192: 167 against 122; float32, 8196: 327, 8192: 295 against 254)
     if (BLOCK && a.nch * Elems<DT>::kPerChunk > kNormWide) {
       if (a.means) norm_means_kernel<DT><<<row_grid(a.T), a.nch >= 1024 ? 1024 : 512, 0, s>>>(a);
@@ -733,11 +733,11 @@ hipError_t launch_quant(const NormArgs& a, hipStream_t s) {
 // Rows of a run, runs that share a gate, and runs in all: about 2048 waves (4096 x 2048
 // bfloat16, four waves a row: 34 us with 512 runs, 44 with 256, 36 with 1024; 7168, eight
 // waves: 110 with 256, 116 with 512).  Wide rows in two kernels have a wave for every 64
-// chunks of a run: 128 runs (4096 x 8200: 183 us, 226 with 64, 195 with 512; 2048 x 16384:
-// 175, 163, 189).  A run has at most 256 rows, more runs instead of longer ones past that,
-// because its sums are in 32 bits (2^21 rows of 4 float32 alike in 1024 runs were off by
-// 518 u of themselves, u = 2^-24; 2^18 x 2048 after a block: 1450 us so, 1310 with 512 runs,
-// 2^19 x 2048 2660 both, 2^20 x 256 1080 and 1650).
+// chunks of a run: 128 runs (4096 x 8200: 178 us, 219 with 64, 183 with 512; 2048 x 16384:
+// 168, 156, 170; 4096 x 12288: 227, 255, 246).  A run has at most 256 rows, more runs instead
+// of longer ones past that, because its sums are in 32 bits (2^21 rows of 4 float32 alike in
+// 1024 runs were off by 518 u of themselves, u = 2^-24; 2^18 x 2048 after a block: 1450 us so,
+// 1310 with 512 runs, 2^19 x 2048 2660 both, 2^20 x 256 1080 and 1650).
 void norm_bwd_plan(int64_t T, int64_t group, int nch, bool wide, int* rows, int* parts, int* runs) {
   if (T == 0) {
     *rows = *parts = *runs = 0;
