@@ -100,9 +100,9 @@ struct Tiles {
 // f(g) = g sigmoid(x): x = g (silu), or 2 sqrt(2 / pi) (g + 0.044715 g^3), since
 // (1 + tanh(x / 2)) / 2 = sigmoid(x).  The exponential is off by 4 u of itself (u = 2^-24),
 // the sum by u, the reciprocal by 2 u and the product by u: silu by 8 u of itself down to g =
-// -87, below which it is under 2^-118 and may be 0.  (The exponential's first part alone is off by (|x| + 2) u.  4096 tokens of 8
-// of 128 experts, 2048 x 1536: 154 us, with the first part alone 152, with expf and a division
-// 168.)
+// -87, below which it is under 2^-118 and may be 0.  (The exponential's first part alone is
+// off by (|x| + 2) u.  4096 tokens of 8 of 128 experts, 2048 x 1536: 154 us, with the first
+// part alone 152, with expf and a division 168.)
 __device__ __forceinline__ float activate(float g, int act) {
   const float x = act == MOE_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
   float t;
